@@ -20,6 +20,10 @@ Entry points (same names as the C ABI):
     shrink_expand_mask(x, A, B, y, idx, out_offsets, workspace=...)
                                          the mask ("laning") form for S * r_max <= 128
     alloc_workspace(T, S, n_slices, r_max, device) -> zeroed workspace for it
+
+and, from .attention (include/lora_attention.h), what follows the q/k/v
+projection: rope_table, rotary, qk_norm_rotary, build_tree, tree_attention,
+keep_path.
 """
 
 import ctypes
@@ -567,3 +571,9 @@ def pack_b_rank_rows(B, ranks_host, *, stream=None):
         dst = packed[s_].view(-1)[:out * ld].view(out, ld)
         copy_padded(B[s_][:, :r] if r else B[s_][:, :0], dst, stream=stream)
     return packed
+
+
+# after the helpers above, which it uses
+from .attention import (  # noqa: E402
+    alloc_attention_workspace, attention_workspace_bytes, build_tree, keep_path, qk_norm_rotary, rope_frequencies,
+    rope_table, rotary, tree_attention)

@@ -7,12 +7,14 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblora_mi355x.so")
-SOURCES = ["api.hip", "segments.hip", "shrink.hip", "bgmv.hip", "sgmv.hip", "fused.hip", "embedding.hip", "slots.hip", "mask.hip"]
+SOURCES = ["api.hip", "segments.hip", "shrink.hip", "bgmv.hip", "sgmv.hip", "fused.hip", "embedding.hip", "slots.hip", "mask.hip",
+           "attention_api.hip", "rotary.hip", "tree.hip", "attend.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -37,11 +39,11 @@ def hipcc():
 
 def build(verbose=False):
     """Compile every HIP source and link the shared library.  Always rebuilds."""
-    objs = []
     obj_dir = os.path.join(PKG, "_build")
     os.makedirs(obj_dir, exist_ok=True)
     cc = hipcc()
-    for src in SOURCES:
+
+    def compile_one(src):
         obj = os.path.join(obj_dir, src.replace(".hip", ".o"))
         cmd = [cc, *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-c",
                os.path.join(CSRC, src), "-o", obj]
@@ -53,7 +55,10 @@ def build(verbose=False):
             raise RuntimeError(f"hipcc failed on {src}:\n{err}")
         if err.strip() and verbose:
             print(err, file=sys.stderr)
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(max_workers=min(4, os.cpu_count() or 1)) as pool:
+        objs = list(pool.map(compile_one, SOURCES))
     tmp = LIB + ".tmp"
     cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)

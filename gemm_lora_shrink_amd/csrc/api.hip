@@ -24,6 +24,8 @@ namespace {
 
 thread_local char g_err[512];
 
+}  // namespace
+
 lora_status fail(lora_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -38,11 +40,7 @@ lora_status hip_fail(hipError_t e, const char* what) {
 
 void clear_error() { g_err[0] = 0; }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int vec_of(lora_dtype dt) { return dt == LORA_F32 ? 4 : 8; }
-
-bool valid_dtype(int dt) { return dt == LORA_F32 || dt == LORA_F16 || dt == LORA_BF16; }
+namespace {
 
 // Kernel used for the expand of gather (decode) groups of 16-bit data.  The
 // matrix-core kernel is the default; LORA_MI355X_GATHER_EXPAND=valu selects the

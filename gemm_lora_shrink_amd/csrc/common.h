@@ -330,6 +330,16 @@ __device__ inline int slot_rank(const int32_t* ranks, int s, int r_max) {
   return r < 0 ? 0 : (r > r_max ? r_max : r);
 }
 
+// The calling thread's error state, behind lora_last_error() (api.hip).
+__attribute__((format(printf, 2, 3))) lora_status fail(lora_status st, const char* fmt, ...);
+lora_status hip_fail(hipError_t e, const char* what);
+void clear_error();
+
+// What every entry point's argument checks share.
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline int vec_of(lora_dtype dt) { return dt == LORA_F32 ? 4 : 8; }
+inline bool valid_dtype(int dt) { return dt == LORA_F32 || dt == LORA_F16 || dt == LORA_BF16; }
+
 // Workgroups of `kernel` the current device holds at once (occupancy x
 // compute units), computed once per device and kernel.
 int resident_workgroups(const void* kernel, int block, size_t dyn_lds);
