@@ -1,80 +1,855 @@
-// Attention of a step's drafted tokens over the paged cache.
+// Attention of a step's tokens over the paged cache.
 //
-// One wave a (token, query head): the lanes hold the query, take the keys one
-// after another and keep the running maximum and sum of the softmax.
+// For one sequence and one key/value head the rows are its nodes times the
+// query heads of the group; all of them read the same keys, so a workgroup
+// takes up to 128 rows of one (sequence, key/value head) over one chunk of the
+// keys, and a second launch joins the chunks where there are several.  With m
+// the running maximum and l the running sum of a row, a tile of scores s
+// changes them by
+//     m' = max(m, max s),  l' = l e^(m - m') + sum e^(s - m'),
+//     o' = o e^(m - m') + sum e^(s - m') v,
+// all in fp32 and in powers of two (scores are multiplied by scale * log2 e).
+//
+// Products run on the matrix cores as 32 x 32 blocks, transposed: S^T = K Q^T
+// leaves a lane with 16 scores of ONE row (row = lane % 32; lanes l and l + 32
+// share it), so maximum, sum and rescaling are per-lane scalars and one half
+// swap, and the scores are already the operand of O^T = V^T P^T: the contraction
+// index may run over the keys in any order as long as both operands agree, and
+// taking it in the order in which S^T lies in registers needs no exchange.
+// V^T comes from row-major V in LDS by transposing reads (16-bit) or single
+// element reads (fp32).
+//
+// K and V rows go from global memory to LDS by direct loads, whole rows of
+// contiguous bytes; the 16-byte pieces of a row lie XOR-swizzled by row so that
+// reading 16 rows at one piece, and 4 rows at 64 contiguous bytes, are both
+// free of bank conflicts.  A row that is no key (past the end, no page) is
+// loaded from a row of zeros.
 #include "attention.h"
 
 namespace lora {
 
 namespace {
 
-template <typename Elem>
-__global__ __launch_bounds__(64) void attend_kernel(AttendParams p) {
-  warm_args(p);
-  const int b = blockIdx.z, h = blockIdx.y, i = blockIdx.x, lane = threadIdx.x;
-  const int start = p.q_start[b];
-  int n = p.q_start[b + 1] - start;
-  if (start < 0 || start > p.T) return;
-  n = n > p.max_nodes ? p.max_nodes : n;
-  n = n > p.T - start ? p.T - start : n;
-  if (i >= n) return;
-  int ctx = p.context[b];
-  ctx = ctx < 0 ? 0 : (ctx > p.max_context ? p.max_context : ctx);
-  const int64_t row = start + i;
-  const int kv = p.group.div(h);
-  const Elem* q = static_cast<const Elem*>(p.q) + row * p.ldq + (int64_t)h * p.d;
-  float qf[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kThreads = 256;
+constexpr int kBlock = 32;  // rows and keys of a matrix block
+constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.44269504088896340736f;
+
+__device__ const u32x4 g_zero_row[64] = {};  // 1 KB of zeros: the longest row
+
+template <typename Elem> struct Mma32;
+template <> struct Mma32<bf16_t> {
+  __device__ static inline f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+  __device__ static inline uint32_t pack2(float a, float b) { return pack2_bf16(a, b); }
+  static constexpr uint32_t kExp = 0x7f80u;  // all ones: no finite number
+  static constexpr uint32_t kOne = 0x3f80u;
+};
+template <> struct Mma32<half_t> {
+  __device__ static inline f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+  }
+  __device__ static inline uint32_t pack2(float a, float b) { return pack2_f16(a, b); }
+  static constexpr uint32_t kExp = 0x7c00u;
+  static constexpr uint32_t kOne = 0x3c00u;
+};
+template <> struct Mma32<float> {
+  __device__ static inline f32x16 mma1(float a, float b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+  }
+  // element e of every lane's four is one product of 32 x 32 x 2
+  __device__ static inline f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) qf[e] = lane + 64 * e < p.d ? (float)q[lane + 64 * e] : 0.f;
-  for (int64_t pos = 0; pos < (int64_t)ctx + n; ++pos) {
-    const int64_t j = pos - ctx;
-    if (j >= 0) {
-      if (!p.mask) {
-        if (j > i) break;
-      } else if (!(p.mask[row * p.mask_words + (j >> 6)] >> (j & 63) & 1)) {
-        continue;
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t ae = a[e], be = b[e];
+      c = mma1(__uint_as_float(ae), __uint_as_float(be), c);
+    }
+    return c;
+  }
+  static constexpr uint32_t kExp = 0x7f800000u;
+};
+
+// Rows of DP elements (the head, padded) in LDS.
+template <typename Elem, int DP> struct Rows {
+  static constexpr bool k16 = sizeof(Elem) == 2;
+  static constexpr int kBytes = DP * (int)sizeof(Elem);  // of a row
+  static constexpr int kPieces = kBytes / 16;
+  static constexpr int kSteps = kBytes / 32;       // 16-byte operands of a lane and half
+  static constexpr int kDB = DP / kBlock;          // blocks of the output
+  static constexpr int kPerLoad = 1024 / kBytes;   // rows of one 64-lane load
+  static_assert(kBytes >= 128 && kBytes <= 1024, "");
+  // position of piece c of row r: c ^ swz(r)
+  __device__ static inline int swz(int r) {
+    if (kBytes == 128) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    if (k16) return ((r & 3) << 2) | ((r >> 2) & 3);
+    return (((r >> 2) & 1) << 3) | ((r & 3) << 1) | ((r >> 3) & 1);
+  }
+};
+
+// Global-to-LDS loads with 64-bit addresses: lane l's 16 (or 4) bytes land at
+// LDS byte lds + 16 l (4 l).  Issued by hand for the reason given at the
+// shrink's: the compiler would wait for every load in flight before each LDS
+// read.  lds is wave-uniform.
+__device__ inline void row_to_lds(const char* g, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %2, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(g)
+      : "memory");
+}
+__device__ inline void word_to_lds(const char* g, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %2, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(g)
+      : "memory");
+}
+template <int n> __device__ inline void wait_loads() {
+  static_assert(n <= 63, "the wait counter's range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
+}
+__device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// The two lanes of a row.
+__device__ inline float half_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ inline float half_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// What a workgroup works on.
+struct Work {
+  int64_t start;       // first row of the sequence
+  int b, h, n, ctx;    // sequence, key/value head, nodes, context
+  int row0, rows;      // this workgroup's first row (node * group + head) and the sequence's rows
+  int k0, k1, split;   // keys [k0, k1)
+  bool none;           // nothing to do
+};
+
+__device__ inline void sequence_of(const AttendParams& p, int b, int64_t& start, int& n, int& ctx) {
+  start = p.q_start[b];
+  int64_t c = (int64_t)p.q_start[b + 1] - start;
+  if (start < 0 || start > p.T) {
+    start = 0;
+    c = 0;
+  }
+  if (c > p.T - start) c = p.T - start;
+  n = (int)(c < 0 ? 0 : (c > p.max_nodes ? p.max_nodes : c));
+  const int x = p.context[b];
+  ctx = x < 0 ? 0 : (x > p.max_context ? p.max_context : x);
+}
+__device__ inline int splits_of(const AttendParams& p, int n, int ctx) {
+  const int s = (int)(((uint32_t)ctx + (uint32_t)n + (uint32_t)p.chunk - 1u) / (uint32_t)p.chunk);
+  return s < 1 ? 1 : s;
+}
+
+// Units of work lie in the order sequence, head, chunk, row tile; the workgroups
+// of one XCD (b % 8) take a contiguous range, so the row tiles of a chunk read
+// its keys through one L2.
+template <int ROWS>
+__device__ inline Work work_of(const AttendParams& p) {
+  Work w;
+  const int per = (int)(gridDim.x / kXcds);
+  int u = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
+  const int rt = u % p.row_tiles;
+  u /= p.row_tiles;
+  w.split = u % p.splits;
+  u /= p.splits;
+  w.h = u % p.hk;
+  w.b = u / p.hk;
+  w.none = w.b >= p.B;
+  if (w.none) return w;
+  sequence_of(p, w.b, w.start, w.n, w.ctx);
+  const int group = (int)p.group.d;
+  w.row0 = rt * ROWS;
+  w.rows = w.n * group;
+  w.none = w.row0 >= w.rows || w.split >= splits_of(p, w.n, w.ctx);
+  const int last = min(w.row0 + ROWS, w.rows) - 1;
+  const int end = w.ctx + (p.mask ? w.n : min(w.n, (int)p.group.div((uint32_t)max(last, 0)) + 1));
+  const int64_t k0 = (int64_t)w.split * p.chunk;
+  w.k0 = (int)k0;
+  w.k1 = (int)min(k0 + p.chunk, (int64_t)end);
+  return w;
+}
+
+// One row block of 32 rows: the query operand, the running softmax and the
+// output, held by one wave.
+template <typename Elem, int DP> struct RowBlock {
+  using R = Rows<Elem, DP>;
+  u32x4 q[R::kSteps];
+  f32x16 o[R::kDB];
+  float m, l;
+  int lane, r32, hi;   // row in the block, half
+  int node;            // of this lane's row
+  int64_t row;         // of q and out, -1: none
+  int head;
+  uint64_t bits0;      // first word of the mask row
+
+  __device__ inline void init(const AttendParams& p, const Work& w, int row_first) {
+    lane = threadIdx.x & 63;
+    r32 = lane & 31;
+    hi = lane >> 5;
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int db = 0; db < R::kDB; ++db)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
+    const int r = row_first + r32;
+    const bool ok = r < w.rows;
+    node = (int)p.group.div((uint32_t)(ok ? r : 0));
+    head = w.h * (int)p.group.d + (ok ? r - node * (int)p.group.d : 0);
+    row = ok ? w.start + node : -1;
+    const Elem* qr = static_cast<const Elem*>(p.q) + (ok ? row : 0) * p.ldq + (int64_t)head * p.d;
+    constexpr int kVec = Traits<Elem>::kVec;
+#pragma unroll
+    for (int s = 0; s < R::kSteps; ++s) {
+      const int c = (2 * s + hi) * kVec;
+      q[s] = ld16_or0(qr + c, ok && c < p.d);
+    }
+    bits0 = 0;
+    if (p.mask && ok) bits0 = p.mask[row * p.mask_words];
+    // here, so that no wait for it lands among the loads of the loop
+    asm volatile("" ::"v"((uint32_t)bits0), "v"((uint32_t)(bits0 >> 32)));
+  }
+
+  // Bit j: this lane's row sees key first + j (j < 32) as far as the mask goes.
+  __device__ inline uint32_t sees(const AttendParams& p, const Work& w, int first) const {
+    const int rel = first - w.ctx;  // of node 0
+    if (row < 0 || rel <= -32) return ~0u;
+    if (!p.mask) {
+      const int c = node + 1 - rel;  // keys up to its own
+      return c >= 32 ? ~0u : (c <= 0 ? 0u : (1u << c) - 1u);
+    }
+    if (rel < 0) return ((uint32_t)bits0 << -rel) | ((1u << -rel) - 1u);
+    const int word = rel >> 6, sh = rel & 63;
+    if (word >= p.mask_words) return 0u;
+    const uint64_t* mr = p.mask + row * p.mask_words;
+    uint64_t x = (word ? mr[word] : bits0) >> sh;
+    if (sh > 32 && word + 1 < p.mask_words) x |= mr[word + 1] << (64 - sh);
+    return (uint32_t)x;
+  }
+
+  // Scores of 32 keys whose rows start at LDS pointer kb.
+  __device__ inline f32x16 scores(const char* kb) const {
+    f32x16 s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = 0.f;
+    const char* base = kb + r32 * R::kBytes;
+    const int x = R::swz(r32) ^ hi;
+#pragma unroll
+    for (int st = 0; st < R::kSteps; ++st) {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(base + (((2 * st) ^ x) << 4));
+      s = Mma32<Elem>::mma(a, q[st], s);
+    }
+    return s;
+  }
+
+  // Running softmax over NS blocks of scores (already scaled, -inf where
+  // masked): scores become weights.
+  template <int NS> __device__ inline void weigh(f32x16 (&s)[NS]) {
+    float mx = s[0][0];
+#pragma unroll
+    for (int b = 0; b < NS; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
+    const float mn = fmaxf(m, half_max(mx));
+    const float ms = mn == -INFINITY ? 0.f : mn;
+    if (__any(mn != m)) {
+      const float f = __builtin_amdgcn_exp2f(m - ms);
+      l *= f;
+#pragma unroll
+      for (int db = 0; db < R::kDB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[db][i] *= f;
+      m = mn;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int b = 0; b < NS; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[b][i] = __builtin_amdgcn_exp2f(s[b][i] - ms);
+        sum += s[b][i];
+      }
+    l += sum;
+  }
+
+  // o += V^T P^T over 32 keys whose value rows start at LDS pointer vb.
+  // ODD: some value may be no finite number and some row may not see its key.  A
+  // masked weight of 0 times NaN would reach every row, so such values enter as
+  // 0, and rows that see them (bit in seen) get +-infinity added where a sum of
+  // indicators says so (both: NaN).
+  template <bool ODD> __device__ inline void add_values(const char* vb, const f32x16& s, uint32_t seen) {
+    if constexpr (R::k16) {
+      const int j = lane & 15, g1 = (lane >> 4) & 1;
+      const int ra = 4 * hi + (j >> 2), rb = ra + 8;
+      const int c = 2 * g1 + ((j & 3) >> 1), tail = (j & 1) * 8;
+      const int xa = c ^ R::swz(ra), xb = c ^ R::swz(rb);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = Mma32<Elem>::pack2(s[8 * u + 2 * e], s[8 * u + 2 * e + 1]);
+        u32x4 ones;
+        if constexpr (ODD) {
+          const uint32_t sb = seen >> (16 * u + 4 * hi);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = 8 * (e >> 1) + 2 * (e & 1);
+            ones[e] = (((sb >> k) & 1) * Mma32<Elem>::kOne) | ((((sb >> (k + 1)) & 1) * Mma32<Elem>::kOne) << 16);
+          }
+        }
+        const char* pa = vb + (16 * u + ra) * R::kBytes + tail;
+        const char* pb = vb + (16 * u + rb) * R::kBytes + tail;
+#pragma unroll
+        for (int db = 0; db < R::kDB; ++db) {
+          const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(pa + (((4 * db) ^ xa) << 4)));
+          const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(pb + (((4 * db) ^ xb) << 4)));
+          const u32x2 a2 = __builtin_bit_cast(u32x2, a), b2 = __builtin_bit_cast(u32x2, b);
+          u32x4 v = u32x4{a2[0], a2[1], b2[0], b2[1]};
+          if constexpr (ODD) {
+            u32x4 up, down;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t x = v[e];
+              uint32_t y = 0, pu = 0, pd = 0;
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const uint32_t z = (x >> (16 * t)) & 0xffffu;
+                const bool odd = (z & Mma32<Elem>::kExp) == Mma32<Elem>::kExp;
+                const bool nan = odd && (z & 0x7fffu) != Mma32<Elem>::kExp;
+                y |= odd ? 0u : z << (16 * t);
+                pu |= (odd && (nan || !(z & 0x8000u)) ? Mma32<Elem>::kOne : 0u) << (16 * t);
+                pd |= (odd && (nan || (z & 0x8000u)) ? Mma32<Elem>::kOne : 0u) << (16 * t);
+              }
+              v[e] = y;
+              up[e] = pu;
+              down[e] = pd;
+            }
+            f32x16 zero;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) zero[i] = 0.f;
+            const f32x16 tu = Mma32<Elem>::mma(up, ones, zero), td = Mma32<Elem>::mma(down, ones, zero);
+            o[db] = Mma32<Elem>::mma(v, w, o[db]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[db][i] += (tu[i] > 0.f ? INFINITY : 0.f) + (td[i] > 0.f ? -INFINITY : 0.f);
+          } else {
+            o[db] = Mma32<Elem>::mma(v, w, o[db]);
+          }
+        }
+      }
+    } else {
+      const int c = (r32 >> 2) ^ (hi << 3);
+      const char* pr = vb + 4 * hi * R::kBytes + (r32 & 3) * 4;
+#pragma unroll
+      for (int db = 0; db < R::kDB; ++db) {
+        f32x16 tu, td;
+        if constexpr (ODD)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) tu[i] = td[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = 8 * (i >> 2) + (i & 3);  // + 4 hi
+          const int x = ((i & 3) << 1) | ((i >> 2) & 1);
+          float v = *reinterpret_cast<const float*>(pr + key * R::kBytes + (((8 * db) ^ c ^ x) << 4));
+          if constexpr (ODD) {
+            const bool odd = (__float_as_uint(v) & Mma32<Elem>::kExp) == Mma32<Elem>::kExp;
+            const float one = (seen >> (key + 4 * hi)) & 1 ? 1.f : 0.f;
+            tu = Mma32<Elem>::mma1(odd && !(v < 0.f) ? 1.f : 0.f, one, tu);
+            td = Mma32<Elem>::mma1(odd && !(v > 0.f) ? 1.f : 0.f, one, td);
+            v = odd ? 0.f : v;
+          }
+          o[db] = Mma32<Elem>::mma1(v, s[i], o[db]);
+        }
+        if constexpr (ODD)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[db][i] += (tu[i] > 0.f ? INFINITY : 0.f) + (td[i] > 0.f ? -INFINITY : 0.f);
       }
     }
-    const int64_t col = p.cache.page.div((uint32_t)pos);
-    if (col >= p.n_table) break;
-    const int64_t page = p.page_table[b * p.ld_table + col];
-    if (page < 0 || page >= p.cache.n_pages) continue;
-    const int64_t place = pos - col * p.cache.page.d;
-    const Elem* k = static_cast<const Elem*>(p.cache.k) + page * p.cache.k_page + kv * p.cache.k_head + place * p.cache.k_row;
-    const Elem* v = static_cast<const Elem*>(p.cache.v) + page * p.cache.v_page + kv * p.cache.v_head + place * p.cache.v_row;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (lane + 64 * e < p.d) s = __builtin_fmaf(qf[e], (float)k[lane + 64 * e], s);
-#pragma unroll
-    for (int w = 32; w; w >>= 1) s += __shfl_xor(s, w);
-    s *= p.scale;
-    if (s == -INFINITY) continue;
-    const float mn = fmaxf(m, s), f = __expf(m - mn), wgt = __expf(s - mn);
-    m = mn;
-    l = l * f + wgt;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (lane + 64 * e < p.d) o[e] = o[e] * f + wgt * (float)v[lane + 64 * e];
   }
-  Elem* out = static_cast<Elem*>(p.out) + row * p.ldo + (int64_t)h * p.d;
-  const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+
+  // Whether the value rows [0, keys) at vb hold something that is no finite
+  // number; the wave looks at all of them.
+  __device__ inline bool any_odd(const char* vb, int keys) const {
+    bool odd = false;
+    for (int e = lane; e < keys * R::kPieces; e += 64) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(vb + 16 * e);
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (lane + 64 * e < p.d) out[lane + 64 * e] = static_cast<Elem>(o[e] * inv);
-  if (p.lse && lane == 0) p.lse[row * p.hq + h] = m + logf(l);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = x[i], e1 = Mma32<Elem>::kExp;
+        if constexpr (R::k16) odd |= (w & e1) == e1 || ((w >> 16) & e1) == e1;
+        else odd |= (w & e1) == e1;
+      }
+    }
+    return __any(odd);
+  }
+
+  // Store four consecutive elements of the row's output.
+  __device__ inline static void store4(const AttendParams& p, int64_t row, int head, int at, f32x4 x) {
+    Elem* out = static_cast<Elem*>(p.out) + row * p.ldo + (int64_t)head * p.d + at;
+    if constexpr (R::k16) {
+      *reinterpret_cast<u32x2*>(out) =
+          u32x2{Mma32<Elem>::pack2(x[0], x[1]), Mma32<Elem>::pack2(x[2], x[3])};
+    } else {
+      *reinterpret_cast<f32x4*>(out) = x;
+    }
+  }
+  // Element of the row that register quad qd of block db holds first.
+  __device__ inline int element(int db, int qd) const { return 32 * db + 8 * qd + 4 * hi; }
+};
+
+__device__ inline float inverse(float l) { return l == 0.f ? 0.f : 1.0f / l; }
+
+// The workspace: for each chunk and row the unnormalised output and (m, l).
+__device__ inline float* part_o(const AttendParams& p, int split, int64_t row, int head) {
+  return p.part + (((int64_t)split * p.T + row) * p.hq + head) * p.d;
+}
+__device__ inline float* part_ml(const AttendParams& p, int split, int64_t row, int head) {
+  return p.part + (int64_t)p.splits * p.T * p.hq * p.d + (((int64_t)split * p.T + row) * p.hq + head) * 2;
+}
+
+// Where the rows of a tile's keys lie: lane's key at position pos.
+struct PageAt {
+  int pos, col;
+  bool in_table;
+};
+__device__ inline PageAt page_at(const AttendParams& p, int64_t pos, int end) {
+  PageAt a;
+  a.pos = (int)min(pos, (int64_t)end);
+  a.col = (int)p.cache.page.div((uint32_t)a.pos);
+  a.in_table = a.col < p.n_table;
+  return a;
+}
+__device__ inline const char* entry_of(const AttendParams& p, int b, const PageAt& a) {
+  return a.in_table ? reinterpret_cast<const char*>(p.page_table + b * p.ld_table + a.col)
+                    : reinterpret_cast<const char*>(g_zero_row);
+}
+template <typename Elem>
+__device__ inline const char* row_of(const AttendParams& p, int h, const PageAt& a, int id, bool is_v, bool valid) {
+  const CacheView& c = p.cache;
+  const int64_t place = a.pos - a.col * (int)c.page.d;
+  const int64_t off = (int64_t)id * (is_v ? c.v_page : c.k_page) + (int64_t)h * (is_v ? c.v_head : c.k_head) +
+                      place * (is_v ? c.v_row : c.k_row);
+  const char* at = static_cast<const char*>(is_v ? c.v : c.k) + off * (int64_t)sizeof(Elem);
+  return valid ? at : reinterpret_cast<const char*>(g_zero_row);
+}
+
+// Up to 32 rows: the NW waves of the workgroup hold the same rows and take the
+// chunk's blocks of 32 keys in turn, each through LDS of its own, so no wave
+// waits for another until their outputs meet at the end.  The next block's
+// keys are on their way during the weights and values of this one, its values
+// during the next scores.
+template <typename Elem, int DP, int NW>
+__global__ __launch_bounds__(NW * 64, 1) void attend_narrow_kernel(AttendParams p) {
+  using R = Rows<Elem, DP>;
+  constexpr int kTile = kBlock * R::kBytes;
+  constexpr int NL = kTile / 1024;  // loads of a tile of keys or values
+  __shared__ __attribute__((aligned(1024))) char s_kv[NW][2 * kTile];
+  __shared__ __attribute__((aligned(16))) const char* s_row[NW][64];
+  __shared__ int s_id[NW][2][64];
+  __shared__ float s_ml[NW][2][kBlock];
+  warm_args(p);
+  const Work w = work_of<kBlock>(p);
+  if (w.none) return;
+  RowBlock<Elem, DP> rb;
+  rb.init(p, w, w.row0);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = rb.lane;
+  char* kbuf = s_kv[wave];
+  char* vbuf = kbuf + kTile;
+  const uint32_t k_lds = (uint32_t)(uintptr_t)kbuf, v_lds = (uint32_t)(uintptr_t)vbuf;
+  const float c = p.scale * kLog2e;
+  const int blocks = w.k1 > w.k0 ? (w.k1 - w.k0 + kBlock - 1) / kBlock : 0;
+  const int nt = blocks > wave ? (blocks - wave + NW - 1) / NW : 0;
+  const int pieces_d = p.d * (int)sizeof(Elem) / 16;
+
+  auto first_key = [&](int t) { return (int64_t)w.k0 + ((int64_t)wave + (int64_t)NW * t) * kBlock; };
+  auto fetch_ids = [&](int t) {
+    word_to_lds(entry_of(p, w.b, page_at(p, first_key(t) + rb.r32, w.k1)), (uint32_t)(uintptr_t)s_id[wave][t & 1]);
+  };
+  uint32_t valid_next = 0;
+  auto find_rows = [&](int t) {  // lanes 0..31 the keys' rows, 32..63 the values'
+    const int64_t pos = first_key(t) + rb.r32;
+    const PageAt a = page_at(p, pos, w.k1);
+    const int id = s_id[wave][t & 1][lane];
+    const bool valid = pos < w.k1 && a.in_table && id >= 0 && id < p.cache.n_pages;
+    s_row[wave][lane] = row_of<Elem>(p, w.h, a, id, rb.hi, valid);
+    valid_next = (uint32_t)__ballot(valid);
+  };
+  auto load_tile = [&](int is_v) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int row = i * R::kPerLoad + lane / R::kPieces;
+      const int piece = (lane % R::kPieces) ^ R::swz(row);
+      const char* at = s_row[wave][32 * is_v + row] + 16 * piece;
+      row_to_lds(piece < pieces_d ? at : reinterpret_cast<const char*>(g_zero_row), (is_v ? v_lds : k_lds) + 1024 * i);
+    }
+  };
+
+  uint32_t valid = 0;
+  if (nt > 0) {
+    fetch_ids(0);
+    wait_loads<0>();
+    find_rows(0);
+    valid = valid_next;
+    load_tile(0);
+    fetch_ids(1);
+    load_tile(1);
+  }
+  for (int t = 0; t < nt; ++t) {
+    const bool more = t + 1 < nt;
+    const int first = (int)first_key(t);
+    wait_loads<NL>();  // keys of t and ids of t + 1 are there
+    f32x16 s[1] = {rb.scores(kbuf)};
+    wait_lds();
+    if (more) {
+      find_rows(t + 1);
+      load_tile(0);
+      fetch_ids(t + 2);
+    }
+    const uint32_t seen = valid & (first + kBlock <= w.ctx ? ~0u : rb.sees(p, w, first));
+    const bool masked = __any(seen != ~0u), uneven = __any(seen != valid);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[0][i] *= c;
+    if (masked) {
+      const uint32_t sb = seen >> (4 * rb.hi);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[0][i] = (sb >> (8 * (i >> 2) + (i & 3))) & 1 ? s[0][i] : -INFINITY;
+    }
+    rb.weigh(s);
+    if (more) wait_loads<NL + 1>();
+    else wait_loads<0>();
+    if (uneven && rb.any_odd(vbuf, kBlock)) rb.template add_values<true>(vbuf, s[0], seen);
+    else rb.template add_values<false>(vbuf, s[0], seen);
+    wait_lds();
+    if (more) load_tile(1);
+    valid = valid_next;
+  }
+
+  // the waves' outputs meet: weights to their common maximum, then block db of
+  // the output is summed and stored by wave db % NW
+  const float l = half_sum(rb.l);
+  if (rb.hi == 0) {
+    s_ml[wave][0][rb.r32] = rb.m;
+    s_ml[wave][1][rb.r32] = l;
+  }
+  f32x4* red = reinterpret_cast<f32x4*>(kbuf);
+#pragma unroll
+  for (int db = 0; db < R::kDB; ++db)
+#pragma unroll
+    for (int qd = 0; qd < 4; ++qd)
+      red[(db * 4 + qd) * 64 + lane] =
+          f32x4{rb.o[db][4 * qd], rb.o[db][4 * qd + 1], rb.o[db][4 * qd + 2], rb.o[db][4 * qd + 3]};
+  __syncthreads();
+  float M = -INFINITY, L = 0.f, f[NW];
+#pragma unroll
+  for (int i = 0; i < NW; ++i) M = fmaxf(M, s_ml[i][0][rb.r32]);
+  const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    f[i] = __builtin_amdgcn_exp2f(s_ml[i][0][rb.r32] - ms);
+    L += s_ml[i][1][rb.r32] * f[i];
+  }
+  if (rb.row < 0) return;
+  const bool whole = p.splits == 1;
+  const float inv = whole ? inverse(L) : 1.0f;
+  for (int db = wave; db < R::kDB; db += NW) {
+#pragma unroll
+    for (int qd = 0; qd < 4; ++qd) {
+      const int at = rb.element(db, qd);
+      if (at >= p.d) continue;
+      f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const f32x4 x = reinterpret_cast<const f32x4*>(s_kv[i])[(db * 4 + qd) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(x[e], f[i], sum[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] *= inv;
+      if (whole) rb.store4(p, rb.row, rb.head, at, sum);
+      else *reinterpret_cast<f32x4*>(part_o(p, w.split, rb.row, rb.head) + at) = sum;
+    }
+  }
+  if (wave == 0 && rb.hi == 0) {
+    if (!whole) {
+      float* ml = part_ml(p, w.split, rb.row, rb.head);
+      ml[0] = M;
+      ml[1] = L;
+    } else if (p.lse) {
+      p.lse[rb.row * p.hq + rb.head] = (M + __builtin_amdgcn_logf(L)) * kLn2;
+    }
+  }
+}
+
+// More rows: four waves of 32 rows share tiles of KT keys, double buffered; a
+// wave fetches a quarter of each tile's rows.
+template <typename Elem, int DP, int KT>
+__global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p) {
+  using R = Rows<Elem, DP>;
+  constexpr int NS = KT / kBlock;
+  constexpr int kTile = KT * R::kBytes;
+  constexpr int kMine = KT / 4;                       // rows a wave fetches of K, and of V
+  constexpr int NL = kMine * R::kBytes / 1024;
+  static_assert(kMine % R::kPerLoad == 0 && NL >= 1, "");
+  __shared__ __attribute__((aligned(1024))) char s_kv[2][2 * kTile];
+  __shared__ __attribute__((aligned(16))) const char* s_row[4][64];
+  __shared__ int s_id[4][2][64];
+  __shared__ uint32_t s_valid[2][4];
+  warm_args(p);
+  const Work w = work_of<4 * kBlock>(p);
+  if (w.none) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowBlock<Elem, DP> rb;
+  rb.init(p, w, w.row0 + wave * kBlock);
+  const bool idle = w.row0 + wave * kBlock >= w.rows;  // a wave without rows only fetches
+  const int lane = rb.lane;
+  const float c = p.scale * kLog2e;
+  const int nt = w.k1 > w.k0 ? (w.k1 - w.k0 + KT - 1) / KT : 0;
+  const int pieces_d = p.d * (int)sizeof(Elem) / 16;
+  const int my = lane % kMine, my_v = (lane / kMine) & 1;
+
+  auto fetch_ids = [&](int t) {
+    word_to_lds(entry_of(p, w.b, page_at(p, (int64_t)w.k0 + (int64_t)t * KT + wave * kMine + my, w.k1)),
+                (uint32_t)(uintptr_t)s_id[wave][t & 1]);
+  };
+  auto load_tile = [&](int t) {
+    const int64_t pos = (int64_t)w.k0 + (int64_t)t * KT + wave * kMine + my;
+    const PageAt a = page_at(p, pos, w.k1);
+    const int id = s_id[wave][t & 1][lane];
+    const bool valid = pos < w.k1 && a.in_table && id >= 0 && id < p.cache.n_pages;
+    s_row[wave][lane] = row_of<Elem>(p, w.h, a, id, my_v, valid);
+    const uint32_t got = (uint32_t)__ballot(valid) & (uint32_t)((1ull << kMine) - 1);
+    if (lane == 0) s_valid[t & 1][wave] = got;
+#pragma unroll
+    for (int is_v = 0; is_v < 2; ++is_v)
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int r = i * R::kPerLoad + lane / R::kPieces;
+        const int piece = (lane % R::kPieces) ^ R::swz(wave * kMine + r);
+        const char* at = s_row[wave][kMine * is_v + r] + 16 * piece;
+        row_to_lds(piece < pieces_d ? at : reinterpret_cast<const char*>(g_zero_row),
+                   (uint32_t)(uintptr_t)s_kv[t & 1] + is_v * kTile + wave * kMine * R::kBytes + 1024 * i);
+      }
+  };
+
+  if (nt > 0) {
+    fetch_ids(0);
+    wait_loads<0>();
+    load_tile(0);
+    fetch_ids(1);
+  }
+  for (int t = 0; t < nt; ++t) {
+    wait_loads<0>();  // this wave's part of tile t, and its ids of t + 1
+    lds_barrier();    // everyone's, and everyone is done with tile t - 1
+    if (t + 1 < nt) {
+      load_tile(t + 1);
+      fetch_ids(t + 2);
+    }
+    if (idle) continue;
+    const char* kb = s_kv[t & 1];
+    const char* vb = kb + kTile;
+    const int first = w.k0 + t * KT;
+    f32x16 s[NS];
+    uint32_t seen[NS];
+    bool uneven = false;
+#pragma unroll
+    for (int b = 0; b < NS; ++b) {
+      s[b] = rb.scores(kb + b * kBlock * R::kBytes);
+      uint32_t valid = 0;
+#pragma unroll
+      for (int i = 0; i < 4 / NS; ++i) valid |= s_valid[t & 1][b * (4 / NS) + i] << (i * kMine);
+      seen[b] = valid & (first + b * kBlock + kBlock <= w.ctx ? ~0u : rb.sees(p, w, first + b * kBlock));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] *= c;
+      if (__any(seen[b] != ~0u)) {
+        const uint32_t sb = seen[b] >> (4 * rb.hi);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] = (sb >> (8 * (i >> 2) + (i & 3))) & 1 ? s[b][i] : -INFINITY;
+        uneven |= __any(seen[b] != valid);
+      }
+    }
+    rb.weigh(s);
+    if (uneven && rb.any_odd(vb, KT)) {
+#pragma unroll
+      for (int b = 0; b < NS; ++b) rb.template add_values<true>(vb + b * kBlock * R::kBytes, s[b], seen[b]);
+    } else {
+#pragma unroll
+      for (int b = 0; b < NS; ++b) rb.template add_values<false>(vb + b * kBlock * R::kBytes, s[b], seen[b]);
+    }
+  }
+
+  if (rb.row < 0) return;
+  const float l = half_sum(rb.l);
+  const bool whole = p.splits == 1;
+  const float inv = whole ? inverse(l) : 1.0f;
+#pragma unroll
+  for (int db = 0; db < R::kDB; ++db)
+#pragma unroll
+    for (int qd = 0; qd < 4; ++qd) {
+      const int at = rb.element(db, qd);
+      if (at >= p.d) continue;
+      f32x4 x = f32x4{rb.o[db][4 * qd], rb.o[db][4 * qd + 1], rb.o[db][4 * qd + 2], rb.o[db][4 * qd + 3]};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] *= inv;
+      if (whole) rb.store4(p, rb.row, rb.head, at, x);
+      else *reinterpret_cast<f32x4*>(part_o(p, w.split, rb.row, rb.head) + at) = x;
+    }
+  if (rb.hi == 0) {
+    if (!whole) {
+      float* ml = part_ml(p, w.split, rb.row, rb.head);
+      ml[0] = rb.m;
+      ml[1] = l;
+    } else if (p.lse) {
+      p.lse[rb.row * p.hq + rb.head] = (rb.m + __builtin_amdgcn_logf(l)) * kLn2;
+    }
+  }
+}
+
+// Join a row's chunks, in their order: one wave a row, 4 elements a lane, the
+// lanes left over by a short head taking every second (fourth, ..) chunk.
+template <typename Elem>
+__global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendParams p) {
+  warm_args(p);
+  // grid: (rows of the longest sequence * heads / 4, sequences)
+  const int b = blockIdx.y;
+  int64_t start;
+  int n, ctx;
+  sequence_of(p, b, start, n, ctx);
+  const int r = (int)blockIdx.x * (kThreads / 64) + (int)(threadIdx.x >> 6);
+  const int i = r / p.hq, h = r - i * p.hq;
+  if (i >= n) return;
+  const int splits = splits_of(p, n, ctx);
+  const int64_t row = start + i;
+  const int lane = threadIdx.x & 63;
+  int lanes = 1;  // lanes of one chunk: a power of two
+  while (lanes * 4 < p.d) lanes *= 2;
+  const int at = 4 * (lane % lanes);
+  const bool ok = at < p.d;
+  float M = -INFINITY;
+  for (int s = lane; s < splits; s += 64) M = fmaxf(M, part_ml(p, s, row, h)[0]);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
+  const float ms = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int s = lane / lanes; s < splits; s += 64 / lanes) {
+    const float* ml = part_ml(p, s, row, h);
+    const float f = __builtin_amdgcn_exp2f(ml[0] - ms);
+    const float l = ml[1];
+    if (l == 0.f) continue;
+    const f32x4 x = ldf4_or0(part_o(p, s, row, h) + at, ok);
+    L = __builtin_fmaf(l, f, L);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(x[e], f, sum[e]);
+  }
+  for (int o = lanes; o < 64; o <<= 1) {
+    L += __shfl_xor(L, o);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += __shfl_xor(sum[e], o);
+  }
+  const float inv = inverse(L);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum[e] *= inv;
+  if (lane < lanes && ok) RowBlock<Elem, 64>::store4(p, row, h, at, sum);
+  if (p.lse && lane == 0) p.lse[row * p.hq + h] = (M + __builtin_amdgcn_logf(L)) * kLn2;
+}
+
+// ---- host ------------------------------------------------------------------
+
+// How the keys are cut: chunks so long that there are about kTargetGroups
+// workgroups in all where every sequence is as long as its bound, and no
+// shorter than kMinChunk keys.
+constexpr int64_t kTargetGroups = 1024;
+constexpr int64_t kMinChunk = 256;
+constexpr int64_t kMaxGroups = (int64_t)1 << 30;
+
+struct AttendPlan {
+  bool wide;
+  int32_t chunk, splits, row_tiles;
+};
+
+AttendPlan attend_plan(int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk) {
+  AttendPlan a;
+  const int64_t rows = (int64_t)max_nodes * (hq / hk), keys = (int64_t)max_context + max_nodes;
+  a.wide = rows > kBlock;
+  a.row_tiles = (int32_t)ceil_div(rows, a.wide ? 4 * kBlock : kBlock);
+  const int64_t units = (int64_t)B * hk * a.row_tiles;
+  int64_t chunk = ceil_div(keys * units, a.wide ? kTargetGroups / 2 : kTargetGroups);
+  if (chunk < kMinChunk) chunk = kMinChunk;
+  const int64_t fewest = ceil_div(keys * units, kMaxGroups);
+  if (chunk < fewest) chunk = fewest;
+  chunk = ceil_div(chunk, 256) * 256;
+  if (chunk > ((int64_t)1 << 30)) chunk = (int64_t)1 << 30;
+  a.chunk = (int32_t)chunk;
+  a.splits = (int32_t)ceil_div(keys, chunk);
+  return a;
+}
+
+template <typename Elem, int DP>
+hipError_t launch_d(const AttendParams& p, bool wide, hipStream_t stream) {
+  constexpr int kRow = DP * (int)sizeof(Elem);
+  const int64_t units = (int64_t)p.B * p.hk * p.splits * p.row_tiles;
+  const int64_t grid = ceil_div(units, kXcds) * kXcds;
+  if (grid > (int64_t)0x7fffffff) return hipErrorInvalidConfiguration;
+  if (wide) {
+    constexpr int KT = kRow <= 256 ? 64 : 32;
+    hipLaunchKernelGGL((attend_wide_kernel<Elem, DP, KT>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
+  } else {
+    constexpr int NW = kRow <= 512 ? 4 : 2;
+    hipLaunchKernelGGL((attend_narrow_kernel<Elem, DP, NW>), dim3((unsigned)grid), dim3(NW * 64), 0, stream, p);
+  }
+  return hipGetLastError();
 }
 
 template <typename Elem>
-hipError_t launch(const AttendParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL(attend_kernel<Elem>, dim3((unsigned)p.max_nodes, (unsigned)p.hq, (unsigned)p.B), dim3(64), 0,
-                     stream, p);
+hipError_t launch(AttendParams p, hipStream_t stream) {
+  const AttendPlan a = attend_plan(p.B, p.max_nodes, p.max_context, p.hq, p.hk);
+  p.chunk = a.chunk;
+  p.splits = a.splits;
+  p.row_tiles = a.row_tiles;
+  hipError_t e = p.d <= 64    ? launch_d<Elem, 64>(p, a.wide, stream)
+                 : p.d <= 128 ? launch_d<Elem, 128>(p, a.wide, stream)
+                              : launch_d<Elem, 256>(p, a.wide, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t rows = (int64_t)p.max_nodes * p.hq;
+  hipLaunchKernelGGL(attend_join_kernel<Elem>, dim3((unsigned)ceil_div(rows, kThreads / 64), (unsigned)p.B),
+                     dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t attend_need_bytes(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+int64_t attend_need_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
+                          int32_t d) {
+  const AttendPlan a = attend_plan(B, max_nodes, max_context, hq, hk);
+  if (a.splits == 1) return 0;
+  const int64_t bytes = (int64_t)a.splits * T * hq * (d + 2) * 4;
+  return (bytes + 255) & ~int64_t(255);
+}
 
 hipError_t launch_attend(lora_dtype dt, const AttendParams& p, hipStream_t stream) {
   switch (dt) {

@@ -82,6 +82,8 @@ struct AttendParams {
   int32_t T, B, hq, hk, d, n_table, max_nodes, max_context, mask_words;
   FastDiv group;  // by q_heads / kv_heads
   float* part;    // workspace
+  // filled by the launcher (AttendPlan)
+  int32_t chunk, splits, row_tiles;
 };
 
 hipError_t launch_rope_table(const double* inv_freq, int32_t rot, double magnitude, int64_t first, int64_t n,
