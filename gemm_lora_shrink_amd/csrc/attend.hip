@@ -48,7 +48,6 @@ template <> struct Mma32<bf16_t> {
   }
   __device__ static inline uint32_t pack2(float a, float b) { return pack2_bf16(a, b); }
   static constexpr uint32_t kExp = 0x7f80u;  // all ones: no finite number
-  static constexpr uint32_t kOne = 0x3f80u;
 };
 template <> struct Mma32<half_t> {
   __device__ static inline f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
@@ -57,7 +56,6 @@ template <> struct Mma32<half_t> {
   }
   __device__ static inline uint32_t pack2(float a, float b) { return pack2_f16(a, b); }
   static constexpr uint32_t kExp = 0x7c00u;
-  static constexpr uint32_t kOne = 0x3c00u;
 };
 template <> struct Mma32<float> {
   __device__ static inline f32x16 mma1(float a, float b, f32x16 c) {
@@ -83,6 +81,9 @@ template <typename Elem, int DP> struct Rows {
   static constexpr int kSteps = kBytes / 32;       // 16-byte operands of a lane and half
   static constexpr int kDB = DP / kBlock;          // blocks of the output
   static constexpr int kPerLoad = 1024 / kBytes;   // rows of one 64-lane load
+  // waves of a SIMD that the kernels are compiled for: two workgroups a compute
+  // unit where LDS and registers have room for them
+  static constexpr int kWaves = kBytes <= 256 ? 2 : 1;
   static_assert(kBytes >= 128 && kBytes <= 1024, "");
   // position of piece c of row r: c ^ swz(r)
   __device__ static inline int swz(int r) {
@@ -206,7 +207,7 @@ template <typename Elem, int DP> struct RowBlock {
   int head;
   uint64_t bits0;      // first word of the mask row
 
-  __device__ inline void init(const AttendParams& p, const Work& w, int row_first) {
+  __device__ __forceinline__ void init(const AttendParams& p, const Work& w, int row_first) {
     lane = threadIdx.x & 63;
     r32 = lane & 31;
     hi = lane >> 5;
@@ -223,10 +224,15 @@ template <typename Elem, int DP> struct RowBlock {
     row = ok ? w.start + node : -1;
     const Elem* qr = static_cast<const Elem*>(p.q) + (ok ? row : 0) * p.ldq + (int64_t)head * p.d;
     constexpr int kVec = Traits<Elem>::kVec;
+    // the softmax takes a positive factor: a negative scale turns q's signs
+    // instead, and a scale of 0 is a q of zeros
+    const uint32_t flip = p.scale < 0.f ? (R::k16 ? 0x80008000u : 0x80000000u) : 0u;
 #pragma unroll
     for (int s = 0; s < R::kSteps; ++s) {
       const int c = (2 * s + hi) * kVec;
-      q[s] = ld16_or0(qr + c, ok && c < p.d);
+      q[s] = ld16_or0(qr + c, ok && c < p.d && p.scale != 0.f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[s][e] ^= flip;
     }
     bits0 = 0;
     if (p.mask && ok) bits0 = p.mask[row * p.mask_words];
@@ -235,7 +241,7 @@ template <typename Elem, int DP> struct RowBlock {
   }
 
   // Bit j: this lane's row sees key first + j (j < 32) as far as the mask goes.
-  __device__ inline uint32_t sees(const AttendParams& p, const Work& w, int first) const {
+  __device__ __forceinline__ uint32_t sees(const AttendParams& p, const Work& w, int first) const {
     const int rel = first - w.ctx;  // of node 0
     if (row < 0 || rel <= -32) return ~0u;
     if (!p.mask) {
@@ -251,33 +257,43 @@ template <typename Elem, int DP> struct RowBlock {
     return (uint32_t)x;
   }
 
-  // Scores of 32 keys whose rows start at LDS pointer kb.
-  __device__ inline f32x16 scores(const char* kb) const {
+  // Scores of 32 keys whose rows start at LDS pointer kb.  The keys' operands are
+  // requested eight at a time ahead of their products.
+  __device__ __forceinline__ f32x16 scores(const char* kb) const {
     f32x16 s;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = 0.f;
     const char* base = kb + r32 * R::kBytes;
     const int x = R::swz(r32) ^ hi;
+    constexpr int kAhead = R::kSteps < 8 ? R::kSteps : 8;
 #pragma unroll
-    for (int st = 0; st < R::kSteps; ++st) {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(base + (((2 * st) ^ x) << 4));
-      s = Mma32<Elem>::mma(a, q[st], s);
+    for (int s0 = 0; s0 < R::kSteps; s0 += kAhead) {
+      u32x4 a[kAhead];
+#pragma unroll
+      for (int st = 0; st < kAhead; ++st)
+        a[st] = *reinterpret_cast<const u32x4*>(base + (((2 * (s0 + st)) ^ x) << 4));
+#pragma unroll
+      for (int st = 0; st < kAhead; ++st) s = Mma32<Elem>::mma(a[st], q[s0 + st], s);
     }
     return s;
   }
 
-  // Running softmax over NS blocks of scores (already scaled, -inf where
-  // masked): scores become weights.
-  template <int NS> __device__ inline void weigh(f32x16 (&s)[NS]) {
+  // Running softmax over NS blocks of scores (-inf where masked): scores become
+  // weights.  c > 0 turns scores into powers of two.  The maximum a row is
+  // measured from is moved only where a score passes it by kSlack powers of two:
+  // sums and weights stay far from overflow (2^8 in fp16's 65504), and most tiles
+  // leave the output as it is.
+  template <int NS> __device__ __forceinline__ void weigh(f32x16 (&s)[NS], float c) {
+    constexpr float kSlack = 8.0f;
     float mx = s[0][0];
 #pragma unroll
     for (int b = 0; b < NS; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
-    const float mn = fmaxf(m, half_max(mx));
-    const float ms = mn == -INFINITY ? 0.f : mn;
-    if (__any(mn != m)) {
-      const float f = __builtin_amdgcn_exp2f(m - ms);
+    mx = half_max(mx) * c;
+    if (__any(mx > m + kSlack)) {
+      const float mn = mx > m + kSlack ? mx : m;
+      const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
       l *= f;
 #pragma unroll
       for (int db = 0; db < R::kDB; ++db)
@@ -285,23 +301,28 @@ template <typename Elem, int DP> struct RowBlock {
         for (int i = 0; i < 16; ++i) o[db][i] *= f;
       m = mn;
     }
+    const float ms = m == -INFINITY ? 0.f : m;
     float sum = 0.f;
 #pragma unroll
     for (int b = 0; b < NS; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        s[b][i] = __builtin_amdgcn_exp2f(s[b][i] - ms);
+        s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, -ms));
         sum += s[b][i];
       }
     l += sum;
   }
 
-  // o += V^T P^T over 32 keys whose value rows start at LDS pointer vb.
-  // ODD: some value may be no finite number and some row may not see its key.  A
-  // masked weight of 0 times NaN would reach every row, so such values enter as
-  // 0, and rows that see them (bit in seen) get +-infinity added where a sum of
-  // indicators says so (both: NaN).
-  template <bool ODD> __device__ inline void add_values(const char* vb, const f32x16& s, uint32_t seen) {
+  // -inf for the keys that this lane's row does not see.
+  __device__ __forceinline__ void mask_scores(f32x16& s, uint32_t seen) const {
+    const uint32_t sb = seen >> (4 * hi);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = (sb >> (8 * (i >> 2) + (i & 3))) & 1 ? s[i] : -INFINITY;
+  }
+
+  // o += V^T P^T over 32 keys whose value rows start at LDS pointer vb.  ODD: what
+  // is no finite number enters as 0 (see add_odd).
+  template <bool ODD> __device__ __forceinline__ void add_values(const char* vb, const f32x16& s) {
     if constexpr (R::k16) {
       const int j = lane & 15, g1 = (lane >> 4) & 1;
       const int ra = 4 * hi + (j >> 2), rb = ra + 8;
@@ -312,89 +333,84 @@ template <typename Elem, int DP> struct RowBlock {
         u32x4 w;
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = Mma32<Elem>::pack2(s[8 * u + 2 * e], s[8 * u + 2 * e + 1]);
-        u32x4 ones;
-        if constexpr (ODD) {
-          const uint32_t sb = seen >> (16 * u + 4 * hi);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = 8 * (e >> 1) + 2 * (e & 1);
-            ones[e] = (((sb >> k) & 1) * Mma32<Elem>::kOne) | ((((sb >> (k + 1)) & 1) * Mma32<Elem>::kOne) << 16);
-          }
-        }
         const char* pa = vb + (16 * u + ra) * R::kBytes + tail;
         const char* pb = vb + (16 * u + rb) * R::kBytes + tail;
+        s16x4 va[R::kDB], vc[R::kDB];
 #pragma unroll
         for (int db = 0; db < R::kDB; ++db) {
-          const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(pa + (((4 * db) ^ xa) << 4)));
-          const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(pb + (((4 * db) ^ xb) << 4)));
-          const u32x2 a2 = __builtin_bit_cast(u32x2, a), b2 = __builtin_bit_cast(u32x2, b);
+          va[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(pa + (((4 * db) ^ xa) << 4)));
+          vc[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(pb + (((4 * db) ^ xb) << 4)));
+        }
+#pragma unroll
+        for (int db = 0; db < R::kDB; ++db) {
+          const u32x2 a2 = __builtin_bit_cast(u32x2, va[db]), b2 = __builtin_bit_cast(u32x2, vc[db]);
           u32x4 v = u32x4{a2[0], a2[1], b2[0], b2[1]};
-          if constexpr (ODD) {
-            u32x4 up, down;
+          if constexpr (ODD)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t x = v[e];
-              uint32_t y = 0, pu = 0, pd = 0;
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                const uint32_t z = (x >> (16 * t)) & 0xffffu;
-                const bool odd = (z & Mma32<Elem>::kExp) == Mma32<Elem>::kExp;
-                const bool nan = odd && (z & 0x7fffu) != Mma32<Elem>::kExp;
-                y |= odd ? 0u : z << (16 * t);
-                pu |= (odd && (nan || !(z & 0x8000u)) ? Mma32<Elem>::kOne : 0u) << (16 * t);
-                pd |= (odd && (nan || (z & 0x8000u)) ? Mma32<Elem>::kOne : 0u) << (16 * t);
-              }
-              v[e] = y;
-              up[e] = pu;
-              down[e] = pd;
+              const uint32_t x = v[e], e1 = Mma32<Elem>::kExp, e2 = e1 << 16;
+              v[e] = ((x & e1) == e1 ? 0u : x & 0xffffu) | ((x & e2) == e2 ? 0u : x & 0xffff0000u);
             }
-            f32x16 zero;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) zero[i] = 0.f;
-            const f32x16 tu = Mma32<Elem>::mma(up, ones, zero), td = Mma32<Elem>::mma(down, ones, zero);
-            o[db] = Mma32<Elem>::mma(v, w, o[db]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              o[db][i] += (tu[i] > 0.f ? INFINITY : 0.f) + (td[i] > 0.f ? -INFINITY : 0.f);
-          } else {
-            o[db] = Mma32<Elem>::mma(v, w, o[db]);
-          }
+          o[db] = Mma32<Elem>::mma(v, w, o[db]);
         }
       }
     } else {
       const int c = (r32 >> 2) ^ (hi << 3);
       const char* pr = vb + 4 * hi * R::kBytes + (r32 & 3) * 4;
 #pragma unroll
-      for (int db = 0; db < R::kDB; ++db) {
-        f32x16 tu, td;
-        if constexpr (ODD)
+      for (int i = 0; i < 16; ++i) {
+        const int key = 8 * (i >> 2) + (i & 3);  // + 4 hi
+        const int x = ((i & 3) << 1) | ((i >> 2) & 1);
+        float v[R::kDB];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) tu[i] = td[i] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = 8 * (i >> 2) + (i & 3);  // + 4 hi
-          const int x = ((i & 3) << 1) | ((i >> 2) & 1);
-          float v = *reinterpret_cast<const float*>(pr + key * R::kBytes + (((8 * db) ^ c ^ x) << 4));
-          if constexpr (ODD) {
-            const bool odd = (__float_as_uint(v) & Mma32<Elem>::kExp) == Mma32<Elem>::kExp;
-            const float one = (seen >> (key + 4 * hi)) & 1 ? 1.f : 0.f;
-            tu = Mma32<Elem>::mma1(odd && !(v < 0.f) ? 1.f : 0.f, one, tu);
-            td = Mma32<Elem>::mma1(odd && !(v > 0.f) ? 1.f : 0.f, one, td);
-            v = odd ? 0.f : v;
-          }
-          o[db] = Mma32<Elem>::mma1(v, s[i], o[db]);
+        for (int db = 0; db < R::kDB; ++db) {
+          v[db] = *reinterpret_cast<const float*>(pr + key * R::kBytes + (((8 * db) ^ c ^ x) << 4));
+          if (ODD && (__float_as_uint(v[db]) & Mma32<Elem>::kExp) == Mma32<Elem>::kExp) v[db] = 0.f;
         }
-        if constexpr (ODD)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            o[db][i] += (tu[i] > 0.f ? INFINITY : 0.f) + (td[i] > 0.f ? -INFINITY : 0.f);
+        for (int db = 0; db < R::kDB; ++db) o[db] = Mma32<Elem>::mma1(v[db], s[i], o[db]);
       }
+    }
+  }
+
+  // The values that add_values<true> left out: infinities and NaN reach the rows
+  // that see their key.  In the product a masked weight of 0 would have turned
+  // them into NaN for every row.
+  __device__ __forceinline__ void add_odd(const char* vb, uint32_t seen) {
+#pragma unroll 1
+    for (int k = 0; k < kBlock; ++k) {
+      if (!any_odd(vb + k * R::kBytes, 1)) continue;
+      const bool mine = (seen >> k) & 1;
+#pragma unroll
+      for (int db = 0; db < R::kDB; ++db)
+#pragma unroll
+        for (int qd = 0; qd < 4; ++qd) {
+          const int at = element(db, qd) * (int)sizeof(Elem);
+          const char* px = vb + k * R::kBytes + (((at >> 4) ^ R::swz(k)) << 4) + (at & 15);
+          uint32_t x[4];
+          if constexpr (R::k16) {
+            const u32x2 h = *reinterpret_cast<const u32x2*>(px);
+            const uint32_t h0 = h[0], h1 = h[1];
+            x[0] = h0 & 0xffffu;
+            x[1] = h0 >> 16;
+            x[2] = h1 & 0xffffu;
+            x[3] = h1 >> 16;
+          } else {
+            const u32x4 h = *reinterpret_cast<const u32x4*>(px);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = h[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (mine && (x[e] & Mma32<Elem>::kExp) == Mma32<Elem>::kExp)
+              o[db][4 * qd + e] += Traits<Elem>::elem_to_float(x[e]);
+        }
     }
   }
 
   // Whether the value rows [0, keys) at vb hold something that is no finite
   // number; the wave looks at all of them.
-  __device__ inline bool any_odd(const char* vb, int keys) const {
+  __device__ __forceinline__ bool any_odd(const char* vb, int keys) const {
     bool odd = false;
     for (int e = lane; e < keys * R::kPieces; e += 64) {
       const u32x4 x = *reinterpret_cast<const u32x4*>(vb + 16 * e);
@@ -409,7 +425,7 @@ template <typename Elem, int DP> struct RowBlock {
   }
 
   // Store four consecutive elements of the row's output.
-  __device__ inline static void store4(const AttendParams& p, int64_t row, int head, int at, f32x4 x) {
+  __device__ __forceinline__ static void store4(const AttendParams& p, int64_t row, int head, int at, f32x4 x) {
     Elem* out = static_cast<Elem*>(p.out) + row * p.ldo + (int64_t)head * p.d + at;
     if constexpr (R::k16) {
       *reinterpret_cast<u32x2*>(out) =
@@ -419,7 +435,14 @@ template <typename Elem, int DP> struct RowBlock {
     }
   }
   // Element of the row that register quad qd of block db holds first.
-  __device__ inline int element(int db, int qd) const { return 32 * db + 8 * qd + 4 * hi; }
+  __device__ __forceinline__ int element(int db, int qd) const { return 32 * db + 8 * qd + 4 * hi; }
+};
+
+struct No {
+  static constexpr bool value = false;
+};
+struct Yes {
+  static constexpr bool value = true;
 };
 
 __device__ inline float inverse(float l) { return l == 0.f ? 0.f : 1.0f / l; }
@@ -458,13 +481,21 @@ __device__ inline const char* row_of(const AttendParams& p, int h, const PageAt&
   return valid ? at : reinterpret_cast<const char*>(g_zero_row);
 }
 
+// The global addresses that this lane loads for a tile, found one tile ahead:
+// loads of a row's 16-byte pieces, NL of the keys and NL of the values.
+template <int NL> struct TileRows {
+  const char *k[NL], *v[NL];
+  uint32_t valid;  // rows that are keys
+};
+
 // Up to 32 rows: the NW waves of the workgroup hold the same rows and take the
 // chunk's blocks of 32 keys in turn, each through LDS of its own, so no wave
 // waits for another until their outputs meet at the end.  The next block's
 // keys are on their way during the weights and values of this one, its values
-// during the next scores.
+// during the next scores; page numbers come through LDS three blocks ahead,
+// addresses are found two blocks ahead.
 template <typename Elem, int DP, int NW>
-__global__ __launch_bounds__(NW * 64, 1) void attend_narrow_kernel(AttendParams p) {
+__global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kWaves)) void attend_narrow_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
   constexpr int kTile = kBlock * R::kBytes;
   constexpr int NL = kTile / 1024;  // loads of a tile of keys or values
@@ -481,73 +512,90 @@ __global__ __launch_bounds__(NW * 64, 1) void attend_narrow_kernel(AttendParams 
   char* kbuf = s_kv[wave];
   char* vbuf = kbuf + kTile;
   const uint32_t k_lds = (uint32_t)(uintptr_t)kbuf, v_lds = (uint32_t)(uintptr_t)vbuf;
-  const float c = p.scale * kLog2e;
-  const int blocks = w.k1 > w.k0 ? (w.k1 - w.k0 + kBlock - 1) / kBlock : 0;
-  const int nt = blocks > wave ? (blocks - wave + NW - 1) / NW : 0;
+  const float c = p.scale == 0.f ? 1.0f : fabsf(p.scale) * kLog2e;
+  // this wave's tiles, the first nf of them wholly inside the context
+  const auto tiles = [&](int keys, bool whole) {
+    const int blocks = keys <= 0 ? 0 : whole ? keys / kBlock : (keys + kBlock - 1) / kBlock;
+    return blocks > wave ? (blocks - wave + NW - 1) / NW : 0;
+  };
+  const int nt = tiles(w.k1 - w.k0, false), nf = tiles(min(w.ctx, w.k1) - w.k0, true);
   const int pieces_d = p.d * (int)sizeof(Elem) / 16;
+  const char* zeros = reinterpret_cast<const char*>(g_zero_row);
 
   auto first_key = [&](int t) { return (int64_t)w.k0 + ((int64_t)wave + (int64_t)NW * t) * kBlock; };
   auto fetch_ids = [&](int t) {
     word_to_lds(entry_of(p, w.b, page_at(p, first_key(t) + rb.r32, w.k1)), (uint32_t)(uintptr_t)s_id[wave][t & 1]);
   };
-  uint32_t valid_next = 0;
+  TileRows<NL> at;
   auto find_rows = [&](int t) {  // lanes 0..31 the keys' rows, 32..63 the values'
     const int64_t pos = first_key(t) + rb.r32;
     const PageAt a = page_at(p, pos, w.k1);
     const int id = s_id[wave][t & 1][lane];
     const bool valid = pos < w.k1 && a.in_table && id >= 0 && id < p.cache.n_pages;
     s_row[wave][lane] = row_of<Elem>(p, w.h, a, id, rb.hi, valid);
-    valid_next = (uint32_t)__ballot(valid);
-  };
-  auto load_tile = [&](int is_v) {
+    at.valid = (uint32_t)__ballot(valid);
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const int row = i * R::kPerLoad + lane / R::kPieces;
       const int piece = (lane % R::kPieces) ^ R::swz(row);
-      const char* at = s_row[wave][32 * is_v + row] + 16 * piece;
-      row_to_lds(piece < pieces_d ? at : reinterpret_cast<const char*>(g_zero_row), (is_v ? v_lds : k_lds) + 1024 * i);
+      const bool in = piece < pieces_d;
+      const char *kr = s_row[wave][row], *vr = s_row[wave][32 + row];
+      at.k[i] = (in ? kr : zeros) + 16 * piece;
+      at.v[i] = (in ? vr : zeros) + 16 * piece;
     }
+  };
+  auto load_keys = [&]() {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) row_to_lds(at.k[i], k_lds + 1024 * i);
+  };
+  auto load_values = [&]() {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) row_to_lds(at.v[i], v_lds + 1024 * i);
   };
 
   uint32_t valid = 0;
   if (nt > 0) {
     fetch_ids(0);
+    fetch_ids(1);
     wait_loads<0>();
     find_rows(0);
-    valid = valid_next;
-    load_tile(0);
-    fetch_ids(1);
-    load_tile(1);
+    valid = at.valid;
+    load_keys();
+    fetch_ids(2);
+    load_values();
+    find_rows(1);
   }
-  for (int t = 0; t < nt; ++t) {
+  auto tile = [&](int t, auto tail) __attribute__((always_inline)) {
     const bool more = t + 1 < nt;
-    const int first = (int)first_key(t);
-    wait_loads<NL>();  // keys of t and ids of t + 1 are there
+    wait_loads<NL>();  // keys of t and page numbers of t + 2 are there
     f32x16 s[1] = {rb.scores(kbuf)};
     wait_lds();
     if (more) {
-      find_rows(t + 1);
-      load_tile(0);
-      fetch_ids(t + 2);
+      load_keys();
+      fetch_ids(t + 3);
     }
-    const uint32_t seen = valid & (first + kBlock <= w.ctx ? ~0u : rb.sees(p, w, first));
-    const bool masked = __any(seen != ~0u), uneven = __any(seen != valid);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s[0][i] *= c;
-    if (masked) {
-      const uint32_t sb = seen >> (4 * rb.hi);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[0][i] = (sb >> (8 * (i >> 2) + (i & 3))) & 1 ? s[0][i] : -INFINITY;
-    }
-    rb.weigh(s);
+    uint32_t seen = valid;
+    if constexpr (decltype(tail)::value) seen &= rb.sees(p, w, (int)first_key(t));
+    if (__any(seen != ~0u)) rb.mask_scores(s[0], seen);
+    rb.weigh(s, c);
     if (more) wait_loads<NL + 1>();
     else wait_loads<0>();
-    if (uneven && rb.any_odd(vbuf, kBlock)) rb.template add_values<true>(vbuf, s[0], seen);
-    else rb.template add_values<false>(vbuf, s[0], seen);
+    if (decltype(tail)::value && __any(seen != valid) && rb.any_odd(vbuf, kBlock)) {
+      rb.template add_values<decltype(tail)::value>(vbuf, s[0]);
+      rb.add_odd(vbuf, seen);
+    } else {
+      rb.template add_values<false>(vbuf, s[0]);
+    }
     wait_lds();
-    if (more) load_tile(1);
-    valid = valid_next;
-  }
+    valid = at.valid;
+    if (more) {
+      load_values();
+      find_rows(t + 2);
+    }
+  };
+  int t = 0;
+  for (; t < nf; ++t) tile(t, No{});
+  for (; t < nt; ++t) tile(t, Yes{});
 
   // the waves' outputs meet: weights to their common maximum, then block db of
   // the output is summed and stored by wave db % NW
@@ -608,17 +656,17 @@ __global__ __launch_bounds__(NW * 64, 1) void attend_narrow_kernel(AttendParams 
 // More rows: four waves of 32 rows share tiles of KT keys, double buffered; a
 // wave fetches a quarter of each tile's rows.
 template <typename Elem, int DP, int KT>
-__global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p) {
+__global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWaves)) void attend_wide_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
   constexpr int NS = KT / kBlock;
   constexpr int kTile = KT * R::kBytes;
-  constexpr int kMine = KT / 4;                       // rows a wave fetches of K, and of V
+  constexpr int kMine = KT / 4;  // rows a wave fetches of K, and of V
   constexpr int NL = kMine * R::kBytes / 1024;
   static_assert(kMine % R::kPerLoad == 0 && NL >= 1, "");
   __shared__ __attribute__((aligned(1024))) char s_kv[2][2 * kTile];
   __shared__ __attribute__((aligned(16))) const char* s_row[4][64];
   __shared__ int s_id[4][2][64];
-  __shared__ uint32_t s_valid[2][4];
+  __shared__ uint32_t s_valid[4][4];
   warm_args(p);
   const Work w = work_of<4 * kBlock>(p);
   if (w.none) return;
@@ -627,80 +675,100 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p
   rb.init(p, w, w.row0 + wave * kBlock);
   const bool idle = w.row0 + wave * kBlock >= w.rows;  // a wave without rows only fetches
   const int lane = rb.lane;
-  const float c = p.scale * kLog2e;
-  const int nt = w.k1 > w.k0 ? (w.k1 - w.k0 + KT - 1) / KT : 0;
+  const float c = p.scale == 0.f ? 1.0f : fabsf(p.scale) * kLog2e;
+  const int keys = w.k1 - w.k0, inside = min(w.ctx, w.k1) - w.k0;
+  const int nt = keys > 0 ? (keys + KT - 1) / KT : 0, nf = inside > 0 ? inside / KT : 0;
   const int pieces_d = p.d * (int)sizeof(Elem) / 16;
+  const char* zeros = reinterpret_cast<const char*>(g_zero_row);
   const int my = lane % kMine, my_v = (lane / kMine) & 1;
 
+  auto my_pos = [&](int t) { return (int64_t)w.k0 + (int64_t)t * KT + wave * kMine + my; };
   auto fetch_ids = [&](int t) {
-    word_to_lds(entry_of(p, w.b, page_at(p, (int64_t)w.k0 + (int64_t)t * KT + wave * kMine + my, w.k1)),
-                (uint32_t)(uintptr_t)s_id[wave][t & 1]);
+    word_to_lds(entry_of(p, w.b, page_at(p, my_pos(t), w.k1)), (uint32_t)(uintptr_t)s_id[wave][t & 1]);
   };
-  auto load_tile = [&](int t) {
-    const int64_t pos = (int64_t)w.k0 + (int64_t)t * KT + wave * kMine + my;
+  TileRows<NL> at;
+  auto find_rows = [&](int t) {
+    const int64_t pos = my_pos(t);
     const PageAt a = page_at(p, pos, w.k1);
     const int id = s_id[wave][t & 1][lane];
     const bool valid = pos < w.k1 && a.in_table && id >= 0 && id < p.cache.n_pages;
     s_row[wave][lane] = row_of<Elem>(p, w.h, a, id, my_v, valid);
     const uint32_t got = (uint32_t)__ballot(valid) & (uint32_t)((1ull << kMine) - 1);
-    if (lane == 0) s_valid[t & 1][wave] = got;
+    if (lane == 0) s_valid[t & 3][wave] = got;
 #pragma unroll
-    for (int is_v = 0; is_v < 2; ++is_v)
+    for (int i = 0; i < NL; ++i) {
+      const int r = i * R::kPerLoad + lane / R::kPieces;
+      const int piece = (lane % R::kPieces) ^ R::swz(wave * kMine + r);
+      const bool in = piece < pieces_d;
+      const char *kr = s_row[wave][r], *vr = s_row[wave][kMine + r];
+      at.k[i] = (in ? kr : zeros) + 16 * piece;
+      at.v[i] = (in ? vr : zeros) + 16 * piece;
+    }
+  };
+  auto load_tile = [&](int t) {
+    const uint32_t to = (uint32_t)(uintptr_t)s_kv[t & 1] + wave * kMine * R::kBytes;
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int r = i * R::kPerLoad + lane / R::kPieces;
-        const int piece = (lane % R::kPieces) ^ R::swz(wave * kMine + r);
-        const char* at = s_row[wave][kMine * is_v + r] + 16 * piece;
-        row_to_lds(piece < pieces_d ? at : reinterpret_cast<const char*>(g_zero_row),
-                   (uint32_t)(uintptr_t)s_kv[t & 1] + is_v * kTile + wave * kMine * R::kBytes + 1024 * i);
-      }
+    for (int i = 0; i < NL; ++i) row_to_lds(at.k[i], to + 1024 * i);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) row_to_lds(at.v[i], to + kTile + 1024 * i);
   };
 
   if (nt > 0) {
     fetch_ids(0);
-    wait_loads<0>();
-    load_tile(0);
     fetch_ids(1);
+    wait_loads<0>();
+    find_rows(0);
+    load_tile(0);
+    fetch_ids(2);
+    find_rows(1);
   }
-  for (int t = 0; t < nt; ++t) {
-    wait_loads<0>();  // this wave's part of tile t, and its ids of t + 1
+  auto tile = [&](int t, auto tail) __attribute__((always_inline)) {
+    constexpr bool kTail = decltype(tail)::value;
+    wait_loads<0>();  // this wave's part of tile t, and its page numbers of t + 2
     lds_barrier();    // everyone's, and everyone is done with tile t - 1
-    if (t + 1 < nt) {
+    const bool more = t + 1 < nt;
+    if (more) {
       load_tile(t + 1);
-      fetch_ids(t + 2);
+      fetch_ids(t + 3);
     }
-    if (idle) continue;
-    const char* kb = s_kv[t & 1];
-    const char* vb = kb + kTile;
-    const int first = w.k0 + t * KT;
-    f32x16 s[NS];
-    uint32_t seen[NS];
-    bool uneven = false;
+    if (!idle) {
+      const char* kb = s_kv[t & 1];
+      const char* vb = kb + kTile;
+      f32x16 s[NS];
+      uint32_t seen[NS];
+      bool uneven = false;
 #pragma unroll
-    for (int b = 0; b < NS; ++b) {
-      s[b] = rb.scores(kb + b * kBlock * R::kBytes);
-      uint32_t valid = 0;
+      for (int b = 0; b < NS; ++b) {
+        s[b] = rb.scores(kb + b * kBlock * R::kBytes);
+        uint32_t valid = 0;
 #pragma unroll
-      for (int i = 0; i < 4 / NS; ++i) valid |= s_valid[t & 1][b * (4 / NS) + i] << (i * kMine);
-      seen[b] = valid & (first + b * kBlock + kBlock <= w.ctx ? ~0u : rb.sees(p, w, first + b * kBlock));
+        for (int i = 0; i < 4 / NS; ++i) valid |= s_valid[t & 3][b * (4 / NS) + i] << (i * kMine);
+        seen[b] = valid;
+        if constexpr (kTail) {
+          seen[b] &= rb.sees(p, w, w.k0 + t * KT + b * kBlock);
+          uneven |= __any(seen[b] != valid);
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[b][i] *= c;
-      if (__any(seen[b] != ~0u)) {
-        const uint32_t sb = seen[b] >> (4 * rb.hi);
+      for (int b = 0; b < NS; ++b)
+        if (__any(seen[b] != ~0u)) rb.mask_scores(s[b], seen[b]);
+      rb.weigh(s, c);
+      if (kTail && uneven && rb.any_odd(vb, KT)) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[b][i] = (sb >> (8 * (i >> 2) + (i & 3))) & 1 ? s[b][i] : -INFINITY;
-        uneven |= __any(seen[b] != valid);
+        for (int b = 0; b < NS; ++b) {
+          rb.template add_values<kTail>(vb + b * kBlock * R::kBytes, s[b]);
+          rb.add_odd(vb + b * kBlock * R::kBytes, seen[b]);
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < NS; ++b) rb.template add_values<false>(vb + b * kBlock * R::kBytes, s[b]);
       }
     }
-    rb.weigh(s);
-    if (uneven && rb.any_odd(vb, KT)) {
-#pragma unroll
-      for (int b = 0; b < NS; ++b) rb.template add_values<true>(vb + b * kBlock * R::kBytes, s[b], seen[b]);
-    } else {
-#pragma unroll
-      for (int b = 0; b < NS; ++b) rb.template add_values<false>(vb + b * kBlock * R::kBytes, s[b], seen[b]);
-    }
-  }
+    if (more) find_rows(t + 2);
+  };
+  int t = 0;
+  for (; t < nf; ++t) tile(t, No{});
+  for (; t < nt; ++t) tile(t, Yes{});
 
   if (rb.row < 0) return;
   const float l = half_sum(rb.l);
