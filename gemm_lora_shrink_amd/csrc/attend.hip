@@ -33,6 +33,9 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) const float lds_float;
+typedef __attribute__((address_space(3))) char lds_byte;
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 32;  // rows and keys of a matrix block
@@ -81,9 +84,9 @@ template <typename Elem, int DP> struct Rows {
   static constexpr int kSteps = kBytes / 32;       // 16-byte operands of a lane and half
   static constexpr int kDB = DP / kBlock;          // blocks of the output
   static constexpr int kPerLoad = 1024 / kBytes;   // rows of one 64-lane load
-  // waves of a SIMD that the kernels are compiled for: two workgroups a compute
-  // unit where LDS and registers have room for them
-  static constexpr int kWaves = kBytes <= 256 ? 2 : 1;
+  // waves of a SIMD that the kernels are compiled for
+  static constexpr int kNarrowWaves = kBytes <= 128 ? 2 : 1;
+  static constexpr int kWideWaves = kBytes <= 256 ? 2 : 1;
   static_assert(kBytes >= 128 && kBytes <= 1024, "");
   // position of piece c of row r: c ^ swz(r)
   __device__ static inline int swz(int r) {
@@ -94,22 +97,30 @@ template <typename Elem, int DP> struct Rows {
 };
 
 // Global-to-LDS loads with 64-bit addresses: lane l's 16 (or 4) bytes land at
-// LDS byte lds + 16 l (4 l).  Issued by hand for the reason given at the
-// shrink's: the compiler would wait for every load in flight before each LDS
-// read.  lds is wave-uniform.
-__device__ inline void row_to_lds(const char* g, uint32_t lds) {
+// LDS byte lds + 16 l (4 l); load i of a call 1 KB further.  Issued by hand for
+// the reason given at the shrink's: the compiler would wait for every load in
+// flight before each LDS read.  lds is wave-uniform.  ONCE: a non-temporal hint,
+// for rows that no other workgroup reads.
+#define LORA_LOAD_ROWS(NT)                                                                                      \
+  asm volatile(                                                                                                 \
+      "s_mov_b32 %0, m0\n\t"                                                                                    \
+      "s_mov_b32 m0, %1\n\t"                                                                                    \
+      "s_nop 0\n\t"                                                                                             \
+      "global_load_lds_dwordx4 %2, off" NT "\n\t"                                                               \
+      "s_add_u32 m0, m0, 0x400\n\t"                                                                             \
+      "s_nop 0\n\t"                                                                                             \
+      "global_load_lds_dwordx4 %3, off" NT "\n\t"                                                               \
+      "s_mov_b32 m0, %0"                                                                                        \
+      : "=&s"(saved)                                                                                            \
+      : "s"(lds), "v"(a), "v"(b)                                                                                \
+      : "memory", "scc")
+template <bool ONCE> __device__ inline void two_rows_to_lds(const char* a, const char* b, uint32_t lds) {
   lds = __builtin_amdgcn_readfirstlane(lds);
   uint32_t saved;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %1\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %2, off\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(saved)
-      : "s"(lds), "v"(g)
-      : "memory");
+  if constexpr (ONCE) LORA_LOAD_ROWS(" nt");
+  else LORA_LOAD_ROWS("");
 }
+#undef LORA_LOAD_ROWS
 __device__ inline void word_to_lds(const char* g, uint32_t lds) {
   lds = __builtin_amdgcn_readfirstlane(lds);
   uint32_t saved;
@@ -206,6 +217,41 @@ template <typename Elem, int DP> struct RowBlock {
   int64_t row;         // of q and out, -1: none
   int head;
   uint64_t bits0;      // first word of the mask row
+  // LDS addresses of this lane's operands in a tile: piece 2 st + hi of key row
+  // r32 for the scores; for the values the rows and pieces described at
+  // add_values.  What differs from these by a constant is an offset of the read.
+  static constexpr int kKeyAt = R::kSteps < 8 ? R::kSteps : 8;
+  static constexpr int kValueAt = R::k16 ? (R::kDB < 4 ? R::kDB : 4) : 0;
+  uint32_t key_at[kKeyAt];
+  uint32_t value_a[R::k16 ? kValueAt : 1], value_b[R::k16 ? kValueAt : 1];
+
+  // Tiles of keys and values start at these LDS addresses.
+  __device__ __forceinline__ void place(uint32_t keys, uint32_t values) {
+#pragma unroll
+    for (int st = 0; st < kKeyAt; ++st) key_at[st] = keys + r32 * R::kBytes + (((2 * st) ^ R::swz(r32) ^ hi) << 4);
+    if constexpr (R::k16) {
+      const int j = lane & 15, g1 = (lane >> 4) & 1;
+      const int ra = 4 * hi + (j >> 2), rb = ra + 8;
+      const int c = 2 * g1 + ((j & 3) >> 1), tail = (j & 1) * 8;
+#pragma unroll
+      for (int db = 0; db < kValueAt; ++db) {
+        value_a[db] = values + ra * R::kBytes + tail + ((c ^ R::swz(ra) ^ (4 * db)) << 4);
+        value_b[db] = values + rb * R::kBytes + tail + ((c ^ R::swz(rb) ^ (4 * db)) << 4);
+      }
+    } else {
+      value_a[0] = values;
+    }
+  }
+  // The other of two tiles 2^k bytes apart.
+  __device__ __forceinline__ void other_tile(uint32_t apart) {
+#pragma unroll
+    for (int st = 0; st < kKeyAt; ++st) key_at[st] ^= apart;
+#pragma unroll
+    for (int db = 0; db < (R::k16 ? kValueAt : 1); ++db) {
+      value_a[db] ^= apart;
+      if (R::k16) value_b[db] ^= apart;
+    }
+  }
 
   __device__ __forceinline__ void init(const AttendParams& p, const Work& w, int row_first) {
     lane = threadIdx.x & 63;
@@ -257,23 +303,20 @@ template <typename Elem, int DP> struct RowBlock {
     return (uint32_t)x;
   }
 
-  // Scores of 32 keys whose rows start at LDS pointer kb.  The keys' operands are
-  // requested eight at a time ahead of their products.
-  __device__ __forceinline__ f32x16 scores(const char* kb) const {
+  // Scores of the 32 keys from row kFirst of the tile on.  The keys' operands
+  // are requested eight at a time ahead of their products.
+  template <int kFirst> __device__ __forceinline__ f32x16 scores() const {
     f32x16 s;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = 0.f;
-    const char* base = kb + r32 * R::kBytes;
-    const int x = R::swz(r32) ^ hi;
-    constexpr int kAhead = R::kSteps < 8 ? R::kSteps : 8;
 #pragma unroll
-    for (int s0 = 0; s0 < R::kSteps; s0 += kAhead) {
-      u32x4 a[kAhead];
+    for (int s0 = 0; s0 < R::kSteps; s0 += kKeyAt) {
+      u32x4 a[kKeyAt];
 #pragma unroll
-      for (int st = 0; st < kAhead; ++st)
-        a[st] = *reinterpret_cast<const u32x4*>(base + (((2 * (s0 + st)) ^ x) << 4));
+      for (int st = 0; st < kKeyAt; ++st)
+        a[st] = *((lds_u32x4*)(lds_byte*)(uintptr_t)key_at[st] + (kFirst * R::kBytes + 32 * s0) / 16);
 #pragma unroll
-      for (int st = 0; st < kAhead; ++st) s = Mma32<Elem>::mma(a[st], q[s0 + st], s);
+      for (int st = 0; st < kKeyAt; ++st) s = Mma32<Elem>::mma(a[st], q[s0 + st], s);
     }
     return s;
   }
@@ -320,26 +363,25 @@ template <typename Elem, int DP> struct RowBlock {
     for (int i = 0; i < 16; ++i) s[i] = (sb >> (8 * (i >> 2) + (i & 3))) & 1 ? s[i] : -INFINITY;
   }
 
-  // o += V^T P^T over 32 keys whose value rows start at LDS pointer vb.  ODD: what
-  // is no finite number enters as 0 (see add_odd).
-  template <bool ODD> __device__ __forceinline__ void add_values(const char* vb, const f32x16& s) {
+  // o += V^T P^T over the 32 keys from row kFirst of the tile on.  ODD: what is no
+  // finite number enters as 0 (see add_odd).
+  // 16-bit: for step u the contraction runs over keys 16 u + 4 hi + (0..3) and
+  // 16 u + 8 + 4 hi + (0..3), as the weights lie in registers; a transposing read
+  // gives a lane 4 keys of one element, its 16 lanes reading 4 rows of 32 bytes.
+  template <bool ODD, int kFirst> __device__ __forceinline__ void add_values(const f32x16& s) {
     if constexpr (R::k16) {
-      const int j = lane & 15, g1 = (lane >> 4) & 1;
-      const int ra = 4 * hi + (j >> 2), rb = ra + 8;
-      const int c = 2 * g1 + ((j & 3) >> 1), tail = (j & 1) * 8;
-      const int xa = c ^ R::swz(ra), xb = c ^ R::swz(rb);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         u32x4 w;
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = Mma32<Elem>::pack2(s[8 * u + 2 * e], s[8 * u + 2 * e + 1]);
-        const char* pa = vb + (16 * u + ra) * R::kBytes + tail;
-        const char* pb = vb + (16 * u + rb) * R::kBytes + tail;
         s16x4 va[R::kDB], vc[R::kDB];
 #pragma unroll
         for (int db = 0; db < R::kDB; ++db) {
-          va[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(pa + (((4 * db) ^ xa) << 4)));
-          vc[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(pb + (((4 * db) ^ xb) << 4)));
+          // blocks past the fourth lie 256 bytes (the swizzle's range) further
+          const int off = ((kFirst + 16 * u) * R::kBytes + (db / 4) * 256) / 8;
+          va[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)(uintptr_t)value_a[db % 4] + off);
+          vc[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)(uintptr_t)value_b[db % 4] + off);
         }
 #pragma unroll
         for (int db = 0; db < R::kDB; ++db) {
@@ -356,7 +398,7 @@ template <typename Elem, int DP> struct RowBlock {
       }
     } else {
       const int c = (r32 >> 2) ^ (hi << 3);
-      const char* pr = vb + 4 * hi * R::kBytes + (r32 & 3) * 4;
+      const lds_byte* pr = (lds_byte*)(uintptr_t)(value_a[0] + 4 * hi * R::kBytes + (r32 & 3) * 4);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int key = 8 * (i >> 2) + (i & 3);  // + 4 hi
@@ -364,7 +406,7 @@ template <typename Elem, int DP> struct RowBlock {
         float v[R::kDB];
 #pragma unroll
         for (int db = 0; db < R::kDB; ++db) {
-          v[db] = *reinterpret_cast<const float*>(pr + key * R::kBytes + (((8 * db) ^ c ^ x) << 4));
+          v[db] = *(lds_float*)(pr + ((((8 * db) & 8) ^ c ^ x) << 4) + (kFirst + key) * R::kBytes + (db / 2) * 256);
           if (ODD && (__float_as_uint(v[db]) & Mma32<Elem>::kExp) == Mma32<Elem>::kExp) v[db] = 0.f;
         }
 #pragma unroll
@@ -455,38 +497,62 @@ __device__ inline float* part_ml(const AttendParams& p, int split, int64_t row, 
   return p.part + (int64_t)p.splits * p.T * p.hq * p.d + (((int64_t)split * p.T + row) * p.hq + head) * 2;
 }
 
-// Where the rows of a tile's keys lie: lane's key at position pos.
+// Where a lane's key lies: its page's number comes from the table by way of LDS.
 struct PageAt {
-  int pos, col;
-  bool in_table;
+  int place;      // row in the page
+  bool in_table;  // a key of the chunk whose page the table has
 };
-__device__ inline PageAt page_at(const AttendParams& p, int64_t pos, int end) {
+__device__ inline PageAt page_at(const AttendParams& p, int64_t pos, int end, int& col) {
   PageAt a;
-  a.pos = (int)min(pos, (int64_t)end);
-  a.col = (int)p.cache.page.div((uint32_t)a.pos);
-  a.in_table = a.col < p.n_table;
+  const uint32_t at = (uint32_t)min(pos, (int64_t)end);
+  col = (int)p.cache.page.div(at);
+  a.place = (int)(at - (uint32_t)col * p.cache.page.d);
+  a.in_table = pos < end && col < p.n_table;
   return a;
 }
-__device__ inline const char* entry_of(const AttendParams& p, int b, const PageAt& a) {
-  return a.in_table ? reinterpret_cast<const char*>(p.page_table + b * p.ld_table + a.col)
+__device__ inline const char* entry_of(const AttendParams& p, int b, const PageAt& a, int col) {
+  return a.in_table ? reinterpret_cast<const char*>(p.page_table + b * p.ld_table + col)
                     : reinterpret_cast<const char*>(g_zero_row);
 }
-template <typename Elem>
-__device__ inline const char* row_of(const AttendParams& p, int h, const PageAt& a, int id, bool is_v, bool valid) {
+// One of the cache's two tensors, at the call's head; strides in bytes below
+// 2^32 (the host checks), so a row's address is two 32 x 32 + 64-bit products.
+struct HeadAt {
+  uint64_t base;
+  uint32_t page, row;
+  __device__ __forceinline__ uint64_t row_at(uint32_t id, int place) const {
+    return base + (uint64_t)id * page + (uint64_t)(uint32_t)place * row;
+  }
+};
+template <typename Elem> __device__ inline HeadAt head_at(const AttendParams& p, int h, bool is_v) {
   const CacheView& c = p.cache;
-  const int64_t place = a.pos - a.col * (int)c.page.d;
-  const int64_t off = (int64_t)id * (is_v ? c.v_page : c.k_page) + (int64_t)h * (is_v ? c.v_head : c.k_head) +
-                      place * (is_v ? c.v_row : c.k_row);
-  const char* at = static_cast<const char*>(is_v ? c.v : c.k) + off * (int64_t)sizeof(Elem);
-  return valid ? at : reinterpret_cast<const char*>(g_zero_row);
+  HeadAt a;
+  a.base = reinterpret_cast<uint64_t>(is_v ? c.v : c.k) + (uint64_t)(h * (is_v ? c.v_head : c.k_head)) * sizeof(Elem);
+  a.page = (uint32_t)((is_v ? c.v_page : c.k_page) * (int64_t)sizeof(Elem));
+  a.row = (uint32_t)((is_v ? c.v_row : c.k_row) * (int64_t)sizeof(Elem));
+  return a;
 }
 
-// The global addresses that this lane loads for a tile, found one tile ahead:
-// loads of a row's 16-byte pieces, NL of the keys and NL of the values.
-template <int NL> struct TileRows {
-  const char *k[NL], *v[NL];
+// The global addresses that this lane loads for a tile, found one tile ahead
+// (NL loads of the keys and of the values), where the registers have room for
+// them; else they are read from the rows' addresses in LDS for each load.
+template <typename Elem, int DP, int NL, bool HELD> struct TileRows {
+  using R = Rows<Elem, DP>;
+  static constexpr bool kHeld = HELD;
+  const char *k[kHeld ? NL : 1], *v[kHeld ? NL : 1];
   uint32_t valid;  // rows that are keys
 };
+// Address of the 16-byte piece that this lane brings in load i: the rows'
+// addresses are in LDS at `rows`, row_0 is the tile's row of the first of them.
+template <typename Elem, int DP>
+__device__ __forceinline__ const char* piece_of(const AttendParams& p, const char* const* rows, int row_0, int i,
+                                                int lane) {
+  using R = Rows<Elem, DP>;
+  const int r = i * R::kPerLoad + lane / R::kPieces;
+  const int piece = (lane % R::kPieces) ^ R::swz(row_0 + r);
+  const char* at = rows[r];
+  if (p.d != DP && piece * 16 >= p.d * (int)sizeof(Elem)) at = reinterpret_cast<const char*>(g_zero_row);
+  return at + 16 * piece;
+}
 
 // Up to 32 rows: the NW waves of the workgroup hold the same rows and take the
 // chunk's blocks of 32 keys in turn, each through LDS of its own, so no wave
@@ -495,7 +561,7 @@ template <int NL> struct TileRows {
 // during the next scores; page numbers come through LDS three blocks ahead,
 // addresses are found two blocks ahead.
 template <typename Elem, int DP, int NW>
-__global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kWaves)) void attend_narrow_kernel(AttendParams p) {
+__global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void attend_narrow_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
   constexpr int kTile = kBlock * R::kBytes;
   constexpr int NL = kTile / 1024;  // loads of a tile of keys or values
@@ -519,80 +585,82 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kWaves)) void attend_narr
     return blocks > wave ? (blocks - wave + NW - 1) / NW : 0;
   };
   const int nt = tiles(w.k1 - w.k0, false), nf = tiles(min(w.ctx, w.k1) - w.k0, true);
-  const int pieces_d = p.d * (int)sizeof(Elem) / 16;
-  const char* zeros = reinterpret_cast<const char*>(g_zero_row);
 
   auto first_key = [&](int t) { return (int64_t)w.k0 + ((int64_t)wave + (int64_t)NW * t) * kBlock; };
-  auto fetch_ids = [&](int t) {
-    word_to_lds(entry_of(p, w.b, page_at(p, first_key(t) + rb.r32, w.k1)), (uint32_t)(uintptr_t)s_id[wave][t & 1]);
+  const HeadAt hk = head_at<Elem>(p, w.h, false), hv = head_at<Elem>(p, w.h, true);
+  PageAt ahead[2];
+  auto fetch_ids = [&](int t, PageAt& a) {
+    int col;
+    a = page_at(p, first_key(t) + rb.r32, w.k1, col);
+    word_to_lds(entry_of(p, w.b, a, col), (uint32_t)(uintptr_t)s_id[wave][t & 1]);
   };
-  TileRows<NL> at;
-  auto find_rows = [&](int t) {  // lanes 0..31 the keys' rows, 32..63 the values'
-    const int64_t pos = first_key(t) + rb.r32;
-    const PageAt a = page_at(p, pos, w.k1);
-    const int id = s_id[wave][t & 1][lane];
-    const bool valid = pos < w.k1 && a.in_table && id >= 0 && id < p.cache.n_pages;
-    s_row[wave][lane] = row_of<Elem>(p, w.h, a, id, rb.hi, valid);
+  TileRows<Elem, DP, NL, (NL <= 8)> at;
+  auto find_rows = [&](int t, const PageAt& a) {  // half of the lanes the keys' rows, half the values'
+    const uint32_t id = (uint32_t)s_id[wave][t & 1][lane];
+    const bool valid = a.in_table && id < (uint64_t)p.cache.n_pages && (int)id >= 0;
+    const uint64_t row = (rb.hi ? hv : hk).row_at(id, a.place);
+    s_row[wave][lane] = valid ? reinterpret_cast<const char*>(row) : reinterpret_cast<const char*>(g_zero_row);
     at.valid = (uint32_t)__ballot(valid);
+    if constexpr (at.kHeld) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int row = i * R::kPerLoad + lane / R::kPieces;
-      const int piece = (lane % R::kPieces) ^ R::swz(row);
-      const bool in = piece < pieces_d;
-      const char *kr = s_row[wave][row], *vr = s_row[wave][32 + row];
-      at.k[i] = (in ? kr : zeros) + 16 * piece;
-      at.v[i] = (in ? vr : zeros) + 16 * piece;
+      for (int i = 0; i < NL; ++i) {
+        at.k[i] = piece_of<Elem, DP>(p, s_row[wave], 0, i, lane);
+        at.v[i] = piece_of<Elem, DP>(p, s_row[wave] + 32, 0, i, lane);
+      }
     }
   };
-  auto load_keys = [&]() {
+  auto load = [&](const char* const* held, const char* const* rows, uint32_t lds) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) row_to_lds(at.k[i], k_lds + 1024 * i);
-  };
-  auto load_values = [&]() {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) row_to_lds(at.v[i], v_lds + 1024 * i);
+    for (int i = 0; i < NL; i += 2) {
+      const char* a = at.kHeld ? held[at.kHeld ? i : 0] : piece_of<Elem, DP>(p, rows, 0, i, lane);
+      const char* b = at.kHeld ? held[at.kHeld ? i + 1 : 0] : piece_of<Elem, DP>(p, rows, 0, i + 1, lane);
+      two_rows_to_lds<true>(a, b, lds + 1024 * i);
+    }
   };
 
   uint32_t valid = 0;
   if (nt > 0) {
-    fetch_ids(0);
-    fetch_ids(1);
+    fetch_ids(0, ahead[0]);
+    fetch_ids(1, ahead[1]);
     wait_loads<0>();
-    find_rows(0);
+    find_rows(0, ahead[0]);
     valid = at.valid;
-    load_keys();
-    fetch_ids(2);
-    load_values();
-    find_rows(1);
+    load(at.k, s_row[wave], k_lds);
+    fetch_ids(2, ahead[0]);
+    load(at.v, s_row[wave] + 32, v_lds);
+    find_rows(1, ahead[1]);
   }
   auto tile = [&](int t, auto tail) __attribute__((always_inline)) {
+    constexpr bool kTail = decltype(tail)::value;
     const bool more = t + 1 < nt;
     wait_loads<NL>();  // keys of t and page numbers of t + 2 are there
-    f32x16 s[1] = {rb.scores(kbuf)};
+    f32x16 s[1] = {rb.template scores<0>()};
     wait_lds();
     if (more) {
-      load_keys();
-      fetch_ids(t + 3);
+      load(at.k, s_row[wave], k_lds);
+      fetch_ids(t + 3, ahead[1]);
     }
     uint32_t seen = valid;
-    if constexpr (decltype(tail)::value) seen &= rb.sees(p, w, (int)first_key(t));
+    if constexpr (kTail) seen &= rb.sees(p, w, (int)first_key(t));
     if (__any(seen != ~0u)) rb.mask_scores(s[0], seen);
     rb.weigh(s, c);
     if (more) wait_loads<NL + 1>();
     else wait_loads<0>();
-    if (decltype(tail)::value && __any(seen != valid) && rb.any_odd(vbuf, kBlock)) {
-      rb.template add_values<decltype(tail)::value>(vbuf, s[0]);
+    if (kTail && __any(seen != valid) && rb.any_odd(vbuf, kBlock)) {
+      rb.template add_values<kTail, 0>(s[0]);
       rb.add_odd(vbuf, seen);
     } else {
-      rb.template add_values<false>(vbuf, s[0]);
+      rb.template add_values<false, 0>(s[0]);
     }
     wait_lds();
     valid = at.valid;
     if (more) {
-      load_values();
-      find_rows(t + 2);
+      load(at.v, s_row[wave] + 32, v_lds);
+      find_rows(t + 2, ahead[0]);
+      ahead[0] = ahead[1];
     }
   };
+  rb.place(k_lds, v_lds);
   int t = 0;
   for (; t < nf; ++t) tile(t, No{});
   for (; t < nt; ++t) tile(t, Yes{});
@@ -656,14 +724,15 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kWaves)) void attend_narr
 // More rows: four waves of 32 rows share tiles of KT keys, double buffered; a
 // wave fetches a quarter of each tile's rows.
 template <typename Elem, int DP, int KT>
-__global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWaves)) void attend_wide_kernel(AttendParams p) {
+__global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWideWaves)) void attend_wide_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
   constexpr int NS = KT / kBlock;
   constexpr int kTile = KT * R::kBytes;
   constexpr int kMine = KT / 4;  // rows a wave fetches of K, and of V
   constexpr int NL = kMine * R::kBytes / 1024;
   static_assert(kMine % R::kPerLoad == 0 && NL >= 1, "");
-  __shared__ __attribute__((aligned(1024))) char s_kv[2][2 * kTile];
+  // (a multiple of its two tiles' distance, so that an XOR changes tiles)
+  __shared__ __attribute__((aligned(4 * kTile))) char s_kv[2][2 * kTile];
   __shared__ __attribute__((aligned(16))) const char* s_row[4][64];
   __shared__ int s_id[4][2][64];
   __shared__ uint32_t s_valid[4][4];
@@ -678,49 +747,45 @@ __global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWaves)) void attend_wid
   const float c = p.scale == 0.f ? 1.0f : fabsf(p.scale) * kLog2e;
   const int keys = w.k1 - w.k0, inside = min(w.ctx, w.k1) - w.k0;
   const int nt = keys > 0 ? (keys + KT - 1) / KT : 0, nf = inside > 0 ? inside / KT : 0;
-  const int pieces_d = p.d * (int)sizeof(Elem) / 16;
-  const char* zeros = reinterpret_cast<const char*>(g_zero_row);
   const int my = lane % kMine, my_v = (lane / kMine) & 1;
 
-  auto my_pos = [&](int t) { return (int64_t)w.k0 + (int64_t)t * KT + wave * kMine + my; };
-  auto fetch_ids = [&](int t) {
-    word_to_lds(entry_of(p, w.b, page_at(p, my_pos(t), w.k1)), (uint32_t)(uintptr_t)s_id[wave][t & 1]);
+  const HeadAt hk = head_at<Elem>(p, w.h, false), hv = head_at<Elem>(p, w.h, true);
+  PageAt ahead[2];
+  auto fetch_ids = [&](int t, PageAt& a) {
+    int col;
+    a = page_at(p, (int64_t)w.k0 + (int64_t)t * KT + wave * kMine + my, w.k1, col);
+    word_to_lds(entry_of(p, w.b, a, col), (uint32_t)(uintptr_t)s_id[wave][t & 1]);
   };
-  TileRows<NL> at;
-  auto find_rows = [&](int t) {
-    const int64_t pos = my_pos(t);
-    const PageAt a = page_at(p, pos, w.k1);
-    const int id = s_id[wave][t & 1][lane];
-    const bool valid = pos < w.k1 && a.in_table && id >= 0 && id < p.cache.n_pages;
-    s_row[wave][lane] = row_of<Elem>(p, w.h, a, id, my_v, valid);
+  auto find_rows = [&](int t, const PageAt& a) {
+    const uint32_t id = (uint32_t)s_id[wave][t & 1][lane];
+    const bool valid = a.in_table && id < (uint64_t)p.cache.n_pages && (int)id >= 0;
+    const uint64_t row = (my_v ? hv : hk).row_at(id, a.place);
+    s_row[wave][lane] = valid ? reinterpret_cast<const char*>(row) : reinterpret_cast<const char*>(g_zero_row);
     const uint32_t got = (uint32_t)__ballot(valid) & (uint32_t)((1ull << kMine) - 1);
     if (lane == 0) s_valid[t & 3][wave] = got;
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int r = i * R::kPerLoad + lane / R::kPieces;
-      const int piece = (lane % R::kPieces) ^ R::swz(wave * kMine + r);
-      const bool in = piece < pieces_d;
-      const char *kr = s_row[wave][r], *vr = s_row[wave][kMine + r];
-      at.k[i] = (in ? kr : zeros) + 16 * piece;
-      at.v[i] = (in ? vr : zeros) + 16 * piece;
-    }
   };
   auto load_tile = [&](int t) {
     const uint32_t to = (uint32_t)(uintptr_t)s_kv[t & 1] + wave * kMine * R::kBytes;
+    const char* a[2 * NL];
 #pragma unroll
-    for (int i = 0; i < NL; ++i) row_to_lds(at.k[i], to + 1024 * i);
+    for (int i = 0; i < NL; ++i) {
+      a[i] = piece_of<Elem, DP>(p, s_row[wave], wave * kMine, i, lane);
+      a[NL + i] = piece_of<Elem, DP>(p, s_row[wave] + kMine, wave * kMine, i, lane);
+    }
 #pragma unroll
-    for (int i = 0; i < NL; ++i) row_to_lds(at.v[i], to + kTile + 1024 * i);
+    for (int i = 0; i < NL; i += 2) two_rows_to_lds<false>(a[i], a[i + 1], to + 1024 * i);
+#pragma unroll
+    for (int i = 0; i < NL; i += 2) two_rows_to_lds<false>(a[NL + i], a[NL + i + 1], to + kTile + 1024 * i);
   };
 
   if (nt > 0) {
-    fetch_ids(0);
-    fetch_ids(1);
+    fetch_ids(0, ahead[0]);
+    fetch_ids(1, ahead[1]);
     wait_loads<0>();
-    find_rows(0);
+    find_rows(0, ahead[0]);
     load_tile(0);
-    fetch_ids(2);
-    find_rows(1);
+    fetch_ids(2, ahead[0]);
+    find_rows(1, ahead[1]);
   }
   auto tile = [&](int t, auto tail) __attribute__((always_inline)) {
     constexpr bool kTail = decltype(tail)::value;
@@ -729,43 +794,49 @@ __global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWaves)) void attend_wid
     const bool more = t + 1 < nt;
     if (more) {
       load_tile(t + 1);
-      fetch_ids(t + 3);
+      fetch_ids(t + 3, ahead[1]);
     }
     if (!idle) {
-      const char* kb = s_kv[t & 1];
-      const char* vb = kb + kTile;
       f32x16 s[NS];
-      uint32_t seen[NS];
+      uint32_t seen[NS], valid[NS];
+      s[0] = rb.template scores<0>();
+      if constexpr (NS == 2) s[1] = rb.template scores<kBlock>();
       bool uneven = false;
 #pragma unroll
       for (int b = 0; b < NS; ++b) {
-        s[b] = rb.scores(kb + b * kBlock * R::kBytes);
-        uint32_t valid = 0;
+        valid[b] = 0;
 #pragma unroll
-        for (int i = 0; i < 4 / NS; ++i) valid |= s_valid[t & 3][b * (4 / NS) + i] << (i * kMine);
-        seen[b] = valid;
+        for (int i = 0; i < 4 / NS; ++i) valid[b] |= s_valid[t & 3][b * (4 / NS) + i] << (i * kMine);
+        seen[b] = valid[b];
         if constexpr (kTail) {
           seen[b] &= rb.sees(p, w, w.k0 + t * KT + b * kBlock);
-          uneven |= __any(seen[b] != valid);
+          uneven |= __any(seen[b] != valid[b]);
         }
       }
 #pragma unroll
       for (int b = 0; b < NS; ++b)
         if (__any(seen[b] != ~0u)) rb.mask_scores(s[b], seen[b]);
       rb.weigh(s, c);
+      const char* vb = s_kv[t & 1] + kTile;
       if (kTail && uneven && rb.any_odd(vb, KT)) {
-#pragma unroll
-        for (int b = 0; b < NS; ++b) {
-          rb.template add_values<kTail>(vb + b * kBlock * R::kBytes, s[b]);
-          rb.add_odd(vb + b * kBlock * R::kBytes, seen[b]);
+        rb.template add_values<kTail, 0>(s[0]);
+        rb.add_odd(vb, seen[0]);
+        if constexpr (NS == 2) {
+          rb.template add_values<kTail, kBlock>(s[1]);
+          rb.add_odd(vb + kBlock * R::kBytes, seen[1]);
         }
       } else {
-#pragma unroll
-        for (int b = 0; b < NS; ++b) rb.template add_values<false>(vb + b * kBlock * R::kBytes, s[b]);
+        rb.template add_values<false, 0>(s[0]);
+        if constexpr (NS == 2) rb.template add_values<false, kBlock>(s[1]);
       }
     }
-    if (more) find_rows(t + 2);
+    rb.other_tile(2 * kTile);
+    if (more) {
+      find_rows(t + 2, ahead[0]);
+      ahead[0] = ahead[1];
+    }
   };
+  rb.place((uint32_t)(uintptr_t)s_kv[0], (uint32_t)(uintptr_t)s_kv[0] + kTile);
   int t = 0;
   for (; t < nf; ++t) tile(t, No{});
   for (; t < nt; ++t) tile(t, Yes{});

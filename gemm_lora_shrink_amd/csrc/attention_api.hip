@@ -335,6 +335,9 @@ LORA_EXPORT lora_status lora_tree_attention(lora_dtype dt, const void* q, int64_
   if (!context || !q_start) return fail(LORA_ERR_INVALID_ARG, "context or q_start is null");
   if (!cache) return fail(LORA_ERR_INVALID_ARG, "cache is null");
   if ((st = check_cache(dt, *cache)) != LORA_OK) return st;
+  const int64_t most = (((int64_t)1 << 32) - 1) / elem_bytes(dt);
+  if (cache->k_page > most || cache->v_page > most || cache->k_row > most || cache->v_row > most)
+    return fail(LORA_ERR_UNSUPPORTED, "a page or row of the cache spans 4 GiB");
   const int64_t width = (int64_t)q_heads * d;
   if ((st = check_rows(dt, "q", q, ldq, width)) != LORA_OK) return st;
   if ((st = check_rows(dt, "out", out, ldo, width)) != LORA_OK) return st;
