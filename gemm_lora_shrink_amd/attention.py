@@ -19,11 +19,11 @@ LoraError and every computation runs in the library's HIP kernels.
 """
 
 import ctypes
+import struct
 
 import torch
 
-from . import (LORA_ERR_INVALID_ARG, LORA_ERR_UNSUPPORTED, LoraError, _check, _check_tensor, _dtype_code, _load, _on_device,
-               _rows, _stream)
+from . import LORA_ERR_INVALID_ARG, LORA_ERR_UNSUPPORTED, LoraError, _check, _DTYPES, _load
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4}
@@ -34,12 +34,6 @@ MAX_KEEP_LAYERS = 128
 class _RopeConfig(ctypes.Structure):
     _fields_ = [("scaling", ctypes.c_int32), ("factor", ctypes.c_double), ("original_context", ctypes.c_double),
                 ("low", ctypes.c_double), ("high", ctypes.c_double), ("magnitude", ctypes.c_double)]
-
-
-class _KVCache(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_page", ctypes.c_int64), ("k_head", ctypes.c_int64),
-                ("k_row", ctypes.c_int64), ("v_page", ctypes.c_int64), ("v_head", ctypes.c_int64),
-                ("v_row", ctypes.c_int64), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32)]
 
 
 _bound = None
@@ -63,7 +57,7 @@ def _lib():
         lib.lora_tree_attention_workspace_bytes.restype = sz
         lib.lora_tree_attention.argtypes = [i32, vp, i64, i32, i32, i32, i32, i32, vp, vp, i64, i32, vp, vp, i32, i32, vp,
                                             i32, f32, vp, i64, vp, vp, sz, vp]
-        lib.lora_keep_path.argtypes = [i32, vp, i32, i32, i32, i32, vp, i64, i32, vp, vp, i64, i32, vp, vp]
+        lib.lora_keep_path.argtypes = [i32, vp, vp, vp, i32, i32, i32, i32, vp, i64, i32, vp, vp, i64, i32, vp, vp]
         for name in ("rope_frequencies", "rope_table", "rotary", "qk_norm_rotary", "build_tree", "tree_attention",
                      "keep_path"):
             getattr(lib, "lora_" + name).restype = ctypes.c_int
@@ -82,39 +76,73 @@ def _choice(table, name, what):
         raise _bad(f"unknown {what} {name!r}") from None
 
 
-def _ints(t, name, dev, numel):
-    """A contiguous int32 vector of `numel` entries on the call's GPU."""
-    if t.dtype != torch.int32 or t.numel() != numel or not t.is_contiguous() or not _on_device(t, dev):
-        raise _bad(f"{name} must be a contiguous int32 tensor of {numel} entries on {dev}")
+# The checks below run on every call of a decode step, where the host's time
+# counts: they ask each tensor once for its shape, strides, type and device
+# index (-1 on the host) and build no message unless they refuse.
+
+_I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
+
+
+def _gpu(t, name):
+    """The GPU index of the tensor that says where the call runs."""
+    dev = t.get_device()
+    if dev < 0:
+        raise _bad(f"{name} must be on a GPU (it is on {t.device})")
+    return dev
+
+
+def _stream_of(stream, dev):
+    """The stream's handle: `stream`, or the current one of GPU `dev`."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _matrix(t, name, dtype, dev):
+    """(rows, width, row stride) of a matrix with contiguous rows."""
+    shape = t.shape
+    if len(shape) != 2 or t.dtype is not dtype or t.get_device() != dev:
+        raise _bad(f"{name} must be a matrix of {dtype} on GPU {dev} (it is {t.dtype} of {tuple(shape)} on {t.device})")
+    rows, width = shape
+    ld, inner = t.stride()
+    if rows < 2 or width < 1:  # the stride of a single row is no one's
+        ld = max(ld, width, 1)
+    if inner != 1 and width > 1:
+        raise _bad(f"{name} must have contiguous rows")
+    return rows, width, ld
+
+
+def _vector(t, name, dtype, dev, numel):
+    """The address of a contiguous tensor of numel entries."""
+    if t.dtype is not dtype or t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
+        raise _bad(f"{name} must be contiguous, {numel} entries of {dtype} on GPU {dev}")
     return t.data_ptr()
 
 
 def _int_rows(t, name, dev, rows):
-    """(pointer, row stride, columns) of an int32 matrix with contiguous rows."""
-    if t.dtype != torch.int32 or t.dim() != 2 or t.size(0) != rows or not _on_device(t, dev) \
-            or (t.size(1) > 1 and t.stride(1) != 1):
-        raise _bad(f"{name} must be an int32 tensor of {rows} contiguous rows on {dev}")
-    cols = t.size(1)
-    return t.data_ptr(), max(t.stride(0), cols) if rows > 1 else cols, cols
+    """(address, row stride, columns) of an int32 matrix of `rows` rows."""
+    n, cols, ld = _matrix(t, name, _I32, dev)
+    if n != rows:
+        raise _bad(f"{name} must have {rows} rows (it has {n})")
+    return t.data_ptr(), ld if ld > cols else cols, cols
 
 
-def _cache(k, v, dtype, dev, heads, d):
-    """The C view of a cache; heads and d None: any."""
-    if k.dim() != 4 or v.shape != k.shape:
+_CACHE_FIELDS = struct.Struct("@PP7qi")  # lora_kv_cache
+
+
+def _cache(k, v, dtype, dev):
+    """(the C view of a cache, its shape)."""
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape:
         raise _bad("k_cache and v_cache must be [n_pages, kv_heads, page_size, head_dim] of one shape")
-    n_pages, h, page, width = k.shape
-    if (heads is not None and h != heads) or (d is not None and width != d):
-        raise _bad(f"the cache holds {h} heads of {width}, the call has {heads} of {d}")
-    ks, vs = k.stride(), v.stride()
-    if ks[3] != 1 or vs[3] != 1:
+    if k.dtype is not dtype or v.dtype is not dtype or k.get_device() != dev or v.get_device() != dev:
+        raise _bad(f"the cache must be {dtype} on GPU {dev}")
+    k_page, k_head, k_row, k_one = k.stride()
+    v_page, v_head, v_row, v_one = v.stride()
+    if k_one != 1 or v_one != 1:
         raise _bad("the cache's heads must be contiguous")
-    if k.dtype != dtype or v.dtype != dtype:
-        raise _bad(f"the cache must be {dtype}")
-    if not (_on_device(k, dev) and _on_device(v, dev)):
-        raise _bad(f"the cache must be on {dev}")
-    if page < 1:
+    if shape[2] < 1:
         raise _bad("the cache's pages hold no rows")
-    return _KVCache(k.data_ptr(), v.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], n_pages, page)
+    return _CACHE_FIELDS.pack(k.data_ptr(), v.data_ptr(), k_page, k_head, k_row, v_page, v_head, v_row, shape[0],
+                              shape[2]), shape
 
 
 # ---- rotary positions --------------------------------------------------------
@@ -155,68 +183,68 @@ def rope_table(n, rot_dim, *, base=10000.0, scaling=None, frequencies=None, magn
         out = torch.empty((n, rot_dim), dtype=torch.float32, device=device)
     if tuple(out.shape) != (n, rot_dim):
         raise _bad(f"out must be [{n}, {rot_dim}]")
-    if out.device.type != "cuda":
-        raise _bad(f"the table must be on a GPU (it is on {out.device})")
-    _check_tensor(out, "out", out.device, dtype=torch.float32)
+    dev = _gpu(out, "the table")
+    to = _vector(out, "out", _F32, dev, n * rot_dim)
     freq = (ctypes.c_double * (rot_dim // 2))(*frequencies)
-    _check(_lib().lora_rope_table(freq, rot_dim, magnitude, first, n, out.data_ptr(), _stream(stream, out.device)))
+    _check(_lib().lora_rope_table(freq, rot_dim, magnitude, first, n, to, _stream_of(stream, dev)))
     return out
 
 
 def _rotate(norm, q, k, positions, table, head_dim, layout, q_out, k_out, v, k_cache, v_cache, cache_rows, stream):
-    dev, dtype = q.device, q.dtype
-    if dev.type != "cuda":
-        raise _bad(f"q must be on a GPU (it is on {dev})")
+    dev, dtype = _gpu(q, "q"), q.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise _bad(f"unsupported dtype {dtype}")
     if head_dim < 1:
         raise _bad(f"head_dim = {head_dim} must be >= 1")
-    T, qw, ldq = _rows(q, "q")
+    T, qw, ldq = _matrix(q, "q", dtype, dev)
+    Tk, kw, ldk = _matrix(k, "k", dtype, dev)
+    q_heads, kv_heads = qw // head_dim, kw // head_dim
+    if q_heads * head_dim != qw or kv_heads * head_dim != kw or Tk != T:
+        raise _bad("q and k must be rows of whole heads, one row a token")
     if q_out is None:
-        q_out = q
-    _, qow, ldqo = _rows(q_out, "q_out")
-    Tk, kw, ldk = _rows(k, "k")
-    if qw % head_dim or kw % head_dim or q_out.shape != q.shape or Tk != T:
-        raise _bad("q, q_out and k must be rows of whole heads, one row a token")
-    hk = kw // head_dim
-    cached = k_cache is not None
-    if k_out is None and not cached:
-        k_out = k
-    ldko = ldk
-    if k_out is not None:
-        if k_out.shape != k.shape:
-            raise _bad("k_out must have k's shape")
-        ldko = _rows(k_out, "k_out")[2]
-    if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous() or not _on_device(table, dev):
-        raise _bad(f"table must be a contiguous float32 [positions, rot_dim] on {dev}")
-    for t, name in ((q_out, "q_out"), (k, "k"), (k_out, "k_out")):
-        if t is not None and (t.dtype != dtype or t.device != dev):
-            raise _bad(f"{name} must be {dtype} on {dev}, as q is")
-    cache = rows = None
-    ldv = 0
-    if cached:
+        q_out, ldqo = q, ldq
+    else:
+        To, wo, ldqo = _matrix(q_out, "q_out", dtype, dev)
+        if To != T or wo != qw:
+            raise _bad("q_out must have q's shape")
+    cache = rows = v_at = k_to = None
+    ldv, ldko = 0, ldk
+    if k_cache is not None:
         if v is None or v_cache is None or cache_rows is None:
             raise _bad("a cache takes v, k_cache, v_cache and cache_rows")
-        if v.shape != k.shape or v.dtype != dtype or v.device != dev:
-            raise _bad(f"v must have k's shape and be {dtype} on {dev}")
-        ldv = _rows(v, "v")[2]
-        cache = _cache(k_cache, v_cache, dtype, dev, hk, head_dim)
-        rows = _ints(cache_rows, "cache_rows", dev, T)
+        Tv, vw, ldv = _matrix(v, "v", dtype, dev)
+        if Tv != T or vw != kw:
+            raise _bad("v must have k's shape")
+        cache, shape = _cache(k_cache, v_cache, dtype, dev)
+        if shape[1] != kv_heads or shape[3] != head_dim:
+            raise _bad(f"the cache holds {shape[1]} heads of {shape[3]}, the call has {kv_heads} of {head_dim}")
+        rows, v_at = _vector(cache_rows, "cache_rows", _I32, dev, T), v.data_ptr()
     elif v is not None or v_cache is not None or cache_rows is not None:
         raise _bad("v, v_cache and cache_rows belong to a k_cache")
-    head = (_dtype_code(q), q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr() if cached else None, ldv, T,
-            qw // head_dim, hk, head_dim, _choice(ROPE_LAYOUTS, layout, "rotary layout"), table.size(1))
-    tail = (table.data_ptr(), table.size(0), _ints(positions, "positions", dev, T), q_out.data_ptr(), ldqo,
-            k_out.data_ptr() if k_out is not None else None, ldko, ctypes.byref(cache) if cached else None, rows,
-            _stream(stream, dev))
+    elif k_out is None:
+        k_out = k
+    if k_out is k:
+        k_to = k.data_ptr()
+    elif k_out is not None:
+        To, wo, ldko = _matrix(k_out, "k_out", dtype, dev)
+        if To != T or wo != kw:
+            raise _bad("k_out must have k's shape")
+        k_to = k_out.data_ptr()
+    n_positions, rot, ld = _matrix(table, "table", _F32, dev)
+    if ld != rot and n_positions > 1:
+        raise _bad("table must be contiguous")
+    lib = _bound or _lib()
     if norm is None:
-        _check(_lib().lora_rotary(*head, *tail))
+        call, extra = lib.lora_rotary, ()
     else:
-        weights = []
-        for w, name in zip(norm[:2], ("q_weight", "k_weight")):
-            if w is not None and (w.dtype != dtype or w.numel() != head_dim or not w.is_contiguous()
-                                  or not _on_device(w, dev)):
-                raise _bad(f"{name} must be {head_dim} contiguous elements of {dtype} on {dev}")
-            weights.append(w.data_ptr() if w is not None else None)
-        _check(_lib().lora_qk_norm_rotary(*head, *weights, norm[2], *tail))
+        call = lib.lora_qk_norm_rotary
+        extra = (None if norm[0] is None else _vector(norm[0], "q_weight", dtype, dev, head_dim),
+                 None if norm[1] is None else _vector(norm[1], "k_weight", dtype, dev, head_dim), norm[2])
+    _check(call(code, q.data_ptr(), ldq, k.data_ptr(), ldk, v_at, ldv, T, q_heads, kv_heads, head_dim,
+                _choice(ROPE_LAYOUTS, layout, "rotary layout"), rot, *extra, table.data_ptr(), n_positions,
+                _vector(positions, "positions", _I32, dev, T), q_out.data_ptr(), ldqo, k_to, ldko, cache, rows,
+                _stream_of(stream, dev)))
     return q_out, k_out
 
 
@@ -257,34 +285,35 @@ def build_tree(parents, q_start, context, *, max_nodes, n_tokens=None, page_tabl
     of each sequence; context: int32 [B], its tokens in the cache.  page_table:
     int32 [B, pages]; without it cache_rows is None.  mask: int64
     [T, ceil(max_nodes / 64)], bit j = sees node j."""
-    dev = context.device
-    if dev.type != "cuda":
-        raise _bad(f"context must be on a GPU (it is on {dev})")
+    dev = _gpu(context, "context")
+    device = context.device
     B = context.numel()
     T = parents.numel() if parents is not None else n_tokens
     if T is None:
         raise _bad("n_tokens is needed where parents is None")
-    words = -(-max_nodes // 64)
+    words = 0
     if parents is not None and mask is None:
-        mask = torch.zeros((T, max(words, 1)), dtype=torch.int64, device=dev)
-    if mask is not None and (mask.dim() != 2 or mask.size(0) != T or mask.dtype != torch.int64
-                             or not mask.is_contiguous() or not _on_device(mask, dev)):
-        raise _bad(f"mask must be a contiguous int64 tensor of {T} rows on {dev}")
+        mask = torch.zeros((T, max(-(-max_nodes // 64), 1)), dtype=_I64, device=device)
+    if mask is not None:
+        if mask.dim() != 2 or mask.size(0) != T:
+            raise _bad(f"mask must have {T} rows")
+        _vector(mask, "mask", _I64, dev, mask.numel())
+        words = mask.size(1)
     if positions is None:
-        positions = torch.full((T,), -1, dtype=torch.int32, device=dev)
+        positions = torch.full((T,), -1, dtype=_I32, device=device)
     table = (None, 0, 0)
     if page_table is not None:
         table = _int_rows(page_table, "page_table", dev, B)
         if cache_rows is None:
-            cache_rows = torch.full((T,), -1, dtype=torch.int32, device=dev)
+            cache_rows = torch.full((T,), -1, dtype=_I32, device=device)
     elif cache_rows is not None:
         raise _bad("cache_rows needs a page_table")
     _check(_lib().lora_build_tree(
-        _ints(parents, "parents", dev, T) if parents is not None else None, T, B, _ints(q_start, "q_start", dev, B + 1),
-        _ints(context, "context", dev, B), max_nodes, *table, n_pages, page_size,
-        mask.data_ptr() if mask is not None else None, mask.size(1) if mask is not None else 0,
-        _ints(positions, "positions", dev, T), _ints(cache_rows, "cache_rows", dev, T) if cache_rows is not None else None,
-        _stream(stream, dev)))
+        None if parents is None else _vector(parents, "parents", _I32, dev, T), T, B,
+        _vector(q_start, "q_start", _I32, dev, B + 1), _vector(context, "context", _I32, dev, B), max_nodes, *table,
+        n_pages, page_size, None if mask is None else mask.data_ptr(), words,
+        _vector(positions, "positions", _I32, dev, T),
+        None if cache_rows is None else _vector(cache_rows, "cache_rows", _I32, dev, T), _stream_of(stream, dev)))
     return mask, positions, cache_rows
 
 
@@ -316,43 +345,43 @@ def tree_attention(q, k_cache, v_cache, page_table, context, q_start, *, max_nod
     head_dim ** -0.5.  lse (optional, float32 [T, q_heads]) receives the
     logarithm of the softmax sums.  workspace: from alloc_attention_workspace
     for these sizes or larger ones of the same heads; None where it is empty."""
-    dev, dtype = q.device, q.dtype
-    if dev.type != "cuda":
-        raise _bad(f"q must be on a GPU (it is on {dev})")
-    T, width, ldq = _rows(q, "q")
-    if k_cache.dim() != 4:
-        raise _bad("k_cache and v_cache must be [n_pages, kv_heads, page_size, head_dim] of one shape")
-    cache = _cache(k_cache, v_cache, dtype, dev, None, None)
-    hk, page, d = k_cache.size(1), k_cache.size(2), k_cache.size(3)
+    dev, dtype = _gpu(q, "q"), q.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise _bad(f"unsupported dtype {dtype}")
+    T, width, ldq = _matrix(q, "q", dtype, dev)
+    cache, (n_pages, kv_heads, page, d) = _cache(k_cache, v_cache, dtype, dev)
     if d < 1 or width % d:
         raise _bad(f"q must be rows of whole heads of {d}")
+    q_heads = width // d
     if out is None:
-        out = torch.empty((T, width), dtype=dtype, device=dev)
-    if out.shape != q.shape or out.dtype != dtype or out.device != dev:
-        raise _bad(f"out must have q's shape and be {dtype} on {dev}")
-    ldo = _rows(out, "out")[2]
+        out = torch.empty((T, width), dtype=dtype, device=q.device)
+    To, wo, ldo = _matrix(out, "out", dtype, dev)
+    if To != T or wo != width:
+        raise _bad("out must have q's shape")
     B = context.numel()
     table, ld_table, n_table = _int_rows(page_table, "page_table", dev, B)
     if max_context is None:
-        max_context = max(0, n_table * page)
-    words = 0
+        max_context = n_table * page
+    mask_at = lse_at = ws = None
+    words = ws_bytes = 0
     if mask is not None:
-        if mask.dtype != torch.int64 or mask.dim() != 2 or mask.size(0) != T or not mask.is_contiguous() \
-                or not _on_device(mask, dev):
-            raise _bad(f"mask must be a contiguous int64 tensor of {T} rows on {dev}")
-        words = mask.size(1)
+        shape = mask.shape
+        if len(shape) != 2 or shape[0] != T:
+            raise _bad(f"mask must have {T} rows")
+        words = shape[1]
+        mask_at = _vector(mask, "mask", _I64, dev, T * words)
     if lse is not None:
-        _check_tensor(lse, "lse", dev, dtype=torch.float32, min_numel=T * (width // d))
-    ws, ws_bytes = None, 0
+        lse_at = _vector(lse, "lse", _F32, dev, T * q_heads)
     if workspace is not None:
-        if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or not _on_device(workspace, dev):
-            raise _bad(f"workspace must be a contiguous uint8 tensor on {dev}")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
-    _check(_lib().lora_tree_attention(
-        _dtype_code(q), q.data_ptr(), ldq, T, B, width // d, hk, d, ctypes.byref(cache), table, ld_table, n_table,
-        _ints(context, "context", dev, B), _ints(q_start, "q_start", dev, B + 1), max_nodes, max_context,
-        mask.data_ptr() if mask is not None else None, words, d ** -0.5 if scale is None else scale, out.data_ptr(),
-        ldo, lse.data_ptr() if lse is not None else None, ws, ws_bytes, _stream(stream, dev)))
+        ws_bytes = workspace.numel()
+        ws = _vector(workspace, "workspace", _U8, dev, ws_bytes)
+    lib = _bound or _lib()
+    _check(lib.lora_tree_attention(
+        code, q.data_ptr(), ldq, T, B, q_heads, kv_heads, d, cache, table, ld_table, n_table,
+        _vector(context, "context", _I32, dev, B), _vector(q_start, "q_start", _I32, dev, B + 1), max_nodes,
+        max_context, mask_at, words, d ** -0.5 if scale is None else scale, out.data_ptr(), ldo, lse_at, ws, ws_bytes,
+        _stream_of(stream, dev)))
     return out
 
 
@@ -362,24 +391,29 @@ def keep_path(k_caches, v_caches, page_table, context, path, n_kept, *, stream=N
     to position context[b] + j.  k_caches, v_caches: the layers' caches, alike
     in shape and strides, any number of them."""
     if isinstance(k_caches, torch.Tensor):
-        k_caches, v_caches = [k_caches], [v_caches]
-    k_caches, v_caches = list(k_caches), list(v_caches)
-    if not k_caches or len(k_caches) != len(v_caches):
+        k_caches, v_caches = (k_caches,), (v_caches,)
+    n = len(k_caches)
+    if n < 1 or len(v_caches) != n:
         raise _bad("need as many k_caches as v_caches, one at least")
-    dev, dtype = k_caches[0].device, k_caches[0].dtype
-    if dev.type != "cuda":
-        raise _bad(f"the caches must be on a GPU (they are on {dev})")
-    if dtype not in (torch.float32, torch.float16, torch.bfloat16):
+    k, v = k_caches[0], v_caches[0]
+    dev, dtype = _gpu(k, "the cache"), k.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise LoraError(LORA_ERR_UNSUPPORTED, f"unsupported dtype {dtype}")
-    caches = [_cache(k, v, dtype, dev, None, None) for k, v in zip(k_caches, v_caches)]
-    shape = k_caches[0].shape
-    if any(k.shape != shape for k in k_caches):
-        raise _bad("the layers' caches must share one shape")
+    cache, shape = _cache(k, v, dtype, dev)
+    if n > 1:
+        ks, vs = k.stride(), v.stride()
+        for caches, strides in ((k_caches, ks), (v_caches, vs)):
+            for c in caches:
+                if c.shape != shape or c.stride() != strides or c.dtype is not dtype or c.get_device() != dev:
+                    raise _bad("the layers' caches must be alike in shape, strides, type and GPU")
     B = context.numel()
     table = _int_rows(page_table, "page_table", dev, B)
-    steps, ld_path, n_path = _int_rows(path, "path", dev, B)
-    kept, at = _ints(n_kept, "n_kept", dev, B), _ints(context, "context", dev, B)
-    for i in range(0, len(caches), MAX_KEEP_LAYERS):
-        some = caches[i:i + MAX_KEEP_LAYERS]
-        _check(_lib().lora_keep_path(_dtype_code(k_caches[0]), (_KVCache * len(some))(*some), len(some), shape[1],
-                                     shape[3], B, *table, at, steps, ld_path, n_path, kept, _stream(stream, dev)))
+    steps = _int_rows(path, "path", dev, B)
+    kept, at = _vector(n_kept, "n_kept", _I32, dev, B), _vector(context, "context", _I32, dev, B)
+    k_at, v_at = [c.data_ptr() for c in k_caches], [c.data_ptr() for c in v_caches]
+    for i in range(0, n, MAX_KEEP_LAYERS):
+        m = min(n - i, MAX_KEEP_LAYERS)
+        layers = struct.Struct(f"@{m}P")
+        _check(_lib().lora_keep_path(code, cache, layers.pack(*k_at[i:i + m]), layers.pack(*v_at[i:i + m]), m, shape[1],
+                                     shape[3], B, *table, at, *steps, kept, _stream_of(stream, dev)))

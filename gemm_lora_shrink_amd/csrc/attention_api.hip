@@ -380,8 +380,8 @@ LORA_EXPORT lora_status lora_tree_attention(lora_dtype dt, const void* q, int64_
   return LORA_OK;
 }
 
-LORA_EXPORT lora_status lora_keep_path(lora_dtype dt, const lora_kv_cache* caches, int32_t n_layers, int32_t kv_heads,
-                                       int32_t d, int32_t B, const int32_t* page_table, int64_t ld_table,
+LORA_EXPORT lora_status lora_keep_path(lora_dtype dt, const lora_kv_cache* cache, void* const* k, void* const* v,
+                                       int32_t n_layers, int32_t kv_heads, int32_t d, int32_t B, const int32_t* page_table, int64_t ld_table,
                                        int32_t n_table, const int32_t* context, const int32_t* path, int64_t ld_path,
                                        int32_t n_path, const int32_t* n_kept, hipStream_t stream) {
   clear_error();
@@ -399,20 +399,18 @@ LORA_EXPORT lora_status lora_keep_path(lora_dtype dt, const lora_kv_cache* cache
   if (ld_path < n_path) return fail(LORA_ERR_INVALID_ARG, "ld_path is smaller than n_path");
   if ((st = check_table(page_table, ld_table, n_table)) != LORA_OK) return st;
   if (B == 0 || n_layers == 0 || n_path == 0) return LORA_OK;
-  if (!caches || !context || !path || !n_kept)
-    return fail(LORA_ERR_INVALID_ARG, "caches, context, path or n_kept is null");
+  if (!cache || !k || !v || !context || !path || !n_kept)
+    return fail(LORA_ERR_INVALID_ARG, "cache, k, v, context, path or n_kept is null");
   KeepParams p{};
+  lora_kv_cache c = *cache;
   for (int i = 0; i < n_layers; ++i) {
-    const lora_kv_cache &c = caches[i], &o = caches[0];
+    c.k = k[i];
+    c.v = v[i];
     if ((st = check_cache(dt, c)) != LORA_OK) return st;
-    if (c.k_page != o.k_page || c.k_head != o.k_head || c.k_row != o.k_row || c.v_page != o.v_page ||
-        c.v_head != o.v_head || c.v_row != o.v_row || c.n_pages != o.n_pages || c.page_size != o.page_size)
-      return fail(LORA_ERR_INVALID_ARG, "cache %d has other strides or sizes than cache 0", i);
-    p.k[i] = c.k;
-    p.v[i] = c.v;
+    p.k[i] = k[i];
+    p.v[i] = v[i];
   }
   const int64_t e = elem_bytes(dt);
-  const lora_kv_cache& c = caches[0];
   p.page_table = page_table;
   p.context = context;
   p.path = path;

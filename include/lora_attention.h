@@ -27,8 +27,9 @@
  * Head shapes: head_dim d is a multiple of 8 from 8 to LORA_MAX_HEAD_DIM;
  * q_heads is a multiple of kv_heads, query head h reads key/value head
  * h / (q_heads / kv_heads).  Rows and cache tensors have unit inner stride;
- * the other strides are free multiples of 16 bytes, and base pointers are
- * 16-byte aligned (LORA_ERR_UNSUPPORTED otherwise).
+ * the other strides are free multiples of 16 bytes (a page and a row of a cache
+ * within 4 GiB for the attention), and base pointers are 16-byte aligned
+ * (LORA_ERR_UNSUPPORTED otherwise).
  */
 #ifndef LORA_ATTENTION_MI355X_H
 #define LORA_ATTENTION_MI355X_H
@@ -227,12 +228,14 @@ lora_status lora_tree_attention(lora_dtype dt, const void *q, int64_t ldq, int32
  * K and V of every layer.  A path's entries must ascend; it ends before the
  * first that does not (or is negative), and a row whose page is missing at
  * either end stays.
- *   caches      [host] n_layers caches that share their strides and sizes
+ *   cache       [host] the layers' strides and sizes, which they share; its k
+ *               and v are not read
+ *   k, v        [host] n_layers pointers each
  *   path        [B][ld_path] int32, n_path columns
  *   n_kept      [B] int32
  */
-lora_status lora_keep_path(lora_dtype dt, const lora_kv_cache *caches, int32_t n_layers, int32_t kv_heads, int32_t d,
-                           int32_t B, const int32_t *page_table, int64_t ld_table, int32_t n_table,
+lora_status lora_keep_path(lora_dtype dt, const lora_kv_cache *cache, void *const *k, void *const *v,
+                           int32_t n_layers, int32_t kv_heads, int32_t d, int32_t B, const int32_t *page_table, int64_t ld_table, int32_t n_table,
                            const int32_t *context, const int32_t *path, int64_t ld_path, int32_t n_path,
                            const int32_t *n_kept, hipStream_t stream);
 

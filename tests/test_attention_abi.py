@@ -96,7 +96,8 @@ def test_frequencies_refused(args, status):
 def _cache(**kw):
     a = dict(k=FAKE, v=FAKE, k_page=1024, k_head=512, k_row=64, v_page=1024, v_head=512, v_row=64, n_pages=4, page_size=8)
     a.update(kw)
-    return A._KVCache(**a)
+    return A._CACHE_FIELDS.pack(*(a[x] or 0 for x in ("k", "v", "k_page", "k_head", "k_row", "v_page", "v_head", "v_row",
+                                                      "n_pages", "page_size")))
 
 
 def _table(**kw):
@@ -122,7 +123,7 @@ def _rotary(norm=False, cache=None, **kw):
     a.update(kw)
     head = [a[x] for x in ("dt", "q", "ldq", "k", "ldk", "v", "ldv", "T", "hq", "hk", "d", "layout", "rot")]
     tail = [a[x] for x in ("table", "n", "positions", "q_out", "ldqo", "k_out", "ldko")] + [
-        ctypes.byref(cache) if cache else None, a["rows"], None]
+        cache, a["rows"], None]
     if norm:
         return A._lib().lora_qk_norm_rotary(*head, a["qw"], a["kw"], a["eps"], *tail)
     return A._lib().lora_rotary(*head, *tail)
@@ -192,7 +193,7 @@ def _attend(cache="", **kw):
     a.update(kw)
     v = list(a.values())
     c = _cache() if cache == "" else cache
-    return A._lib().lora_tree_attention(*v[:8], ctypes.byref(c) if c else None, *v[8:], None)
+    return A._lib().lora_tree_attention(*v[:8], c, *v[8:], None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -201,7 +202,7 @@ def _attend(cache="", **kw):
     (dict(ctx=-1), BAD), (dict(ctx=(1 << 31) - 1), NOT), (dict(words=0), BAD), (dict(mask=FAKE + 4), NOT),
     (dict(scale=math.nan), BAD), (dict(scale=math.inf), BAD), (dict(table=None), BAD), (dict(ld=2), BAD),
     (dict(context=None), BAD), (dict(q_start=None), BAD), (dict(cache=None), BAD), (dict(cache=_cache(v=None)), BAD),
-    (dict(cache=_cache(k_page=1028)), NOT), (dict(q=None), BAD), (dict(q=FAKE + 8), NOT), (dict(ldq=504), BAD),
+    (dict(cache=_cache(k_page=1028)), NOT), (dict(cache=_cache(v_page=1 << 31)), NOT), (dict(q=None), BAD), (dict(q=FAKE + 8), NOT), (dict(ldq=504), BAD),
     (dict(out=None), BAD), (dict(ldo=516), NOT), (dict(ldo=1024), BAD),
     (dict(nodes=1 << 26, mask=None), NOT),
 ])
@@ -224,21 +225,21 @@ def test_workspace_sizes():
     assert n(-1, 1, 1, 1, 1, 1, 8) == 0 and n(1, 1, 1, 1, 3, 2, 8) == 0 and n(1, 1, 0, 1, 1, 1, 8) == 0
 
 
-def _keep(caches=None, **kw):
+def _keep(cache="", k=(FAKE, FAKE), v=(FAKE, FAKE), **kw):
     a = dict(dt=1, layers=2, hk=2, d=64, B=2, table=FAKE, ld=4, n_table=4, context=FAKE, path=FAKE, ldp=4, n_path=4,
              kept=FAKE)
     a.update(kw)
-    v = list(a.values())
-    c = (A._KVCache * 2)(*(caches or [_cache(), _cache()]))
-    return A._lib().lora_keep_path(v[0], c, *v[1:], None)
+    x = list(a.values())
+    layers = [(ctypes.c_void_p * 2)(*p) if p else None for p in (k, v)]
+    return A._lib().lora_keep_path(x[0], _cache() if cache == "" else cache, *layers, *x[1:], None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dt=9), BAD), (dict(layers=-1), BAD), (dict(layers=129), NOT), (dict(hk=0), BAD), (dict(d=4), NOT),
     (dict(B=-1), BAD), (dict(n_path=-1), BAD), (dict(n_path=1025, ldp=1025), NOT), (dict(ldp=3), BAD), (dict(ld=3), BAD),
     (dict(table=None), BAD), (dict(context=None), BAD), (dict(path=None), BAD), (dict(kept=None), BAD),
-    (dict(caches=[_cache(), _cache(k_row=128)]), BAD), (dict(caches=[_cache(), _cache(k=None)]), BAD),
-    (dict(caches=[_cache(page_size=0), _cache()]), BAD),
+    (dict(cache=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD), (dict(k=(FAKE, 0)), BAD), (dict(v=(FAKE + 8, FAKE)), NOT),
+    (dict(cache=_cache(page_size=0)), BAD), (dict(cache=_cache(k_row=60)), NOT),
 ])
 def test_keep_path_refused(kw, status):
     assert _keep(**kw) == status and glsa.lib().lora_last_error()
