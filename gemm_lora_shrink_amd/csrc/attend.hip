@@ -24,6 +24,8 @@
 // reading 16 rows at one piece, and 4 rows at 64 contiguous bytes, are both
 // free of bank conflicts.  A row that is no key (past the end, no page) is
 // loaded from a row of zeros.
+#include <algorithm>
+
 #include "attention.h"
 
 namespace lora {
@@ -84,16 +86,21 @@ template <typename Elem, int DP> struct Rows {
   static constexpr int kSteps = kBytes / 32;       // 16-byte operands of a lane and half
   static constexpr int kDB = DP / kBlock;          // blocks of the output
   static constexpr int kPerLoad = 1024 / kBytes;   // rows of one 64-lane load
+  // Piece c of row r lies at piece c ^ swizzle(r) of the row in LDS.  Keys: 16
+  // rows read at one piece (the lanes of one pass of a 16-byte read) touch 16
+  // different pieces of the banks' 256 bytes.  Values: the four rows of a transposing read, 64 bytes of
+  // each, lie in different quarters of the banks; fp32: the rows of the two
+  // halves of a wave, 128 bytes of each, in different halves.  As few bits as
+  // that takes, so that most addresses differ by constants.
+  __device__ static inline int swizzle_k(int r) { return kBytes == 128 ? (r >> 1) & 7 : r & 15; }
+  __device__ static inline int swizzle_v(int r) {
+    if (!k16) return ((r >> 2) & 1) << 3;
+    return kBytes == 128 ? ((r >> 1) & 1) << 2 : (r & 3) << 2;
+  }
   // waves of a SIMD that the kernels are compiled for
   static constexpr int kNarrowWaves = kBytes <= 128 ? 2 : 1;
   static constexpr int kWideWaves = kBytes <= 256 ? 2 : 1;
   static_assert(kBytes >= 128 && kBytes <= 1024, "");
-  // position of piece c of row r: c ^ swz(r)
-  __device__ static inline int swz(int r) {
-    if (kBytes == 128) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-    if (k16) return ((r & 3) << 2) | ((r >> 2) & 3);
-    return (((r >> 2) & 1) << 3) | ((r & 3) << 1) | ((r >> 3) & 1);
-  }
 };
 
 // Global-to-LDS loads with 64-bit addresses: lane l's 16 (or 4) bytes land at
@@ -114,6 +121,19 @@ template <typename Elem, int DP> struct Rows {
       : "=&s"(saved)                                                                                            \
       : "s"(lds), "v"(a), "v"(b)                                                                                \
       : "memory", "scc")
+__device__ inline void row_to_lds(const char* a, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %2, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(a)
+      : "memory");
+}
 template <bool ONCE> __device__ inline void two_rows_to_lds(const char* a, const char* b, uint32_t lds) {
   lds = __builtin_amdgcn_readfirstlane(lds);
   uint32_t saved;
@@ -148,6 +168,16 @@ __device__ inline float half_max(float x) {
 __device__ inline float half_sum(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The lane's number, as if it could change: what is computed from it is computed
+// again where it is used.  Held across the loops such values cost registers that
+// the products need, and reloading them from scratch memory waits for every load
+// in flight.
+__device__ __forceinline__ int lane_again() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
 }
 
 // What a workgroup works on.
@@ -218,39 +248,36 @@ template <typename Elem, int DP> struct RowBlock {
   int head;
   uint64_t bits0;      // first word of the mask row
   // LDS addresses of this lane's operands in a tile: piece 2 st + hi of key row
-  // r32 for the scores; for the values the rows and pieces described at
+  // r32 for the scores, st < 8; for the values the rows and pieces described at
   // add_values.  What differs from these by a constant is an offset of the read.
   static constexpr int kKeyAt = R::kSteps < 8 ? R::kSteps : 8;
-  static constexpr int kValueAt = R::k16 ? (R::kDB < 4 ? R::kDB : 4) : 0;
-  uint32_t key_at[kKeyAt];
-  uint32_t value_a[R::k16 ? kValueAt : 1], value_b[R::k16 ? kValueAt : 1];
+  static constexpr int kValueAt = R::k16 ? (R::kDB < 4 ? R::kDB : 4) : 2;
+  uint32_t key_at[kKeyAt], value_at[kValueAt];
 
   // Tiles of keys and values start at these LDS addresses.
   __device__ __forceinline__ void place(uint32_t keys, uint32_t values) {
 #pragma unroll
-    for (int st = 0; st < kKeyAt; ++st) key_at[st] = keys + r32 * R::kBytes + (((2 * st) ^ R::swz(r32) ^ hi) << 4);
-    if constexpr (R::k16) {
-      const int j = lane & 15, g1 = (lane >> 4) & 1;
-      const int ra = 4 * hi + (j >> 2), rb = ra + 8;
-      const int c = 2 * g1 + ((j & 3) >> 1), tail = (j & 1) * 8;
+    for (int st = 0; st < kKeyAt; ++st)
+      key_at[st] = keys + r32 * R::kBytes + (((2 * st + hi) ^ R::swizzle_k(r32)) << 4);
 #pragma unroll
-      for (int db = 0; db < kValueAt; ++db) {
-        value_a[db] = values + ra * R::kBytes + tail + ((c ^ R::swz(ra) ^ (4 * db)) << 4);
-        value_b[db] = values + rb * R::kBytes + tail + ((c ^ R::swz(rb) ^ (4 * db)) << 4);
+    for (int db = 0; db < kValueAt; ++db) {
+      if constexpr (R::k16) {
+        const int j = lane & 15, row = 4 * hi + (j >> 2), piece = 4 * db + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
+        value_at[db] = values + row * R::kBytes + ((piece ^ R::swizzle_v(row)) << 4) + (j & 1) * 8;
+      } else {
+        const int row = 4 * hi, piece = 8 * db + (r32 >> 2);
+        value_at[db] = values + row * R::kBytes + ((piece ^ R::swizzle_v(row)) << 4) + (r32 & 3) * 4;
       }
-    } else {
-      value_a[0] = values;
     }
   }
-  // The other of two tiles 2^k bytes apart.
-  __device__ __forceinline__ void other_tile(uint32_t apart) {
+  // On to another tile, whose address differs in the bits of `by`.
+  __device__ __forceinline__ void move_keys(uint32_t by) {
 #pragma unroll
-    for (int st = 0; st < kKeyAt; ++st) key_at[st] ^= apart;
+    for (int st = 0; st < kKeyAt; ++st) key_at[st] ^= by;
+  }
+  __device__ __forceinline__ void move_values(uint32_t by) {
 #pragma unroll
-    for (int db = 0; db < (R::k16 ? kValueAt : 1); ++db) {
-      value_a[db] ^= apart;
-      if (R::k16) value_b[db] ^= apart;
-    }
+    for (int db = 0; db < kValueAt; ++db) value_at[db] ^= by;
   }
 
   __device__ __forceinline__ void init(const AttendParams& p, const Work& w, int row_first) {
@@ -303,22 +330,29 @@ template <typename Elem, int DP> struct RowBlock {
     return (uint32_t)x;
   }
 
-  // Scores of the 32 keys from row kFirst of the tile on.  The keys' operands
-  // are requested eight at a time ahead of their products.
-  template <int kFirst> __device__ __forceinline__ f32x16 scores() const {
-    f32x16 s;
+  // Scores of the NS times 32 keys of the tile.  The blocks' products alternate,
+  // so that none waits for the one before it; the keys' operands are requested
+  // ahead of them.
+  template <int NS> __device__ __forceinline__ void scores(f32x16 (&s)[NS]) const {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = 0.f;
+    for (int b = 0; b < NS; ++b)
 #pragma unroll
-    for (int s0 = 0; s0 < R::kSteps; s0 += kKeyAt) {
-      u32x4 a[kKeyAt];
+      for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+    constexpr int kAhead = kKeyAt / NS;
 #pragma unroll
-      for (int st = 0; st < kKeyAt; ++st)
-        a[st] = *((lds_u32x4*)(lds_byte*)(uintptr_t)key_at[st] + (kFirst * R::kBytes + 32 * s0) / 16);
+    for (int s0 = 0; s0 < R::kSteps; s0 += kAhead) {
+      u32x4 a[NS][kAhead];
 #pragma unroll
-      for (int st = 0; st < kKeyAt; ++st) s = Mma32<Elem>::mma(a[st], q[s0 + st], s);
+      for (int st = 0; st < kAhead; ++st)  // steps past the eighth: 256 bytes, the swizzle's range, further
+#pragma unroll
+        for (int b = 0; b < NS; ++b)
+          a[b][st] = *((lds_u32x4*)(lds_byte*)(uintptr_t)key_at[(s0 + st) % 8] +
+                       (b * kBlock * R::kBytes + (s0 + st) / 8 * 256) / 16);
+#pragma unroll
+      for (int st = 0; st < kAhead; ++st)
+#pragma unroll
+        for (int b = 0; b < NS; ++b) s[b] = Mma32<Elem>::mma(a[b][st], q[s0 + st], s[b]);
     }
-    return s;
   }
 
   // Running softmax over NS blocks of scores (-inf where masked): scores become
@@ -363,25 +397,39 @@ template <typename Elem, int DP> struct RowBlock {
     for (int i = 0; i < 16; ++i) s[i] = (sb >> (8 * (i >> 2) + (i & 3))) & 1 ? s[i] : -INFINITY;
   }
 
+  // A block's weights as the operand of its product with the values.
+  struct Weights {
+    u32x4 w[R::k16 ? 2 : 4];
+  };
+  __device__ __forceinline__ static Weights pack(const f32x16& s) {
+    Weights r;
+#pragma unroll
+    for (int i = 0; i < (R::k16 ? 2 : 4); ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (R::k16) r.w[i][e] = Mma32<Elem>::pack2(s[8 * i + 2 * e], s[8 * i + 2 * e + 1]);
+        else r.w[i][e] = __float_as_uint(s[4 * i + e]);
+      }
+    return r;
+  }
+
   // o += V^T P^T over the 32 keys from row kFirst of the tile on.  ODD: what is no
   // finite number enters as 0 (see add_odd).
   // 16-bit: for step u the contraction runs over keys 16 u + 4 hi + (0..3) and
   // 16 u + 8 + 4 hi + (0..3), as the weights lie in registers; a transposing read
   // gives a lane 4 keys of one element, its 16 lanes reading 4 rows of 32 bytes.
-  template <bool ODD, int kFirst> __device__ __forceinline__ void add_values(const f32x16& s) {
+  template <bool ODD, int kFirst> __device__ __forceinline__ void add_values(const Weights& p) {
     if constexpr (R::k16) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        u32x4 w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = Mma32<Elem>::pack2(s[8 * u + 2 * e], s[8 * u + 2 * e + 1]);
         s16x4 va[R::kDB], vc[R::kDB];
 #pragma unroll
         for (int db = 0; db < R::kDB; ++db) {
           // blocks past the fourth lie 256 bytes (the swizzle's range) further
-          const int off = ((kFirst + 16 * u) * R::kBytes + (db / 4) * 256) / 8;
-          va[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)(uintptr_t)value_a[db % 4] + off);
-          vc[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)(uintptr_t)value_b[db % 4] + off);
+          lds_s16x4* at = (lds_s16x4*)(lds_byte*)(uintptr_t)value_at[db % 4] +
+                          ((kFirst + 16 * u) * R::kBytes + db / 4 * 256) / 8;
+          va[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at);
+          vc[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at + R::kBytes);  // 8 rows further
         }
 #pragma unroll
         for (int db = 0; db < R::kDB; ++db) {
@@ -393,24 +441,23 @@ template <typename Elem, int DP> struct RowBlock {
               const uint32_t x = v[e], e1 = Mma32<Elem>::kExp, e2 = e1 << 16;
               v[e] = ((x & e1) == e1 ? 0u : x & 0xffffu) | ((x & e2) == e2 ? 0u : x & 0xffff0000u);
             }
-          o[db] = Mma32<Elem>::mma(v, w, o[db]);
+          o[db] = Mma32<Elem>::mma(v, p.w[u], o[db]);
         }
       }
     } else {
-      const int c = (r32 >> 2) ^ (hi << 3);
-      const lds_byte* pr = (lds_byte*)(uintptr_t)(value_a[0] + 4 * hi * R::kBytes + (r32 & 3) * 4);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int key = 8 * (i >> 2) + (i & 3);  // + 4 hi
-        const int x = ((i & 3) << 1) | ((i >> 2) & 1);
         float v[R::kDB];
 #pragma unroll
         for (int db = 0; db < R::kDB; ++db) {
-          v[db] = *(lds_float*)(pr + ((((8 * db) & 8) ^ c ^ x) << 4) + (kFirst + key) * R::kBytes + (db / 2) * 256);
+          v[db] = *((lds_float*)(lds_byte*)(uintptr_t)value_at[db % 2] +
+                    ((kFirst + key) * R::kBytes + db / 2 * 256) / 4);
           if (ODD && (__float_as_uint(v[db]) & Mma32<Elem>::kExp) == Mma32<Elem>::kExp) v[db] = 0.f;
         }
+        const uint32_t wi = p.w[i / 4][i % 4];
 #pragma unroll
-        for (int db = 0; db < R::kDB; ++db) o[db] = Mma32<Elem>::mma1(v[db], s[i], o[db]);
+        for (int db = 0; db < R::kDB; ++db) o[db] = Mma32<Elem>::mma1(v[db], __uint_as_float(wi), o[db]);
       }
     }
   }
@@ -428,7 +475,7 @@ template <typename Elem, int DP> struct RowBlock {
 #pragma unroll
         for (int qd = 0; qd < 4; ++qd) {
           const int at = element(db, qd) * (int)sizeof(Elem);
-          const char* px = vb + k * R::kBytes + (((at >> 4) ^ R::swz(k)) << 4) + (at & 15);
+          const char* px = vb + k * R::kBytes + (((at >> 4) ^ R::swizzle_v(k)) << 4) + (at & 15);
           uint32_t x[4];
           if constexpr (R::k16) {
             const u32x2 h = *reinterpret_cast<const u32x2*>(px);
@@ -497,6 +544,35 @@ __device__ inline float* part_ml(const AttendParams& p, int split, int64_t row, 
   return p.part + (int64_t)p.splits * p.T * p.hq * p.d + (((int64_t)split * p.T + row) * p.hq + head) * 2;
 }
 
+// Store the rows of a block whose keys are all done: the output where the keys
+// are one chunk, else the chunk's part.
+template <typename Elem, int DP>
+__device__ __forceinline__ void store_rows(const AttendParams& p, const Work& w, const RowBlock<Elem, DP>& rb, float l) {
+  if (rb.row < 0) return;
+  const bool whole = p.splits == 1;
+  const float inv = whole ? inverse(l) : 1.0f;
+#pragma unroll
+  for (int db = 0; db < Rows<Elem, DP>::kDB; ++db)
+#pragma unroll
+    for (int qd = 0; qd < 4; ++qd) {
+      const int at = rb.element(db, qd);
+      if (at >= p.d) continue;
+      f32x4 x = f32x4{rb.o[db][4 * qd], rb.o[db][4 * qd + 1], rb.o[db][4 * qd + 2], rb.o[db][4 * qd + 3]};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] *= inv;
+      if (whole) rb.store4(p, rb.row, rb.head, at, x);
+      else *reinterpret_cast<f32x4*>(part_o(p, w.split, rb.row, rb.head) + at) = x;
+    }
+  if (rb.hi) return;
+  if (!whole) {
+    float* ml = part_ml(p, w.split, rb.row, rb.head);
+    ml[0] = rb.m;
+    ml[1] = l;
+  } else if (p.lse) {
+    p.lse[rb.row * p.hq + rb.head] = (rb.m + __builtin_amdgcn_logf(l)) * kLn2;
+  }
+}
+
 // Where a lane's key lies: its page's number comes from the table by way of LDS.
 struct PageAt {
   int place;      // row in the page
@@ -544,11 +620,11 @@ template <typename Elem, int DP, int NL, bool HELD> struct TileRows {
 // Address of the 16-byte piece that this lane brings in load i: the rows'
 // addresses are in LDS at `rows`, row_0 is the tile's row of the first of them.
 template <typename Elem, int DP>
-__device__ __forceinline__ const char* piece_of(const AttendParams& p, const char* const* rows, int row_0, int i,
-                                                int lane) {
+__device__ __forceinline__ const char* piece_of(const AttendParams& p, const char* const* rows, bool is_v, int row_0,
+                                                int i, int lane) {
   using R = Rows<Elem, DP>;
   const int r = i * R::kPerLoad + lane / R::kPieces;
-  const int piece = (lane % R::kPieces) ^ R::swz(row_0 + r);
+  const int piece = (lane % R::kPieces) ^ (is_v ? R::swizzle_v(row_0 + r) : R::swizzle_k(row_0 + r));
   const char* at = rows[r];
   if (p.d != DP && piece * 16 >= p.d * (int)sizeof(Elem)) at = reinterpret_cast<const char*>(g_zero_row);
   return at + 16 * piece;
@@ -604,16 +680,16 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
     if constexpr (at.kHeld) {
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        at.k[i] = piece_of<Elem, DP>(p, s_row[wave], 0, i, lane);
-        at.v[i] = piece_of<Elem, DP>(p, s_row[wave] + 32, 0, i, lane);
+        at.k[i] = piece_of<Elem, DP>(p, s_row[wave], false, 0, i, lane);
+        at.v[i] = piece_of<Elem, DP>(p, s_row[wave] + 32, true, 0, i, lane);
       }
     }
   };
-  auto load = [&](const char* const* held, const char* const* rows, uint32_t lds) __attribute__((always_inline)) {
+  auto load = [&](const char* const* held, const char* const* rows, bool is_v, uint32_t lds) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NL; i += 2) {
-      const char* a = at.kHeld ? held[at.kHeld ? i : 0] : piece_of<Elem, DP>(p, rows, 0, i, lane);
-      const char* b = at.kHeld ? held[at.kHeld ? i + 1 : 0] : piece_of<Elem, DP>(p, rows, 0, i + 1, lane);
+      const char* a = at.kHeld ? held[at.kHeld ? i : 0] : piece_of<Elem, DP>(p, rows, is_v, 0, i, lane);
+      const char* b = at.kHeld ? held[at.kHeld ? i + 1 : 0] : piece_of<Elem, DP>(p, rows, is_v, 0, i + 1, lane);
       two_rows_to_lds<true>(a, b, lds + 1024 * i);
     }
   };
@@ -625,19 +701,20 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
     wait_loads<0>();
     find_rows(0, ahead[0]);
     valid = at.valid;
-    load(at.k, s_row[wave], k_lds);
+    load(at.k, s_row[wave], false, k_lds);
     fetch_ids(2, ahead[0]);
-    load(at.v, s_row[wave] + 32, v_lds);
+    load(at.v, s_row[wave] + 32, true, v_lds);
     find_rows(1, ahead[1]);
   }
   auto tile = [&](int t, auto tail) __attribute__((always_inline)) {
     constexpr bool kTail = decltype(tail)::value;
     const bool more = t + 1 < nt;
     wait_loads<NL>();  // keys of t and page numbers of t + 2 are there
-    f32x16 s[1] = {rb.template scores<0>()};
+    f32x16 s[1];
+    rb.scores(s);
     wait_lds();
     if (more) {
-      load(at.k, s_row[wave], k_lds);
+      load(at.k, s_row[wave], false, k_lds);
       fetch_ids(t + 3, ahead[1]);
     }
     uint32_t seen = valid;
@@ -647,15 +724,15 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
     if (more) wait_loads<NL + 1>();
     else wait_loads<0>();
     if (kTail && __any(seen != valid) && rb.any_odd(vbuf, kBlock)) {
-      rb.template add_values<kTail, 0>(s[0]);
+      rb.template add_values<kTail, 0>(rb.pack(s[0]));
       rb.add_odd(vbuf, seen);
     } else {
-      rb.template add_values<false, 0>(s[0]);
+      rb.template add_values<false, 0>(rb.pack(s[0]));
     }
     wait_lds();
     valid = at.valid;
     if (more) {
-      load(at.v, s_row[wave] + 32, v_lds);
+      load(at.v, s_row[wave] + 32, true, v_lds);
       find_rows(t + 2, ahead[0]);
       ahead[0] = ahead[1];
     }
@@ -769,8 +846,8 @@ __global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWideWaves)) void attend
     const char* a[2 * NL];
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      a[i] = piece_of<Elem, DP>(p, s_row[wave], wave * kMine, i, lane);
-      a[NL + i] = piece_of<Elem, DP>(p, s_row[wave] + kMine, wave * kMine, i, lane);
+      a[i] = piece_of<Elem, DP>(p, s_row[wave], false, wave * kMine, i, lane);
+      a[NL + i] = piece_of<Elem, DP>(p, s_row[wave] + kMine, true, wave * kMine, i, lane);
     }
 #pragma unroll
     for (int i = 0; i < NL; i += 2) two_rows_to_lds<false>(a[i], a[i + 1], to + 1024 * i);
@@ -799,8 +876,7 @@ __global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWideWaves)) void attend
     if (!idle) {
       f32x16 s[NS];
       uint32_t seen[NS], valid[NS];
-      s[0] = rb.template scores<0>();
-      if constexpr (NS == 2) s[1] = rb.template scores<kBlock>();
+      rb.scores(s);
       bool uneven = false;
 #pragma unroll
       for (int b = 0; b < NS; ++b) {
@@ -819,18 +895,19 @@ __global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWideWaves)) void attend
       rb.weigh(s, c);
       const char* vb = s_kv[t & 1] + kTile;
       if (kTail && uneven && rb.any_odd(vb, KT)) {
-        rb.template add_values<kTail, 0>(s[0]);
+        rb.template add_values<kTail, 0>(rb.pack(s[0]));
         rb.add_odd(vb, seen[0]);
         if constexpr (NS == 2) {
-          rb.template add_values<kTail, kBlock>(s[1]);
+          rb.template add_values<kTail, kBlock>(rb.pack(s[1]));
           rb.add_odd(vb + kBlock * R::kBytes, seen[1]);
         }
       } else {
-        rb.template add_values<false, 0>(s[0]);
-        if constexpr (NS == 2) rb.template add_values<false, kBlock>(s[1]);
+        rb.template add_values<false, 0>(rb.pack(s[0]));
+        if constexpr (NS == 2) rb.template add_values<false, kBlock>(rb.pack(s[1]));
       }
     }
-    rb.other_tile(2 * kTile);
+    rb.move_keys(2 * kTile);
+    rb.move_values(2 * kTile);
     if (more) {
       find_rows(t + 2, ahead[0]);
       ahead[0] = ahead[1];
@@ -841,31 +918,244 @@ __global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWideWaves)) void attend
   for (; t < nf; ++t) tile(t, No{});
   for (; t < nt; ++t) tile(t, Yes{});
 
-  if (rb.row < 0) return;
-  const float l = half_sum(rb.l);
-  const bool whole = p.splits == 1;
-  const float inv = whole ? inverse(l) : 1.0f;
+  store_rows(p, w, rb, half_sum(rb.l));
+}
+
+// Rows of 16-bit heads up to 128 elements and fp32 heads up to 64: eight waves
+// in two groups of four that take turns.  While one group multiplies (the
+// values of its last tile and the scores of its next, on the matrix cores), the
+// other computes weights (on the vector unit); a barrier ends each half step,
+// and the second group runs one half step behind, so that each SIMD always has
+// one wave of each kind.  KG = 1: the eight waves hold 256 rows and all take a
+// stage's 64 keys.  KG = 2: the groups hold the same 128 rows and take 32 keys of
+// a stage each; their outputs meet at the end.
+// Stages are in a ring of four: at step t a wave fetches its eighth of stage
+// t + 2 into the ring place that stage t - 2 left one half step ago.  The row
+// addresses of four stages are found together, one a lane, at the second step of
+// the four before; their page numbers are requested two steps earlier.
+template <typename Elem, int DP, int KG>
+__global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
+  using R = Rows<Elem, DP>;
+  using Block = RowBlock<Elem, DP>;
+  constexpr int KT = 64, NS = 2 / KG, kRing = 4;
+  constexpr int kTile = KT * R::kBytes, kStage = 2 * kTile;
+  constexpr int kMine = KT / 8;  // rows a wave fetches of K, and of V
+  constexpr int NL = kMine * R::kBytes / 1024;
+  static_assert(NL >= 1, "");
+  // (aligned to its size, so that an XOR changes stages)
+  __shared__ __attribute__((aligned(kRing * kStage))) char s_kv[kRing][kStage];
+  __shared__ __attribute__((aligned(16))) const char* s_row[8][64];
+  __shared__ int s_id[8][2][64];
+  __shared__ __attribute__((aligned(8))) uint8_t s_valid[8][8];
+  warm_args(p);
+  const Work w = work_of<32 * 8 / KG>(p);
+  if (w.none) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int late = wave >> 2;                        // the group that runs behind
+  const int block = KG == 1 ? wave : wave & 3, part = KG == 1 ? 0 : late;
+  Block rb;
+  rb.init(p, w, w.row0 + block * kBlock);
+  const bool idle = w.row0 + block * kBlock >= w.rows;  // a wave without rows only fetches
+  const int lane = rb.lane;
+  const float c = p.scale == 0.f ? 1.0f : fabsf(p.scale) * kLog2e;
+  const int keys = w.k1 - w.k0, inside = min(w.ctx, w.k1) - w.k0;
+  const int nt = keys > 0 ? (keys + KT - 1) / KT : 0, nf = inside > 0 ? inside / KT : 0;
+
+  // lane 16 i + 8 v + r finds row r of this wave's eighth of the i-th of four
+  // stages, of the keys (v = 0) and of the values
+  auto page_of = [&](int four, int lane, int& col) {
+    return page_at(p, (int64_t)w.k0 + ((int64_t)four * 4 + (lane >> 4)) * KT + wave * kMine + (lane & 7), w.k1, col);
+  };
+  auto fetch_ids = [&](int four) {
+    int col;
+    const PageAt a = page_of(four, lane_again(), col);
+    word_to_lds(entry_of(p, w.b, a, col), (uint32_t)(uintptr_t)s_id[wave][four & 1]);
+  };
+  auto find_rows = [&](int four) {
+    const int lane = lane_again();
+    int col;
+    const PageAt a = page_of(four, lane, col);
+    const HeadAt h = head_at<Elem>(p, w.h, (lane >> 3) & 1);
+    const uint32_t id = (uint32_t)s_id[wave][four & 1][lane];
+    const bool valid = a.in_table && id < (uint64_t)p.cache.n_pages && (int)id >= 0;
+    s_row[wave][lane] =
+        valid ? reinterpret_cast<const char*>(h.row_at(id, a.place)) : reinterpret_cast<const char*>(g_zero_row);
+    const uint64_t all = __ballot(valid);
+    if ((lane & 15) == 0) s_valid[(four * 4 + (lane >> 4)) & 7][wave] = (uint8_t)(all >> lane);
+  };
+  const char* next[2 * NL];  // of the stage to be fetched next
+  auto find_pieces = [&](int t) {
+    const int lane = lane_again();
+    const char* const* rows = s_row[wave] + 16 * (t & 3);
 #pragma unroll
-  for (int db = 0; db < R::kDB; ++db)
-#pragma unroll
-    for (int qd = 0; qd < 4; ++qd) {
-      const int at = rb.element(db, qd);
-      if (at >= p.d) continue;
-      f32x4 x = f32x4{rb.o[db][4 * qd], rb.o[db][4 * qd + 1], rb.o[db][4 * qd + 2], rb.o[db][4 * qd + 3]};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] *= inv;
-      if (whole) rb.store4(p, rb.row, rb.head, at, x);
-      else *reinterpret_cast<f32x4*>(part_o(p, w.split, rb.row, rb.head) + at) = x;
+    for (int i = 0; i < 2 * NL; ++i) {
+      const int of = (i % NL) * R::kPerLoad + lane / R::kPieces, r = wave * kMine + of;
+      const int piece = (lane % R::kPieces) ^ (i < NL ? R::swizzle_k(r) : R::swizzle_v(r));
+      next[i] = rows[(i / NL) * kMine + of];
+      if (p.d != DP && piece * 16 >= p.d * (int)sizeof(Elem)) next[i] = reinterpret_cast<const char*>(g_zero_row);
+      next[i] += 16 * piece;
     }
-  if (rb.hi == 0) {
-    if (!whole) {
-      float* ml = part_ml(p, w.split, rb.row, rb.head);
-      ml[0] = rb.m;
-      ml[1] = l;
-    } else if (p.lse) {
-      p.lse[rb.row * p.hq + rb.head] = (rb.m + __builtin_amdgcn_logf(l)) * kLn2;
+  };
+  auto load_stage = [&](int t) {
+    const uint32_t to = (uint32_t)(uintptr_t)s_kv[t % kRing] + wave * kMine * R::kBytes;
+#pragma unroll
+    for (int i = 0; i < 2 * NL; ++i) row_to_lds(next[i], to + (i / NL) * kTile + 1024 * (i % NL));
+  };
+
+  f32x16 s[NS];
+  typename Block::Weights weights[NS];
+  uint32_t seen[NS];
+  bool odd = false;
+  uint32_t keys_in = 0, values_in = 0;  // ring places that the operand addresses are at
+  auto to_values = [&](int t) __attribute__((always_inline)) {
+    const uint32_t at = (uint32_t)t % kRing;
+    rb.move_values((values_in ^ at) * kStage);
+    values_in = at;
+  };
+  auto add = [&](auto with_odd) __attribute__((always_inline)) {
+    rb.template add_values<decltype(with_odd)::value, 0>(weights[0]);
+    if constexpr (NS == 2) rb.template add_values<decltype(with_odd)::value, kBlock>(weights[1]);
+  };
+  auto score = [&](int t) __attribute__((always_inline)) {
+    const uint32_t at = (uint32_t)t % kRing;
+    rb.move_keys((keys_in ^ at) * kStage);
+    keys_in = at;
+    rb.scores(s);
+  };
+  // the values of stage t (of the tail: some may be no finite numbers)
+  auto add_tail = [&](int t) __attribute__((always_inline)) {
+    to_values(t);
+    if (odd) {
+      add(Yes{});
+      const char* vb = s_kv[t % kRing] + kTile + part * kBlock * R::kBytes;
+      rb.add_odd(vb, seen[0]);
+      if constexpr (NS == 2) rb.add_odd(vb + kBlock * R::kBytes, seen[1]);
+    } else {
+      add(No{});
     }
+  };
+  // The matrix half step: the values of stage t - 1, the scores of stage t.
+  auto multiply = [&](int t, auto tail) __attribute__((always_inline)) {
+    if (idle) return;
+    if (t == 0) {
+      score(t);
+    } else if constexpr (decltype(tail)::value) {
+      add_tail(t - 1);
+      score(t);
+    } else {
+      to_values(t - 1);
+      add(No{});
+      score(t);
+      if constexpr (R::k16) {
+        // operands are requested six reads ahead of the products all through:
+        // left alone, the compiler saves registers and waits for most of them
+        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+        for (int i = 0; i < NS * 2 * R::kDB; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < NS * R::kSteps; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+      }
+    }
+  };
+  auto soften = [&](int t, auto tail) __attribute__((always_inline)) {
+    if (idle) return;
+    const uint64_t at = *reinterpret_cast<const uint64_t*>(s_valid[t & 7]);
+    const uint64_t all = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) << 32) |
+                         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at);
+    bool uneven = false;
+#pragma unroll
+    for (int b = 0; b < NS; ++b) {
+      const uint32_t valid = (uint32_t)(all >> (32 * (part + b)));
+      seen[b] = valid;
+      if constexpr (decltype(tail)::value) {
+        seen[b] &= rb.sees(p, w, w.k0 + t * KT + (part + b) * kBlock);
+        uneven |= __any(seen[b] != valid);
+        if (__any(seen[b] != ~0u)) rb.mask_scores(s[b], seen[b]);
+      } else if (valid != ~0u) {
+        rb.mask_scores(s[b], valid);
+      }
+    }
+    rb.weigh(s, c);
+#pragma unroll
+    for (int b = 0; b < NS; ++b) weights[b] = rb.pack(s[b]);
+    if constexpr (decltype(tail)::value)
+      odd = uneven && rb.any_odd(s_kv[t % kRing] + kTile + part * kBlock * R::kBytes, NS * kBlock);
+  };
+  auto step = [&](int t, auto tail) __attribute__((always_inline)) {
+    const bool more = t + 2 < nt, ask = more && (t & 3) == 3;
+    if (more) load_stage(t + 2);
+    if (ask) fetch_ids((t >> 2) + 2);
+    multiply(t, tail);
+    // this wave's part of stage t + 1, and what was asked for before this step
+    if (ask) wait_loads<2 * NL + 1>();
+    else if (more) wait_loads<2 * NL>();
+    else wait_loads<0>();
+    lds_barrier();
+    soften(t, tail);
+    if (more && (t & 3) == 1) find_rows((t >> 2) + 1);
+    if (t + 3 < nt) find_pieces(t + 3);
+    lds_barrier();
+  };
+
+  if (nt > 0) {
+    fetch_ids(0);
+    fetch_ids(1);
+    wait_loads<0>();
+    find_rows(0);
+    find_pieces(0);
+    load_stage(0);
+    find_pieces(1);
+    load_stage(1);
+    find_pieces(2);
+    wait_loads<2 * NL>();  // all but stage 1
+    rb.place((uint32_t)(uintptr_t)s_kv[0] + part * kBlock * R::kBytes,
+             (uint32_t)(uintptr_t)s_kv[0] + kTile + part * kBlock * R::kBytes);
+    lds_barrier();
+    if (late) lds_barrier();
+    int t = 0;
+    for (; t < nf; ++t) step(t, No{});
+    for (; t < nt; ++t) step(t, Yes{});
+    if (!idle) add_tail(nt - 1);
+    if (!late) lds_barrier();
   }
+
+  float l = half_sum(rb.l);
+  if constexpr (KG == 2) {
+    // the second group's outputs pass through LDS; nothing is in flight any more
+    __syncthreads();
+    f32x4* red = reinterpret_cast<f32x4*>(s_kv[0]) + block * (R::kDB * 4 + 1) * 64;
+    if (late) {
+#pragma unroll
+      for (int db = 0; db < R::kDB; ++db)
+#pragma unroll
+        for (int qd = 0; qd < 4; ++qd)
+          red[(db * 4 + qd) * 64 + lane] =
+              f32x4{rb.o[db][4 * qd], rb.o[db][4 * qd + 1], rb.o[db][4 * qd + 2], rb.o[db][4 * qd + 3]};
+      red[R::kDB * 4 * 64 + lane] = f32x4{rb.m, l, 0.f, 0.f};
+    }
+    __syncthreads();
+    if (late) return;
+    const f32x4 ml = red[R::kDB * 4 * 64 + lane];
+    const float M = fmaxf(rb.m, ml[0]), ms = M == -INFINITY ? 0.f : M;
+    const float f = __builtin_amdgcn_exp2f(rb.m - ms), g = __builtin_amdgcn_exp2f(ml[0] - ms);
+    l = l * f + ml[1] * g;
+    rb.m = M;
+#pragma unroll
+    for (int db = 0; db < R::kDB; ++db)
+#pragma unroll
+      for (int qd = 0; qd < 4; ++qd) {
+        const f32x4 x = red[(db * 4 + qd) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rb.o[db][4 * qd + e] = rb.o[db][4 * qd + e] * f + x[e] * g;
+      }
+  }
+  store_rows(p, w, rb, l);
 }
 
 // Join a row's chunks, in their order: one wave a row, 4 elements a lane, the
@@ -919,25 +1209,37 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendParams p) {
 
 // ---- host ------------------------------------------------------------------
 
-// How the keys are cut: chunks so long that there are about kTargetGroups
-// workgroups in all where every sequence is as long as its bound, and no
-// shorter than kMinChunk keys.
-constexpr int64_t kTargetGroups = 1024;
-constexpr int64_t kMinChunk = 256;
-constexpr int64_t kMaxGroups = (int64_t)1 << 30;
-
+// Which kernel takes a call, by the rows of a (sequence, key/value head) and the
+// bytes of a padded head: up to 32 rows the narrow one, else the one whose waves
+// take turns where its rows fit its registers, or the wide one.
+enum class Kind { kNarrow, kTurns128, kTurns256, kWide };
 struct AttendPlan {
-  bool wide;
+  Kind kind;
   int32_t chunk, splits, row_tiles;
 };
 
-AttendPlan attend_plan(int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk) {
+// How the keys are cut: chunks so long that about so many workgroups run in all
+// as the chip holds at once (two a compute unit of the wide kernel, one of the
+// one with turns; the narrow kernel's take turns on four), where every sequence
+// is as long as its bound, and no shorter than kMinChunk keys.
+constexpr int64_t kMinChunk = 256;
+constexpr int64_t kMaxGroups = (int64_t)1 << 30;
+
+AttendPlan attend_plan(int elem, int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
+                       int32_t d) {
   AttendPlan a;
   const int64_t rows = (int64_t)max_nodes * (hq / hk), keys = (int64_t)max_context + max_nodes;
-  a.wide = rows > kBlock;
-  a.row_tiles = (int32_t)ceil_div(rows, a.wide ? 4 * kBlock : kBlock);
+  const int row_bytes = elem * (d <= 64 ? 64 : d <= 128 ? 128 : 256);
+  int64_t tile = kBlock, groups = 1024;
+  a.kind = Kind::kNarrow;
+  if (rows > kBlock) {
+    a.kind = row_bytes > 256 ? Kind::kWide : rows > 4 * kBlock ? Kind::kTurns256 : Kind::kTurns128;
+    tile = a.kind == Kind::kTurns256 ? 8 * kBlock : 4 * kBlock;
+    groups = a.kind == Kind::kWide ? 512 : 256;
+  }
+  a.row_tiles = (int32_t)ceil_div(rows, tile);
   const int64_t units = (int64_t)B * hk * a.row_tiles;
-  int64_t chunk = ceil_div(keys * units, a.wide ? kTargetGroups / 2 : kTargetGroups);
+  int64_t chunk = ceil_div(keys * units, groups);
   if (chunk < kMinChunk) chunk = kMinChunk;
   const int64_t fewest = ceil_div(keys * units, kMaxGroups);
   if (chunk < fewest) chunk = fewest;
@@ -949,30 +1251,34 @@ AttendPlan attend_plan(int32_t B, int32_t max_nodes, int32_t max_context, int32_
 }
 
 template <typename Elem, int DP>
-hipError_t launch_d(const AttendParams& p, bool wide, hipStream_t stream) {
+hipError_t launch_d(const AttendParams& p, Kind kind, hipStream_t stream) {
   constexpr int kRow = DP * (int)sizeof(Elem);
   const int64_t units = (int64_t)p.B * p.hk * p.splits * p.row_tiles;
   const int64_t grid = ceil_div(units, kXcds) * kXcds;
   if (grid > (int64_t)0x7fffffff) return hipErrorInvalidConfiguration;
-  if (wide) {
-    constexpr int KT = kRow <= 256 ? 64 : 32;
-    hipLaunchKernelGGL((attend_wide_kernel<Elem, DP, KT>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
-  } else {
+  const dim3 g((unsigned)grid);
+  if (kind == Kind::kNarrow) {
     constexpr int NW = kRow <= 512 ? 4 : 2;
-    hipLaunchKernelGGL((attend_narrow_kernel<Elem, DP, NW>), dim3((unsigned)grid), dim3(NW * 64), 0, stream, p);
+    hipLaunchKernelGGL((attend_narrow_kernel<Elem, DP, NW>), g, dim3(NW * 64), 0, stream, p);
+  } else if constexpr (kRow > 256) {
+    hipLaunchKernelGGL((attend_wide_kernel<Elem, DP, 32>), g, dim3(kThreads), 0, stream, p);
+  } else if (kind == Kind::kTurns256) {
+    hipLaunchKernelGGL((attend_turns_kernel<Elem, DP, 1>), g, dim3(512), 0, stream, p);
+  } else {
+    hipLaunchKernelGGL((attend_turns_kernel<Elem, DP, 2>), g, dim3(512), 0, stream, p);
   }
   return hipGetLastError();
 }
 
 template <typename Elem>
 hipError_t launch(AttendParams p, hipStream_t stream) {
-  const AttendPlan a = attend_plan(p.B, p.max_nodes, p.max_context, p.hq, p.hk);
+  const AttendPlan a = attend_plan(sizeof(Elem), p.B, p.max_nodes, p.max_context, p.hq, p.hk, p.d);
   p.chunk = a.chunk;
   p.splits = a.splits;
   p.row_tiles = a.row_tiles;
-  hipError_t e = p.d <= 64    ? launch_d<Elem, 64>(p, a.wide, stream)
-                 : p.d <= 128 ? launch_d<Elem, 128>(p, a.wide, stream)
-                              : launch_d<Elem, 256>(p, a.wide, stream);
+  hipError_t e = p.d <= 64    ? launch_d<Elem, 64>(p, a.kind, stream)
+                 : p.d <= 128 ? launch_d<Elem, 128>(p, a.kind, stream)
+                              : launch_d<Elem, 256>(p, a.kind, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t rows = (int64_t)p.max_nodes * p.hq;
   hipLaunchKernelGGL(attend_join_kernel<Elem>, dim3((unsigned)ceil_div(rows, kThreads / 64), (unsigned)p.B),
@@ -984,9 +1290,11 @@ hipError_t launch(AttendParams p, hipStream_t stream) {
 
 int64_t attend_need_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
                           int32_t d) {
-  const AttendPlan a = attend_plan(B, max_nodes, max_context, hq, hk);
-  if (a.splits == 1) return 0;
-  const int64_t bytes = (int64_t)a.splits * T * hq * (d + 2) * 4;
+  // the same for every type of the call
+  int64_t splits = 1;
+  for (int elem : {2, 4}) splits = std::max<int64_t>(splits, attend_plan(elem, B, max_nodes, max_context, hq, hk, d).splits);
+  if (splits == 1) return 0;
+  const int64_t bytes = splits * T * hq * (d + 2) * 4;
   return (bytes + 255) & ~int64_t(255);
 }
 
