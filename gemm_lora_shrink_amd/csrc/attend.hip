@@ -86,21 +86,15 @@ template <typename Elem, int DP> struct Rows {
   static constexpr int kSteps = kBytes / 32;       // 16-byte operands of a lane and half
   static constexpr int kDB = DP / kBlock;          // blocks of the output
   static constexpr int kPerLoad = 1024 / kBytes;   // rows of one 64-lane load
-  // Piece c of row r lies at piece c ^ swizzle(r) of the row in LDS.  Keys: 16
-  // rows read at one piece (the lanes of one pass of a 16-byte read) touch 16
-  // different pieces of the banks' 256 bytes.  Values: the four rows of a transposing read, 64 bytes of
-  // each, lie in different quarters of the banks; fp32: the rows of the two
-  // halves of a wave, 128 bytes of each, in different halves.  As few bits as
-  // that takes, so that most addresses differ by constants.
-  __device__ static inline int swizzle_k(int r) { return kBytes == 128 ? (r >> 1) & 7 : r & 15; }
-  __device__ static inline int swizzle_v(int r) {
-    if (!k16) return ((r >> 2) & 1) << 3;
-    return kBytes == 128 ? ((r >> 1) & 1) << 2 : (r & 3) << 2;
-  }
-  // waves of a SIMD that the kernels are compiled for
-  static constexpr int kNarrowWaves = kBytes <= 128 ? 2 : 1;
-  static constexpr int kWideWaves = kBytes <= 256 ? 2 : 1;
+  // waves of a SIMD that the narrow kernel is compiled for
+  static constexpr int kNarrowWaves = DP <= 64 ? 2 : 1;
   static_assert(kBytes >= 128 && kBytes <= 1024, "");
+  // position of piece c of row r: c ^ swz(r)
+  __device__ static inline int swz(int r) {
+    if (kBytes == 128) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    if (k16) return ((r & 3) << 2) | ((r >> 2) & 3);
+    return (((r >> 2) & 1) << 3) | ((r & 3) << 1) | ((r >> 3) & 1);
+  }
 };
 
 // Global-to-LDS loads with 64-bit addresses: lane l's 16 (or 4) bytes land at
@@ -170,16 +164,6 @@ __device__ inline float half_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// The lane's number, as if it could change: what is computed from it is computed
-// again where it is used.  Held across the loops such values cost registers that
-// the products need, and reloading them from scratch memory waits for every load
-// in flight.
-__device__ __forceinline__ int lane_again() {
-  int lane = threadIdx.x & 63;
-  asm volatile("" : "+v"(lane));
-  return lane;
-}
-
 // What a workgroup works on.
 struct Work {
   int64_t start;       // first row of the sequence
@@ -202,8 +186,8 @@ __device__ inline void sequence_of(const AttendParams& p, int b, int64_t& start,
   ctx = x < 0 ? 0 : (x > p.max_context ? p.max_context : x);
 }
 __device__ inline int splits_of(const AttendParams& p, int n, int ctx) {
-  const int s = (int)(((uint32_t)ctx + (uint32_t)n + (uint32_t)p.chunk - 1u) / (uint32_t)p.chunk);
-  return s < 1 ? 1 : s;
+  const int s = (int)p.by_chunk.div((uint32_t)ctx + (uint32_t)n - 1u < 0x7fffffffu ? (uint32_t)ctx + (uint32_t)n - 1u : 0u) + 1;
+  return s;
 }
 
 // Units of work lie in the order sequence, head, chunk, row tile; the workgroups
@@ -213,13 +197,15 @@ template <int ROWS>
 __device__ inline Work work_of(const AttendParams& p) {
   Work w;
   const int per = (int)(gridDim.x / kXcds);
-  int u = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
-  const int rt = u % p.row_tiles;
-  u /= p.row_tiles;
-  w.split = u % p.splits;
-  u /= p.splits;
-  w.h = u % p.hk;
-  w.b = u / p.hk;
+  uint32_t u = (blockIdx.x % kXcds) * (uint32_t)per + blockIdx.x / kXcds, v = p.by_tiles.div(u);
+  const int rt = (int)(u - v * p.by_tiles.d);
+  u = v;
+  v = p.by_splits.div(u);
+  w.split = (int)(u - v * p.by_splits.d);
+  u = v;
+  v = p.by_heads.div(u);
+  w.h = (int)(u - v * p.by_heads.d);
+  w.b = (int)v;
   w.none = w.b >= p.B;
   if (w.none) return w;
   sequence_of(p, w.b, w.start, w.n, w.ctx);
@@ -248,26 +234,34 @@ template <typename Elem, int DP> struct RowBlock {
   int head;
   uint64_t bits0;      // first word of the mask row
   // LDS addresses of this lane's operands in a tile: piece 2 st + hi of key row
-  // r32 for the scores, st < 8; for the values the rows and pieces described at
+  // r32 for the scores; for the values the rows and pieces described at
   // add_values.  What differs from these by a constant is an offset of the read.
-  static constexpr int kKeyAt = R::kSteps < 8 ? R::kSteps : 8;
-  static constexpr int kValueAt = R::k16 ? (R::kDB < 4 ? R::kDB : 4) : 2;
-  uint32_t key_at[kKeyAt], value_at[kValueAt];
+  // Rows past 256 bytes leave no registers for them: their pieces are found by an
+  // XOR from the first one's at each read.
+  static constexpr bool kHeld = R::kBytes <= 256;
+  static constexpr int kAhead = R::kSteps < 8 ? R::kSteps : 8, kKeyAt = kHeld ? kAhead : 1;
+  static constexpr int kValueAt = !R::k16 || !kHeld ? 1 : R::kDB < 4 ? R::kDB : 4;
+  uint32_t key_at[kKeyAt];
+  uint32_t value_a[kValueAt], value_b[kValueAt];
+  __device__ __forceinline__ static uint32_t value_piece(const uint32_t (&at)[kValueAt], int db) {
+    return kHeld ? at[kHeld ? db : 0] : at[0] ^ (64 * db);
+  }
 
   // Tiles of keys and values start at these LDS addresses.
   __device__ __forceinline__ void place(uint32_t keys, uint32_t values) {
 #pragma unroll
-    for (int st = 0; st < kKeyAt; ++st)
-      key_at[st] = keys + r32 * R::kBytes + (((2 * st + hi) ^ R::swizzle_k(r32)) << 4);
+    for (int st = 0; st < kKeyAt; ++st) key_at[st] = keys + r32 * R::kBytes + (((2 * st) ^ R::swz(r32) ^ hi) << 4);
+    if constexpr (R::k16) {
+      const int j = lane & 15, g1 = (lane >> 4) & 1;
+      const int ra = 4 * hi + (j >> 2), rb = ra + 8;
+      const int c = 2 * g1 + ((j & 3) >> 1), tail = (j & 1) * 8;
 #pragma unroll
-    for (int db = 0; db < kValueAt; ++db) {
-      if constexpr (R::k16) {
-        const int j = lane & 15, row = 4 * hi + (j >> 2), piece = 4 * db + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
-        value_at[db] = values + row * R::kBytes + ((piece ^ R::swizzle_v(row)) << 4) + (j & 1) * 8;
-      } else {
-        const int row = 4 * hi, piece = 8 * db + (r32 >> 2);
-        value_at[db] = values + row * R::kBytes + ((piece ^ R::swizzle_v(row)) << 4) + (r32 & 3) * 4;
+      for (int db = 0; db < kValueAt; ++db) {
+        value_a[db] = values + ra * R::kBytes + tail + ((c ^ R::swz(ra) ^ (4 * db)) << 4);
+        value_b[db] = values + rb * R::kBytes + tail + ((c ^ R::swz(rb) ^ (4 * db)) << 4);
       }
+    } else {
+      value_a[0] = values;
     }
   }
   // On to another tile, whose address differs in the bits of `by`.
@@ -277,7 +271,10 @@ template <typename Elem, int DP> struct RowBlock {
   }
   __device__ __forceinline__ void move_values(uint32_t by) {
 #pragma unroll
-    for (int db = 0; db < kValueAt; ++db) value_at[db] ^= by;
+    for (int db = 0; db < kValueAt; ++db) {
+      value_a[db] ^= by;
+      if (R::k16) value_b[db] ^= by;
+    }
   }
 
   __device__ __forceinline__ void init(const AttendParams& p, const Work& w, int row_first) {
@@ -330,29 +327,23 @@ template <typename Elem, int DP> struct RowBlock {
     return (uint32_t)x;
   }
 
-  // Scores of the NS times 32 keys of the tile.  The blocks' products alternate,
-  // so that none waits for the one before it; the keys' operands are requested
-  // ahead of them.
-  template <int NS> __device__ __forceinline__ void scores(f32x16 (&s)[NS]) const {
+  // Scores of the 32 keys from row kFirst of the tile on.  The keys' operands
+  // are requested eight at a time ahead of their products.
+  template <int kFirst> __device__ __forceinline__ f32x16 scores() const {
+    f32x16 s;
 #pragma unroll
-    for (int b = 0; b < NS; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
-    constexpr int kAhead = kKeyAt / NS;
+    for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
     for (int s0 = 0; s0 < R::kSteps; s0 += kAhead) {
-      u32x4 a[NS][kAhead];
-#pragma unroll
-      for (int st = 0; st < kAhead; ++st)  // steps past the eighth: 256 bytes, the swizzle's range, further
-#pragma unroll
-        for (int b = 0; b < NS; ++b)
-          a[b][st] = *((lds_u32x4*)(lds_byte*)(uintptr_t)key_at[(s0 + st) % 8] +
-                       (b * kBlock * R::kBytes + (s0 + st) / 8 * 256) / 16);
+      u32x4 a[kAhead];
 #pragma unroll
       for (int st = 0; st < kAhead; ++st)
+        a[st] = *((lds_u32x4*)(lds_byte*)(uintptr_t)(kHeld ? key_at[kHeld ? st : 0] : key_at[0] ^ (32 * st)) +
+                  (kFirst * R::kBytes + 32 * s0) / 16);
 #pragma unroll
-        for (int b = 0; b < NS; ++b) s[b] = Mma32<Elem>::mma(a[b][st], q[s0 + st], s[b]);
+      for (int st = 0; st < kAhead; ++st) s = Mma32<Elem>::mma(a[st], q[s0 + st], s);
     }
+    return s;
   }
 
   // Running softmax over NS blocks of scores (-inf where masked): scores become
@@ -360,13 +351,19 @@ template <typename Elem, int DP> struct RowBlock {
   // measured from is moved only where a score passes it by kSlack powers of two:
   // sums and weights stay far from overflow (2^8 in fp16's 65504), and most tiles
   // leave the output as it is.
-  template <int NS> __device__ __forceinline__ void weigh(f32x16 (&s)[NS], float c) {
+  // `between` is called with 0 .. 3 at four places among the work, for loads to be
+  // issued there: a wave that issues several at once waits for each.
+  template <int NS, typename F> __device__ __forceinline__ void weigh(f32x16 (&s)[NS], float c, F between) {
     constexpr float kSlack = 8.0f;
-    float mx = s[0][0];
+    // four chains each for the maximum and the sum: an operation waits twice its
+    // own time for the one before it
+    float mx4[4] = {s[0][0], s[0][1], s[0][2], s[0][3]};
 #pragma unroll
     for (int b = 0; b < NS; ++b)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
+      for (int i = b ? 0 : 4; i < 16; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[b][i]);
+    float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+    between(0);
     mx = half_max(mx) * c;
     if (__any(mx > m + kSlack)) {
       const float mn = mx > m + kSlack ? mx : m;
@@ -379,15 +376,16 @@ template <typename Elem, int DP> struct RowBlock {
       m = mn;
     }
     const float ms = m == -INFINITY ? 0.f : m;
-    float sum = 0.f;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int b = 0; b < NS; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
+        if (16 * b + i > 0 && (16 * b + i) % (4 * NS) == 0) between((16 * b + i) / (4 * NS));
         s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, -ms));
-        sum += s[b][i];
+        sum[i & 3] += s[b][i];
       }
-    l += sum;
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
   }
 
   // -inf for the keys that this lane's row does not see.
@@ -426,10 +424,9 @@ template <typename Elem, int DP> struct RowBlock {
 #pragma unroll
         for (int db = 0; db < R::kDB; ++db) {
           // blocks past the fourth lie 256 bytes (the swizzle's range) further
-          lds_s16x4* at = (lds_s16x4*)(lds_byte*)(uintptr_t)value_at[db % 4] +
-                          ((kFirst + 16 * u) * R::kBytes + db / 4 * 256) / 8;
-          va[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at);
-          vc[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(at + R::kBytes);  // 8 rows further
+          const int off = ((kFirst + 16 * u) * R::kBytes + (db / 4) * 256) / 8;
+          va[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)(uintptr_t)value_piece(value_a, db % 4) + off);
+          vc[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)(uintptr_t)value_piece(value_b, db % 4) + off);
         }
 #pragma unroll
         for (int db = 0; db < R::kDB; ++db) {
@@ -445,14 +442,16 @@ template <typename Elem, int DP> struct RowBlock {
         }
       }
     } else {
+      const int c = (r32 >> 2) ^ (hi << 3);
+      const lds_byte* pr = (lds_byte*)(uintptr_t)(value_a[0] + 4 * hi * R::kBytes + (r32 & 3) * 4);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int key = 8 * (i >> 2) + (i & 3);  // + 4 hi
+        const int x = ((i & 3) << 1) | ((i >> 2) & 1);
         float v[R::kDB];
 #pragma unroll
         for (int db = 0; db < R::kDB; ++db) {
-          v[db] = *((lds_float*)(lds_byte*)(uintptr_t)value_at[db % 2] +
-                    ((kFirst + key) * R::kBytes + db / 2 * 256) / 4);
+          v[db] = *(lds_float*)(pr + ((((8 * db) & 8) ^ c ^ x) << 4) + (kFirst + key) * R::kBytes + (db / 2) * 256);
           if (ODD && (__float_as_uint(v[db]) & Mma32<Elem>::kExp) == Mma32<Elem>::kExp) v[db] = 0.f;
         }
         const uint32_t wi = p.w[i / 4][i % 4];
@@ -475,7 +474,7 @@ template <typename Elem, int DP> struct RowBlock {
 #pragma unroll
         for (int qd = 0; qd < 4; ++qd) {
           const int at = element(db, qd) * (int)sizeof(Elem);
-          const char* px = vb + k * R::kBytes + (((at >> 4) ^ R::swizzle_v(k)) << 4) + (at & 15);
+          const char* px = vb + k * R::kBytes + (((at >> 4) ^ R::swz(k)) << 4) + (at & 15);
           uint32_t x[4];
           if constexpr (R::k16) {
             const u32x2 h = *reinterpret_cast<const u32x2*>(px);
@@ -545,25 +544,45 @@ __device__ inline float* part_ml(const AttendParams& p, int split, int64_t row, 
 }
 
 // Store the rows of a block whose keys are all done: the output where the keys
-// are one chunk, else the chunk's part.
+// are one chunk, else the chunk's part.  A lane holds 4 elements here and there
+// of one row; they pass through `lds` (kBlock rows of DP floats, this wave's own),
+// so that a store of the wave covers whole rows, up to 128 elements at a time.
+// The 16-byte pieces of a row lie XOR-swizzled by row there, without which the 32
+// rows of a write would meet in the same banks.
+template <int DP> constexpr int kStoreBytes = kBlock * (DP < 128 ? DP : 128) * 4;
 template <typename Elem, int DP>
-__device__ __forceinline__ void store_rows(const AttendParams& p, const Work& w, const RowBlock<Elem, DP>& rb, float l) {
-  if (rb.row < 0) return;
+__device__ __forceinline__ void store_rows(const AttendParams& p, const Work& w, const RowBlock<Elem, DP>& rb, float l,
+                                           int row_first, char* lds) {
+  constexpr int kCols = DP < 128 ? DP : 128, kPieces = kCols / 4, kRowsAtOnce = 64 / kPieces;
   const bool whole = p.splits == 1;
   const float inv = whole ? inverse(l) : 1.0f;
+  f32x4* at = reinterpret_cast<f32x4*>(lds);
+  const int lane = rb.lane, piece = lane % kPieces;
 #pragma unroll
-  for (int db = 0; db < Rows<Elem, DP>::kDB; ++db)
+  for (int c0 = 0; c0 < DP; c0 += kCols) {
 #pragma unroll
-    for (int qd = 0; qd < 4; ++qd) {
-      const int at = rb.element(db, qd);
-      if (at >= p.d) continue;
-      f32x4 x = f32x4{rb.o[db][4 * qd], rb.o[db][4 * qd + 1], rb.o[db][4 * qd + 2], rb.o[db][4 * qd + 3]};
+    for (int db = 0; db < kCols / kBlock; ++db)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] *= inv;
-      if (whole) rb.store4(p, rb.row, rb.head, at, x);
-      else *reinterpret_cast<f32x4*>(part_o(p, w.split, rb.row, rb.head) + at) = x;
+      for (int qd = 0; qd < 4; ++qd) {
+        const f32x16& o = rb.o[c0 / kBlock + db];
+        const f32x4 x = f32x4{o[4 * qd] * inv, o[4 * qd + 1] * inv, o[4 * qd + 2] * inv, o[4 * qd + 3] * inv};
+        at[rb.r32 * kPieces + ((8 * db + 2 * qd + rb.hi) ^ (rb.r32 & 15))] = x;
+      }
+    wait_lds();
+    const int col = c0 + 4 * piece;
+    // (a loop: code that runs once is fetched at a miss of the instruction cache a line)
+#pragma unroll 2
+    for (int r0 = 0; r0 < kBlock; r0 += kRowsAtOnce) {
+      const int r = r0 + lane / kPieces, row = row_first + r;
+      const f32x4 x = at[r * kPieces + (piece ^ (r & 15))];
+      if (row >= w.rows || col >= p.d) continue;
+      const int node = (int)p.group.div((uint32_t)row), head = w.h * (int)p.group.d + row - node * (int)p.group.d;
+      if (whole) rb.store4(p, w.start + node, head, col, x);
+      else *reinterpret_cast<f32x4*>(part_o(p, w.split, w.start + node, head) + col) = x;
     }
-  if (rb.hi) return;
+    wait_lds();
+  }
+  if (rb.row < 0 || rb.hi) return;
   if (!whole) {
     float* ml = part_ml(p, w.split, rb.row, rb.head);
     ml[0] = rb.m;
@@ -620,11 +639,11 @@ template <typename Elem, int DP, int NL, bool HELD> struct TileRows {
 // Address of the 16-byte piece that this lane brings in load i: the rows'
 // addresses are in LDS at `rows`, row_0 is the tile's row of the first of them.
 template <typename Elem, int DP>
-__device__ __forceinline__ const char* piece_of(const AttendParams& p, const char* const* rows, bool is_v, int row_0,
-                                                int i, int lane) {
+__device__ __forceinline__ const char* piece_of(const AttendParams& p, const char* const* rows, int row_0, int i,
+                                                int lane) {
   using R = Rows<Elem, DP>;
   const int r = i * R::kPerLoad + lane / R::kPieces;
-  const int piece = (lane % R::kPieces) ^ (is_v ? R::swizzle_v(row_0 + r) : R::swizzle_k(row_0 + r));
+  const int piece = (lane % R::kPieces) ^ R::swz(row_0 + r);
   const char* at = rows[r];
   if (p.d != DP && piece * 16 >= p.d * (int)sizeof(Elem)) at = reinterpret_cast<const char*>(g_zero_row);
   return at + 16 * piece;
@@ -680,16 +699,16 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
     if constexpr (at.kHeld) {
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        at.k[i] = piece_of<Elem, DP>(p, s_row[wave], false, 0, i, lane);
-        at.v[i] = piece_of<Elem, DP>(p, s_row[wave] + 32, true, 0, i, lane);
+        at.k[i] = piece_of<Elem, DP>(p, s_row[wave], 0, i, lane);
+        at.v[i] = piece_of<Elem, DP>(p, s_row[wave] + 32, 0, i, lane);
       }
     }
   };
-  auto load = [&](const char* const* held, const char* const* rows, bool is_v, uint32_t lds) __attribute__((always_inline)) {
+  auto load = [&](const char* const* held, const char* const* rows, uint32_t lds) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NL; i += 2) {
-      const char* a = at.kHeld ? held[at.kHeld ? i : 0] : piece_of<Elem, DP>(p, rows, is_v, 0, i, lane);
-      const char* b = at.kHeld ? held[at.kHeld ? i + 1 : 0] : piece_of<Elem, DP>(p, rows, is_v, 0, i + 1, lane);
+      const char* a = at.kHeld ? held[at.kHeld ? i : 0] : piece_of<Elem, DP>(p, rows, 0, i, lane);
+      const char* b = at.kHeld ? held[at.kHeld ? i + 1 : 0] : piece_of<Elem, DP>(p, rows, 0, i + 1, lane);
       two_rows_to_lds<true>(a, b, lds + 1024 * i);
     }
   };
@@ -701,26 +720,25 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
     wait_loads<0>();
     find_rows(0, ahead[0]);
     valid = at.valid;
-    load(at.k, s_row[wave], false, k_lds);
+    load(at.k, s_row[wave], k_lds);
     fetch_ids(2, ahead[0]);
-    load(at.v, s_row[wave] + 32, true, v_lds);
+    load(at.v, s_row[wave] + 32, v_lds);
     find_rows(1, ahead[1]);
   }
   auto tile = [&](int t, auto tail) __attribute__((always_inline)) {
     constexpr bool kTail = decltype(tail)::value;
     const bool more = t + 1 < nt;
     wait_loads<NL>();  // keys of t and page numbers of t + 2 are there
-    f32x16 s[1];
-    rb.scores(s);
+    f32x16 s[1] = {rb.template scores<0>()};
     wait_lds();
     if (more) {
-      load(at.k, s_row[wave], false, k_lds);
+      load(at.k, s_row[wave], k_lds);
       fetch_ids(t + 3, ahead[1]);
     }
     uint32_t seen = valid;
     if constexpr (kTail) seen &= rb.sees(p, w, (int)first_key(t));
     if (__any(seen != ~0u)) rb.mask_scores(s[0], seen);
-    rb.weigh(s, c);
+    rb.weigh(s, c, [](int) {});
     if (more) wait_loads<NL + 1>();
     else wait_loads<0>();
     if (kTail && __any(seen != valid) && rb.any_odd(vbuf, kBlock)) {
@@ -732,7 +750,7 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
     wait_lds();
     valid = at.valid;
     if (more) {
-      load(at.v, s_row[wave] + 32, true, v_lds);
+      load(at.v, s_row[wave] + 32, v_lds);
       find_rows(t + 2, ahead[0]);
       ahead[0] = ahead[1];
     }
@@ -801,7 +819,7 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
 // More rows: four waves of 32 rows share tiles of KT keys, double buffered; a
 // wave fetches a quarter of each tile's rows.
 template <typename Elem, int DP, int KT>
-__global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWideWaves)) void attend_wide_kernel(AttendParams p) {
+__global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
   constexpr int NS = KT / kBlock;
   constexpr int kTile = KT * R::kBytes;
@@ -810,6 +828,7 @@ __global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWideWaves)) void attend
   static_assert(kMine % R::kPerLoad == 0 && NL >= 1, "");
   // (a multiple of its two tiles' distance, so that an XOR changes tiles)
   __shared__ __attribute__((aligned(4 * kTile))) char s_kv[2][2 * kTile];
+  static_assert(4 * kStoreBytes<DP> <= 4 * kTile, "");
   __shared__ __attribute__((aligned(16))) const char* s_row[4][64];
   __shared__ int s_id[4][2][64];
   __shared__ uint32_t s_valid[4][4];
@@ -846,8 +865,8 @@ __global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWideWaves)) void attend
     const char* a[2 * NL];
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      a[i] = piece_of<Elem, DP>(p, s_row[wave], false, wave * kMine, i, lane);
-      a[NL + i] = piece_of<Elem, DP>(p, s_row[wave] + kMine, true, wave * kMine, i, lane);
+      a[i] = piece_of<Elem, DP>(p, s_row[wave], wave * kMine, i, lane);
+      a[NL + i] = piece_of<Elem, DP>(p, s_row[wave] + kMine, wave * kMine, i, lane);
     }
 #pragma unroll
     for (int i = 0; i < NL; i += 2) two_rows_to_lds<false>(a[i], a[i + 1], to + 1024 * i);
@@ -876,7 +895,8 @@ __global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWideWaves)) void attend
     if (!idle) {
       f32x16 s[NS];
       uint32_t seen[NS], valid[NS];
-      rb.scores(s);
+      s[0] = rb.template scores<0>();
+      if constexpr (NS == 2) s[1] = rb.template scores<kBlock>();
       bool uneven = false;
 #pragma unroll
       for (int b = 0; b < NS; ++b) {
@@ -892,7 +912,7 @@ __global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWideWaves)) void attend
 #pragma unroll
       for (int b = 0; b < NS; ++b)
         if (__any(seen[b] != ~0u)) rb.mask_scores(s[b], seen[b]);
-      rb.weigh(s, c);
+      rb.weigh(s, c, [](int) {});
       const char* vb = s_kv[t & 1] + kTile;
       if (kTail && uneven && rb.any_odd(vb, KT)) {
         rb.template add_values<kTail, 0>(rb.pack(s[0]));
@@ -918,7 +938,8 @@ __global__ __launch_bounds__(kThreads, (Rows<Elem, DP>::kWideWaves)) void attend
   for (; t < nf; ++t) tile(t, No{});
   for (; t < nt; ++t) tile(t, Yes{});
 
-  store_rows(p, w, rb, half_sum(rb.l));
+  __syncthreads();
+  store_rows(p, w, rb, half_sum(rb.l), w.row0 + wave * kBlock, &s_kv[0][0] + wave * kStoreBytes<DP>);
 }
 
 // Rows of 16-bit heads up to 128 elements and fp32 heads up to 64: eight waves
@@ -963,19 +984,18 @@ __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
 
   // lane 16 i + 8 v + r finds row r of this wave's eighth of the i-th of four
   // stages, of the keys (v = 0) and of the values
-  auto page_of = [&](int four, int lane, int& col) {
-    return page_at(p, (int64_t)w.k0 + ((int64_t)four * 4 + (lane >> 4)) * KT + wave * kMine + (lane & 7), w.k1, col);
+  const int my_v = (lane >> 3) & 1;
+  PageAt ahead;
+  auto position = [&](int four) {
+    return (int64_t)w.k0 + ((int64_t)four * 4 + (lane >> 4)) * KT + wave * kMine + (lane & 7);
   };
   auto fetch_ids = [&](int four) {
     int col;
-    const PageAt a = page_of(four, lane_again(), col);
-    word_to_lds(entry_of(p, w.b, a, col), (uint32_t)(uintptr_t)s_id[wave][four & 1]);
+    ahead = page_at(p, position(four), w.k1, col);
+    word_to_lds(entry_of(p, w.b, ahead, col), (uint32_t)(uintptr_t)s_id[wave][four & 1]);
   };
-  auto find_rows = [&](int four) {
-    const int lane = lane_again();
-    int col;
-    const PageAt a = page_of(four, lane, col);
-    const HeadAt h = head_at<Elem>(p, w.h, (lane >> 3) & 1);
+  auto find_rows = [&](int four, const PageAt& a) {
+    const HeadAt h = head_at<Elem>(p, w.h, my_v);
     const uint32_t id = (uint32_t)s_id[wave][four & 1][lane];
     const bool valid = a.in_table && id < (uint64_t)p.cache.n_pages && (int)id >= 0;
     s_row[wave][lane] =
@@ -983,23 +1003,18 @@ __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
     const uint64_t all = __ballot(valid);
     if ((lane & 15) == 0) s_valid[(four * 4 + (lane >> 4)) & 7][wave] = (uint8_t)(all >> lane);
   };
-  const char* next[2 * NL];  // of the stage to be fetched next
-  auto find_pieces = [&](int t) {
-    const int lane = lane_again();
-    const char* const* rows = s_row[wave] + 16 * (t & 3);
-#pragma unroll
-    for (int i = 0; i < 2 * NL; ++i) {
-      const int of = (i % NL) * R::kPerLoad + lane / R::kPieces, r = wave * kMine + of;
-      const int piece = (lane % R::kPieces) ^ (i < NL ? R::swizzle_k(r) : R::swizzle_v(r));
-      next[i] = rows[(i / NL) * kMine + of];
-      if (p.d != DP && piece * 16 >= p.d * (int)sizeof(Elem)) next[i] = reinterpret_cast<const char*>(g_zero_row);
-      next[i] += 16 * piece;
-    }
-  };
   auto load_stage = [&](int t) {
     const uint32_t to = (uint32_t)(uintptr_t)s_kv[t % kRing] + wave * kMine * R::kBytes;
+    const char* const* rows = s_row[wave] + 16 * (t & 3);
+    const char* a[2 * NL];
 #pragma unroll
-    for (int i = 0; i < 2 * NL; ++i) row_to_lds(next[i], to + (i / NL) * kTile + 1024 * (i % NL));
+    for (int i = 0; i < 2 * NL; ++i) a[i] = rows[(i / NL) * kMine + (i % NL) * R::kPerLoad + lane / R::kPieces];
+#pragma unroll
+    for (int i = 0; i < 2 * NL; ++i) {
+      const int piece = (lane % R::kPieces) ^ R::swz(wave * kMine + (i % NL) * R::kPerLoad + lane / R::kPieces);
+      if (p.d != DP && piece * 16 >= p.d * (int)sizeof(Elem)) a[i] = reinterpret_cast<const char*>(g_zero_row);
+      row_to_lds(a[i] + 16 * piece, to + (i / NL) * kTile + 1024 * (i % NL));
+    }
   };
 
   f32x16 s[NS];
@@ -1007,60 +1022,31 @@ __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
   uint32_t seen[NS];
   bool odd = false;
   uint32_t keys_in = 0, values_in = 0;  // ring places that the operand addresses are at
-  auto to_values = [&](int t) __attribute__((always_inline)) {
-    const uint32_t at = (uint32_t)t % kRing;
-    rb.move_values((values_in ^ at) * kStage);
-    values_in = at;
-  };
-  auto add = [&](auto with_odd) __attribute__((always_inline)) {
-    rb.template add_values<decltype(with_odd)::value, 0>(weights[0]);
-    if constexpr (NS == 2) rb.template add_values<decltype(with_odd)::value, kBlock>(weights[1]);
-  };
-  auto score = [&](int t) __attribute__((always_inline)) {
-    const uint32_t at = (uint32_t)t % kRing;
-    rb.move_keys((keys_in ^ at) * kStage);
-    keys_in = at;
-    rb.scores(s);
-  };
-  // the values of stage t (of the tail: some may be no finite numbers)
-  auto add_tail = [&](int t) __attribute__((always_inline)) {
-    to_values(t);
-    if (odd) {
-      add(Yes{});
-      const char* vb = s_kv[t % kRing] + kTile + part * kBlock * R::kBytes;
-      rb.add_odd(vb, seen[0]);
-      if constexpr (NS == 2) rb.add_odd(vb + kBlock * R::kBytes, seen[1]);
-    } else {
-      add(No{});
-    }
-  };
-  // The matrix half step: the values of stage t - 1, the scores of stage t.
-  auto multiply = [&](int t, auto tail) __attribute__((always_inline)) {
+  auto multiply = [&](int t, bool values, bool scores, auto tail) __attribute__((always_inline)) {
     if (idle) return;
-    if (t == 0) {
-      score(t);
-    } else if constexpr (decltype(tail)::value) {
-      add_tail(t - 1);
-      score(t);
-    } else {
-      to_values(t - 1);
-      add(No{});
-      score(t);
-      if constexpr (R::k16) {
-        // operands are requested six reads ahead of the products all through:
-        // left alone, the compiler saves registers and waits for most of them
-        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
-#pragma unroll
-        for (int i = 0; i < NS * 2 * R::kDB; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    if (values) {
+      const uint32_t at = (uint32_t)(t - 1) % kRing;
+      rb.move_values((values_in ^ at) * kStage);
+      values_in = at;
+      if (decltype(tail)::value && odd) {
+        const char* vb = s_kv[at] + kTile + part * kBlock * R::kBytes;
+        rb.template add_values<decltype(tail)::value, 0>(weights[0]);
+        rb.add_odd(vb, seen[0]);
+        if constexpr (NS == 2) {
+          rb.template add_values<decltype(tail)::value, kBlock>(weights[1]);
+          rb.add_odd(vb + kBlock * R::kBytes, seen[1]);
         }
-#pragma unroll
-        for (int i = 0; i < NS * R::kSteps; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
+      } else {
+        rb.template add_values<false, 0>(weights[0]);
+        if constexpr (NS == 2) rb.template add_values<false, kBlock>(weights[1]);
       }
+    }
+    if (scores) {
+      const uint32_t at = (uint32_t)t % kRing;
+      rb.move_keys((keys_in ^ at) * kStage);
+      keys_in = at;
+      s[0] = rb.template scores<0>();
+      if constexpr (NS == 2) s[1] = rb.template scores<kBlock>();
     }
   };
   auto soften = [&](int t, auto tail) __attribute__((always_inline)) {
@@ -1081,7 +1067,7 @@ __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
         rb.mask_scores(s[b], valid);
       }
     }
-    rb.weigh(s, c);
+    rb.weigh(s, c, [](int) {});
 #pragma unroll
     for (int b = 0; b < NS; ++b) weights[b] = rb.pack(s[b]);
     if constexpr (decltype(tail)::value)
@@ -1091,28 +1077,25 @@ __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
     const bool more = t + 2 < nt, ask = more && (t & 3) == 3;
     if (more) load_stage(t + 2);
     if (ask) fetch_ids((t >> 2) + 2);
-    multiply(t, tail);
+    multiply(t, t > 0, true, tail);
     // this wave's part of stage t + 1, and what was asked for before this step
     if (ask) wait_loads<2 * NL + 1>();
     else if (more) wait_loads<2 * NL>();
     else wait_loads<0>();
     lds_barrier();
     soften(t, tail);
-    if (more && (t & 3) == 1) find_rows((t >> 2) + 1);
-    if (t + 3 < nt) find_pieces(t + 3);
+    if (more && (t & 3) == 1) find_rows((t >> 2) + 1, ahead);
     lds_barrier();
   };
 
   if (nt > 0) {
     fetch_ids(0);
+    const PageAt first = ahead;
     fetch_ids(1);
     wait_loads<0>();
-    find_rows(0);
-    find_pieces(0);
+    find_rows(0, first);
     load_stage(0);
-    find_pieces(1);
     load_stage(1);
-    find_pieces(2);
     wait_loads<2 * NL>();  // all but stage 1
     rb.place((uint32_t)(uintptr_t)s_kv[0] + part * kBlock * R::kBytes,
              (uint32_t)(uintptr_t)s_kv[0] + kTile + part * kBlock * R::kBytes);
@@ -1121,15 +1104,17 @@ __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
     int t = 0;
     for (; t < nf; ++t) step(t, No{});
     for (; t < nt; ++t) step(t, Yes{});
-    if (!idle) add_tail(nt - 1);
+    multiply(nt, true, false, Yes{});
     if (!late) lds_barrier();
   }
 
+  constexpr int kOut = (R::kDB * 4 + 1) * 1024;  // a block's outputs, maxima and sums in LDS
+  static_assert((KG == 1 ? 8 * kStoreBytes<DP> : 4 * kOut) <= kRing * kStage && kStoreBytes<DP> <= kOut, "");
   float l = half_sum(rb.l);
   if constexpr (KG == 2) {
     // the second group's outputs pass through LDS; nothing is in flight any more
     __syncthreads();
-    f32x4* red = reinterpret_cast<f32x4*>(s_kv[0]) + block * (R::kDB * 4 + 1) * 64;
+    f32x4* red = reinterpret_cast<f32x4*>(&s_kv[0][0] + block * kOut);
     if (late) {
 #pragma unroll
       for (int db = 0; db < R::kDB; ++db)
@@ -1155,7 +1140,10 @@ __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
         for (int e = 0; e < 4; ++e) rb.o[db][4 * qd + e] = rb.o[db][4 * qd + e] * f + x[e] * g;
       }
   }
-  store_rows(p, w, rb, l);
+  // (each wave's LDS lies where it read the other group's outputs, or where no one
+  // reads any more)
+  if constexpr (KG == 1) __syncthreads();
+  store_rows(p, w, rb, l, w.row0 + block * kBlock, &s_kv[0][0] + block * (KG == 1 ? kStoreBytes<DP> : kOut));
 }
 
 // Join a row's chunks, in their order: one wave a row, 4 elements a lane, the
@@ -1243,7 +1231,9 @@ AttendPlan attend_plan(int elem, int32_t B, int32_t max_nodes, int32_t max_conte
   if (chunk < kMinChunk) chunk = kMinChunk;
   const int64_t fewest = ceil_div(keys * units, kMaxGroups);
   if (chunk < fewest) chunk = fewest;
-  chunk = ceil_div(chunk, 256) * 256;
+  // even chunks of whole stages (128 keys are one block of each narrow wave)
+  const int64_t unit = a.kind == Kind::kNarrow ? 4 * kBlock : 2 * kBlock;
+  chunk = ceil_div(ceil_div(keys, ceil_div(keys, chunk)), unit) * unit;
   if (chunk > ((int64_t)1 << 30)) chunk = (int64_t)1 << 30;
   a.chunk = (int32_t)chunk;
   a.splits = (int32_t)ceil_div(keys, chunk);
@@ -1276,6 +1266,10 @@ hipError_t launch(AttendParams p, hipStream_t stream) {
   p.chunk = a.chunk;
   p.splits = a.splits;
   p.row_tiles = a.row_tiles;
+  p.by_tiles = fast_div((uint32_t)a.row_tiles);
+  p.by_splits = fast_div((uint32_t)a.splits);
+  p.by_heads = fast_div((uint32_t)p.hk);
+  p.by_chunk = fast_div((uint32_t)a.chunk);
   hipError_t e = p.d <= 64    ? launch_d<Elem, 64>(p, a.kind, stream)
                  : p.d <= 128 ? launch_d<Elem, 128>(p, a.kind, stream)
                               : launch_d<Elem, 256>(p, a.kind, stream);
