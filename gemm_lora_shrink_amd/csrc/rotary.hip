@@ -10,6 +10,8 @@
 // to nothing, so it is bound by memory, or for a decode batch by its chain of
 // loads: the token's position, then its row of the table.  The x loads do not
 // wait for that chain.
+#include <cmath>
+
 #include "attention.h"
 
 namespace lora {
@@ -24,25 +26,40 @@ struct TableParams {
   float* table;
   int64_t first, n;
   double magnitude;
-  int32_t half;
+  int32_t half, run;  // positions of a thread
   FastDiv by_half;
   double turns[LORA_MAX_HEAD_DIM / 2];  // frequency / (2 pi)
+  double step[LORA_MAX_HEAD_DIM];       // cosine and sine of the frequency
 };
 
-// One thread a pair: the position times the frequency, in turns, is reduced to
-// its fraction in 64 bits before cosine and sine, so that a far position loses
-// nothing but the product's own rounding (2^-53 of the turns).
+// A thread fills `run` positions of one pair.  At the first, the position times
+// the frequency, in turns, is reduced to its fraction in 64 bits before cosine
+// and sine, so that a far position loses nothing but the product's own rounding
+// (2^-53 of the turns); from there on a position turns the one before it by the
+// frequency, in 64 bits too: four products in place of a cosine and a sine, for
+// 2^-52 more a step, far below the table's own 2^-24.
+// With a cosine, a sine and a 64-bit division at every position the kernel was
+// bound by those: 29.0 us for 131072 positions of 64 pairs (67 MB).
 __global__ __launch_bounds__(kThreads) void rope_table_kernel(TableParams p) {
-  const int64_t total = p.n * p.half;
-  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < total; e += (int64_t)gridDim.x * kThreads) {
-    const int64_t pos = e / p.half;
-    const int i = (int)(e - pos * p.half);
-    const double turns = (double)(p.first + pos) * p.turns[i];
-    double s, c;
-    sincospi(2.0 * (turns - rint(turns)), &s, &c);
-    float* row = p.table + pos * 2 * p.half;
-    row[i] = (float)(c * p.magnitude);
-    row[p.half + i] = (float)(s * p.magnitude);
+  const uint32_t e = blockIdx.x * kThreads + threadIdx.x, r = p.by_half.div(e);
+  const int i = (int)(e - r * p.by_half.d);
+  const int64_t pos = (int64_t)r * p.run;
+  const int n = (int)(p.n - pos < p.run ? p.n - pos : p.run);
+  if (n <= 0) return;
+  const double turns = (double)(p.first + pos) * p.turns[i], dc = p.step[2 * i], ds = p.step[2 * i + 1];
+  double s, c;
+  sincospi(2.0 * (turns - rint(turns)), &s, &c);
+  s *= p.magnitude;
+  c *= p.magnitude;
+  float* row = p.table + pos * 2 * p.half + i;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    row[0] = (float)c;
+    row[p.half] = (float)s;
+    row += 2 * p.half;
+    const double next = c * dc - s * ds;
+    s = s * dc + c * ds;
+    c = next;
   }
 }
 
@@ -331,10 +348,16 @@ hipError_t launch_rope_table(const double* inv_freq, int32_t rot, double magnitu
   p.n = n;
   p.magnitude = magnitude;
   p.half = rot / 2;
-  for (int i = 0; i < p.half; ++i) p.turns[i] = inv_freq[i] / 6.283185307179586476925286766559;
-  const int64_t blocks = ceil_div(n * p.half, kThreads);
-  hipLaunchKernelGGL(rope_table_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(kThreads), 0, stream,
-                     p);
+  p.by_half = fast_div((uint32_t)p.half);
+  for (int i = 0; i < p.half; ++i) {
+    p.turns[i] = inv_freq[i] / 6.283185307179586476925286766559;
+    p.step[2 * i] = std::cos(inv_freq[i]);
+    p.step[2 * i + 1] = std::sin(inv_freq[i]);
+  }
+  p.run = 8;
+  while (ceil_div(n, p.run) * p.half > ((int64_t)1 << 30)) p.run *= 2;  // the kernel counts in 32 bits
+  hipLaunchKernelGGL(rope_table_kernel, dim3((unsigned)ceil_div(ceil_div(n, p.run) * p.half, kThreads)), dim3(kThreads),
+                     0, stream, p);
   return hipGetLastError();
 }
 
