@@ -1173,15 +1173,30 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendParams p) {
   const float ms = M == -INFINITY ? 0.f : M;
   float L = 0.f;
   f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int s = lane / lanes; s < splits; s += 64 / lanes) {
-    const float* ml = part_ml(p, s, row, h);
-    const float f = __builtin_amdgcn_exp2f(ml[0] - ms);
-    const float l = ml[1];
-    if (l == 0.f) continue;
-    const f32x4 x = ldf4_or0(part_o(p, s, row, h) + at, ok);
-    L = __builtin_fmaf(l, f, L);
+  // four chunks' loads at a time: one by one, each waited for the one before it
+  // (13.3 -> 8.1 us for 2048 rows of 32 chunks, 33 MB)
+  constexpr int kAhead = 4;
+  const int step = 64 / lanes;
+  for (int s = lane / lanes; s < splits; s += kAhead * step) {
+    float m[kAhead], l[kAhead];
+    f32x4 x[kAhead];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(x[e], f, sum[e]);
+    for (int i = 0; i < kAhead; ++i) {
+      const bool there = s + i * step < splits;
+      const int si = there ? s + i * step : s;
+      const float* ml = part_ml(p, si, row, h);
+      m[i] = ml[0];
+      l[i] = there ? ml[1] : 0.f;
+      x[i] = ldf4_or0(part_o(p, si, row, h) + at, ok);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const bool any = l[i] != 0.f;  // the chunk has keys that the row sees
+      const float f = any ? __builtin_amdgcn_exp2f(m[i] - ms) : 0.f;
+      L = __builtin_fmaf(l[i], f, L);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(any ? x[i][e] : 0.f, f, sum[e]);
+    }
   }
   for (int o = lanes; o < 64; o <<= 1) {
     L += __shfl_xor(L, o);
