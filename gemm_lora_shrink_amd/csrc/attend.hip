@@ -190,23 +190,38 @@ __device__ inline int splits_of(const AttendParams& p, int n, int ctx) {
   return s;
 }
 
-// Units of work lie in the order sequence, head, chunk, row tile; the workgroups
-// of one XCD (b % 8) take a contiguous range, so the row tiles of a chunk read
-// its keys through one L2.
-template <int ROWS>
+// Units of work are (chunk, sequence, head), in that order.
+// SPREAD: they go to the XCDs (b % 8) in turn.  The first chunks, the long ones
+// where contexts differ, are on all XCDs from the start: 24.9 us for 33 with the
+// order below for 8 fp32 sequences of 46 to 1500 keys, 351 for 359 for 256 bf16
+// ones of 128 to 4096.
+// Else an XCD takes a contiguous range of the order sequence, head, chunk: heads
+// side by side in memory are read through one L2, which is worth more where the
+// matrix cores bound the time: 148 us for 156 for 16 sequences of 256 to 8192
+// keys and 23 to 45 nodes, 65.5 for 68.7 for one of 32768 keys and 64 nodes.
+// Either way the row tiles of a unit follow one another on one XCD.
+template <int ROWS, bool SPREAD>
 __device__ inline Work work_of(const AttendParams& p) {
   Work w;
-  const int per = (int)(gridDim.x / kXcds);
-  uint32_t u = (blockIdx.x % kXcds) * (uint32_t)per + blockIdx.x / kXcds, v = p.by_tiles.div(u);
-  const int rt = (int)(u - v * p.by_tiles.d);
-  u = v;
-  v = p.by_splits.div(u);
-  w.split = (int)(u - v * p.by_splits.d);
-  u = v;
+  const uint32_t xcd = blockIdx.x % kXcds, j = blockIdx.x / kXcds, of_xcd = p.by_tiles.div(j);
+  const int rt = (int)(j - of_xcd * p.by_tiles.d);
+  uint32_t u = SPREAD ? of_xcd * kXcds + xcd : xcd * p.by_tiles.div(gridDim.x / kXcds) + of_xcd, v;
+  if constexpr (!SPREAD) {
+    v = p.by_splits.div(u);
+    w.split = (int)(u - v * p.by_splits.d);
+    u = v;
+  }
   v = p.by_heads.div(u);
   w.h = (int)(u - v * p.by_heads.d);
-  w.b = (int)v;
-  w.none = w.b >= p.B;
+  if constexpr (SPREAD) {
+    u = v;
+    v = p.by_sequences.div(u);
+    w.b = (int)(u - v * p.by_sequences.d);
+    w.split = (int)v;
+  } else {
+    w.b = (int)v;
+  }
+  w.none = SPREAD ? w.split >= p.splits : w.b >= p.B;
   if (w.none) return w;
   sequence_of(p, w.b, w.start, w.n, w.ctx);
   const int group = (int)p.group.d;
@@ -665,7 +680,7 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
   __shared__ int s_id[NW][2][64];
   __shared__ float s_ml[NW][2][kBlock];
   warm_args(p);
-  const Work w = work_of<kBlock>(p);
+  const Work w = work_of<kBlock, true>(p);
   if (w.none) return;
   RowBlock<Elem, DP> rb;
   rb.init(p, w, w.row0);
@@ -833,7 +848,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p
   __shared__ int s_id[4][2][64];
   __shared__ uint32_t s_valid[4][4];
   warm_args(p);
-  const Work w = work_of<4 * kBlock>(p);
+  const Work w = work_of<4 * kBlock, true>(p);
   if (w.none) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RowBlock<Elem, DP> rb;
@@ -969,7 +984,7 @@ __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
   __shared__ int s_id[8][2][64];
   __shared__ __attribute__((aligned(8))) uint8_t s_valid[8][8];
   warm_args(p);
-  const Work w = work_of<32 * 8 / KG>(p);
+  const Work w = work_of<32 * 8 / KG, false>(p);
   if (w.none) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int late = wave >> 2;                        // the group that runs behind
@@ -1258,8 +1273,7 @@ AttendPlan attend_plan(int elem, int32_t B, int32_t max_nodes, int32_t max_conte
 template <typename Elem, int DP>
 hipError_t launch_d(const AttendParams& p, Kind kind, hipStream_t stream) {
   constexpr int kRow = DP * (int)sizeof(Elem);
-  const int64_t units = (int64_t)p.B * p.hk * p.splits * p.row_tiles;
-  const int64_t grid = ceil_div(units, kXcds) * kXcds;
+  const int64_t grid = ceil_div((int64_t)p.B * p.hk * p.splits, kXcds) * kXcds * p.row_tiles;
   if (grid > (int64_t)0x7fffffff) return hipErrorInvalidConfiguration;
   const dim3 g((unsigned)grid);
   if (kind == Kind::kNarrow) {
@@ -1283,6 +1297,7 @@ hipError_t launch(AttendParams p, hipStream_t stream) {
   p.row_tiles = a.row_tiles;
   p.by_tiles = fast_div((uint32_t)a.row_tiles);
   p.by_splits = fast_div((uint32_t)a.splits);
+  p.by_sequences = fast_div((uint32_t)p.B);
   p.by_heads = fast_div((uint32_t)p.hk);
   p.by_chunk = fast_div((uint32_t)a.chunk);
   hipError_t e = p.d <= 64    ? launch_d<Elem, 64>(p, a.kind, stream)

@@ -84,7 +84,7 @@ struct AttendParams {
   float* part;    // workspace
   // filled by the launcher (AttendPlan)
   int32_t chunk, splits, row_tiles;
-  FastDiv by_tiles, by_splits, by_heads, by_chunk;
+  FastDiv by_tiles, by_splits, by_sequences, by_heads, by_chunk;
 };
 
 hipError_t launch_rope_table(const double* inv_freq, int32_t rot, double magnitude, int64_t first, int64_t n,
