@@ -2,7 +2,7 @@
 //
 // For one sequence and one key/value head the rows are its nodes times the
 // query heads of the group; all of them read the same keys, so a workgroup
-// takes up to 128 rows of one (sequence, key/value head) over one chunk of the
+// takes up to 256 rows of one (sequence, key/value head) over one chunk of the
 // keys, and a second launch joins the chunks where there are several.  With m
 // the running maximum and l the running sum of a row, a tile of scores s
 // changes them by
@@ -670,6 +670,12 @@ __device__ __forceinline__ const char* piece_of(const AttendParams& p, const cha
 // keys are on their way during the weights and values of this one, its values
 // during the next scores; page numbers come through LDS three blocks ahead,
 // addresses are found two blocks ahead.
+// Bound by memory: 256 sequences of 128 to 4096 keys, 32 + 8 bf16 heads of 128
+// (2.2 GB): 352 us, 6.3 TB/s.  One workgroup a compute unit, 16 KB in flight a
+// wave; two push each other's rows out of L2 (4.9 TB/s).  Loads are non-temporal,
+// each row is read once.  fp32 heads of 64 have too little in flight in one
+// workgroup and run two a compute unit: 33 us for 36 (8 sequences of 46 to 1500
+// keys).  Heads of 256 elements spill some registers: 64 x 8192 keys (1.07 GB) 263 us.
 template <typename Elem, int DP, int NW>
 __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void attend_narrow_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
@@ -831,8 +837,11 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
   }
 }
 
-// More rows: four waves of 32 rows share tiles of KT keys, double buffered; a
-// wave fetches a quarter of each tile's rows.
+// More rows of more than 256 bytes (fp32 heads from 72 elements, 16-bit ones from
+// 136), whose outputs leave no registers for the kernel below: four waves of 32
+// rows share tiles of KT keys, double buffered; a wave fetches a quarter of each
+// tile's rows.  One workgroup a compute unit.  Bound by the matrix cores and the
+// weights in turn.
 template <typename Elem, int DP, int KT>
 __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
@@ -969,6 +978,14 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p
 // t + 2 into the ring place that stage t - 2 left one half step ago.  The row
 // addresses of four stages are found together, one a lane, at the second step of
 // the four before; their page numbers are requested two steps earlier.
+// Bound by the issue of a stage's work, matrix products (0.5 us a group), weights
+// (0.5), the loads' issue and addresses (0.4): 2.8 us a stage of 64 keys with every
+// compute unit at work, 2.3 with all keys in L2.  One sequence of 64 nodes over
+// 32768 keys, 32 + 8 bf16 heads of 128: 67 us (134 MB, 34 GFLOP, 8 of them in the
+// join); 32 sequences of 64 over 4032: 190 us, 710 TFLOP/s.  Measured and slower:
+// all eight waves in step (75 for 71 us on the first), the loads spread over the
+// products (78) or over the weights (72), chunks for two workgroups a compute unit
+// in turn (89).
 template <typename Elem, int DP, int KG>
 __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
@@ -1236,10 +1253,12 @@ struct AttendPlan {
   int32_t chunk, splits, row_tiles;
 };
 
-// How the keys are cut: chunks so long that about so many workgroups run in all
-// as the chip holds at once (two a compute unit of the wide kernel, one of the
-// one with turns; the narrow kernel's take turns on four), where every sequence
-// is as long as its bound, and no shorter than kMinChunk keys.
+// How the keys are cut: even chunks, so long that about `groups` workgroups run
+// in all where every sequence is as long as its bound, and no shorter than
+// kMinChunk keys.  One workgroup a compute unit of the kernel with turns, whose
+// prologue, last join and parts cost 25 us a workgroup; two of the wide one; four of
+// the narrow one (64 x 8192 keys: 175 us, with eight 185; one sequence of 131072:
+// 42, with eight 53).
 constexpr int64_t kMinChunk = 256;
 constexpr int64_t kMaxGroups = (int64_t)1 << 30;
 

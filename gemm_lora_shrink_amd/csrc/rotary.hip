@@ -9,7 +9,10 @@
 // The pass moves 2 (q_heads + 2 kv_heads) d elements a token and computes next
 // to nothing, so it is bound by memory, or for a decode batch by its chain of
 // loads: the token's position, then its row of the table.  The x loads do not
-// wait for that chain.
+// wait for that chain.  Measured: 8192 tokens of 32 + 2 x 8 bf16 heads of 128 with
+// norms 43.5 us (201 MB, 4.6 TB/s, a large copy's rate); 4097 tokens of 16 + 2 x 16
+// fp16 heads of 256, 64 elements rotated, 42.7 us (201 MB); 64 tokens of 32 + 2 x 8
+// 11 us, the time of the call on the host.
 #include <cmath>
 
 #include "attention.h"
@@ -39,7 +42,7 @@ struct TableParams {
 // frequency, in 64 bits too: four products in place of a cosine and a sine, for
 // 2^-52 more a step, far below the table's own 2^-24.
 // With a cosine, a sine and a 64-bit division at every position the kernel was
-// bound by those: 29.0 us for 131072 positions of 64 pairs (67 MB).
+// bound by those: 29.0 us for 131072 positions of 64 pairs (67 MB), now 14.2 (4.7 TB/s).
 __global__ __launch_bounds__(kThreads) void rope_table_kernel(TableParams p) {
   const uint32_t e = blockIdx.x * kThreads + threadIdx.x, r = p.by_half.div(e);
   const int i = (int)(e - r * p.by_half.d);
