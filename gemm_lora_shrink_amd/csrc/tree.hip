@@ -83,15 +83,18 @@ __global__ __launch_bounds__(kThreads) void build_tree_kernel(BuildTreeParams p)
   }
 }
 
-// One workgroup a (layer's K or V, head, sequence).  Destination j never lies
+// One workgroup a (layer's K or V, kKeepHeads heads, sequence).  Destination j never lies
 // past its source path[j] >= j, and the sources ascend, so taking the entries
 // in rounds, each read whole before it is written, never overwrites a row that
-// is still to be read.  All layers are one launch, which is what bounds the call: 64
-// sequences, 16 layers of 8 bf16 heads of 128 take 15 us with the host's part.
-__global__ __launch_bounds__(kThreads) void keep_path_kernel(KeepParams p, int n_layers) {
-  const int b = blockIdx.x, h = blockIdx.y, z = blockIdx.z;
+// is still to be read.  All layers are one launch.  A head's rows are some 1 KB, far
+// less than a workgroup costs to start: 64 sequences, 16 layers of 8 bf16 heads of
+// 128 (34 MB) took 23.8 us with a workgroup each, 15.8 with four heads in one.
+constexpr int kKeepHeads = 4;
+__global__ __launch_bounds__(kThreads) void keep_path_kernel(KeepParams p, int kv_heads) {
+  const int b = blockIdx.x, h0 = (int)blockIdx.y * kKeepHeads, z = blockIdx.z;
   const int layer = z >> 1;
-  char* base = static_cast<char*>(z & 1 ? p.v[layer] : p.k[layer]) + (int64_t)h * (z & 1 ? p.v_head : p.k_head);
+  const int64_t head_b = z & 1 ? p.v_head : p.k_head;
+  char* base = static_cast<char*>(z & 1 ? p.v[layer] : p.k[layer]) + h0 * head_b;
   const int64_t page_b = z & 1 ? p.v_page : p.k_page, row_b = z & 1 ? p.v_row : p.k_row;
   const int64_t ctx = p.context[b];
   int n = p.n_kept[b];
@@ -121,15 +124,22 @@ __global__ __launch_bounds__(kThreads) void keep_path_kernel(KeepParams p, int n
   };
   for (int j0 = 0; j0 < n; j0 += rows) {
     const int j = j0 + r;
-    u32x4 x = u32x4{0, 0, 0, 0};
+    u32x4 x[kKeepHeads];
+    const char* of = nullptr;
     char* to = nullptr;
     if (r < rows && j < n && path[j] != j) {
-      const char* of = at(ctx + path[j]);
+      of = at(ctx + path[j]);
       to = of ? at(ctx + j) : nullptr;
-      if (to) x = *reinterpret_cast<const u32x4*>(of);
     }
+    if (to)
+#pragma unroll
+      for (int i = 0; i < kKeepHeads; ++i)  // (past the last head: the last again)
+        x[i] = *reinterpret_cast<const u32x4*>(of + min(i, kv_heads - 1 - h0) * head_b);
     __syncthreads();
-    if (to) *reinterpret_cast<u32x4*>(to) = x;
+    if (to)
+#pragma unroll
+      for (int i = 0; i < kKeepHeads; ++i)
+        if (h0 + i < kv_heads) *reinterpret_cast<u32x4*>(to + i * head_b) = x[i];
     __syncthreads();
   }
 }
@@ -142,8 +152,9 @@ hipError_t launch_build_tree(const BuildTreeParams& p, hipStream_t stream) {
 }
 
 hipError_t launch_keep_path(const KeepParams& p, int32_t n_layers, int32_t kv_heads, int32_t B, hipStream_t stream) {
-  hipLaunchKernelGGL(keep_path_kernel, dim3((unsigned)B, (unsigned)kv_heads, (unsigned)(2 * n_layers)), dim3(kThreads),
-                     0, stream, p, n_layers);
+  hipLaunchKernelGGL(keep_path_kernel, 
+                     dim3((unsigned)B, (unsigned)ceil_div(kv_heads, kKeepHeads), (unsigned)(2 * n_layers)),
+                     dim3(kThreads), 0, stream, p, kv_heads);
   return hipGetLastError();
 }
 
