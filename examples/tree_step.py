@@ -135,4 +135,5 @@ if __name__ == "__main__":
     ap.add_argument("--norm", action="store_true")
     args = ap.parse_args()
     tree, single = run({"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[args.dtype], args.norm)
-    print(f"{len(tree)} rows, largest difference {float((tree - single).abs().max()):.3g} of {float(single.abs().max()):.3g}")
+    off, most = float((tree - single).abs().max()), float(single.abs().max())
+    print(f"{len(tree)} rows, largest difference {off:.3g} of {most:.3g}")

@@ -186,8 +186,8 @@ __device__ inline void sequence_of(const AttendParams& p, int b, int64_t& start,
   ctx = x < 0 ? 0 : (x > p.max_context ? p.max_context : x);
 }
 __device__ inline int splits_of(const AttendParams& p, int n, int ctx) {
-  const int s = (int)p.by_chunk.div((uint32_t)ctx + (uint32_t)n - 1u < 0x7fffffffu ? (uint32_t)ctx + (uint32_t)n - 1u : 0u) + 1;
-  return s;
+  const int last = ctx + n - 1;
+  return last < 0 ? 1 : (int)p.by_chunk.div((uint32_t)last) + 1;
 }
 
 // Units of work are (chunk, sequence, head), in that order.
@@ -440,8 +440,10 @@ template <typename Elem, int DP> struct RowBlock {
         for (int db = 0; db < R::kDB; ++db) {
           // blocks past the fourth lie 256 bytes (the swizzle's range) further
           const int off = ((kFirst + 16 * u) * R::kBytes + (db / 4) * 256) / 8;
-          va[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)(uintptr_t)value_piece(value_a, db % 4) + off);
-          vc[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)(uintptr_t)value_piece(value_b, db % 4) + off);
+          va[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_s16x4*)(lds_byte*)(uintptr_t)value_piece(value_a, db % 4) + off);
+          vc[db] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_s16x4*)(lds_byte*)(uintptr_t)value_piece(value_b, db % 4) + off);
         }
 #pragma unroll
         for (int db = 0; db < R::kDB; ++db) {
@@ -1335,7 +1337,8 @@ int64_t attend_need_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_c
                           int32_t d) {
   // the same for every type of the call
   int64_t splits = 1;
-  for (int elem : {2, 4}) splits = std::max<int64_t>(splits, attend_plan(elem, B, max_nodes, max_context, hq, hk, d).splits);
+  for (int elem : {2, 4})
+    splits = std::max<int64_t>(splits, attend_plan(elem, B, max_nodes, max_context, hq, hk, d).splits);
   if (splits == 1) return 0;
   const int64_t bytes = splits * T * hq * (d + 2) * 4;
   return (bytes + 255) & ~int64_t(255);
