@@ -170,6 +170,7 @@ struct Work {
   int b, h, n, ctx;    // sequence, key/value head, nodes, context
   int row0, rows;      // this workgroup's first row (node * group + head) and the sequence's rows
   int k0, k1, split;   // keys [k0, k1)
+  bool whole;          // the sequence's keys are one chunk
   bool none;           // nothing to do
 };
 
@@ -227,7 +228,9 @@ __device__ inline Work work_of(const AttendParams& p) {
   const int group = (int)p.group.d;
   w.row0 = rt * ROWS;
   w.rows = w.n * group;
-  w.none = w.row0 >= w.rows || w.split >= splits_of(p, w.n, w.ctx);
+  const int splits = splits_of(p, w.n, w.ctx);
+  w.whole = splits == 1;
+  w.none = w.row0 >= w.rows || w.split >= splits;
   const int last = min(w.row0 + ROWS, w.rows) - 1;
   const int end = w.ctx + (p.mask ? w.n : min(w.n, (int)p.group.div((uint32_t)max(last, 0)) + 1));
   const int64_t k0 = (int64_t)w.split * p.chunk;
@@ -560,8 +563,8 @@ __device__ inline float* part_ml(const AttendParams& p, int split, int64_t row, 
   return p.part + (int64_t)p.splits * p.T * p.hq * p.d + (((int64_t)split * p.T + row) * p.hq + head) * 2;
 }
 
-// Store the rows of a block whose keys are all done: the output where the keys
-// are one chunk, else the chunk's part.  A lane holds 4 elements here and there
+// Store the rows of a block whose keys are all done: the output where the sequence's
+// keys are one chunk, else the chunk's part.  A lane holds 4 elements here and there
 // of one row; they pass through `lds` (kBlock rows of DP floats, this wave's own),
 // so that a store of the wave covers whole rows, up to 128 elements at a time.
 // The 16-byte pieces of a row lie XOR-swizzled by row there, without which the 32
@@ -571,7 +574,7 @@ template <typename Elem, int DP>
 __device__ __forceinline__ void store_rows(const AttendParams& p, const Work& w, const RowBlock<Elem, DP>& rb, float l,
                                            int row_first, char* lds) {
   constexpr int kCols = DP < 128 ? DP : 128, kPieces = kCols / 4, kRowsAtOnce = 64 / kPieces;
-  const bool whole = p.splits == 1;
+  const bool whole = w.whole;
   const float inv = whole ? inverse(l) : 1.0f;
   f32x4* at = reinterpret_cast<f32x4*>(lds);
   const int lane = rb.lane, piece = lane % kPieces;
@@ -808,7 +811,7 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
     L += s_ml[i][1][rb.r32] * f[i];
   }
   if (rb.row < 0) return;
-  const bool whole = p.splits == 1;
+  const bool whole = w.whole;
   const float inv = whole ? inverse(L) : 1.0f;
   for (int db = wave; db < R::kDB; db += NW) {
 #pragma unroll
@@ -1192,8 +1195,8 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendParams p) {
   sequence_of(p, b, start, n, ctx);
   const int r = (int)blockIdx.x * (kThreads / 64) + (int)(threadIdx.x >> 6);
   const int i = r / p.hq, h = r - i * p.hq;
-  if (i >= n) return;
   const int splits = splits_of(p, n, ctx);
+  if (i >= n || splits == 1) return;  // one chunk: its workgroup wrote the output
   const int64_t row = start + i;
   const int lane = threadIdx.x & 63;
   int lanes = 1;  // lanes of one chunk: a power of two
