@@ -979,8 +979,8 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p
 // one wave of each kind.  KG = 1: the eight waves hold 256 rows and all take a
 // stage's 64 keys.  KG = 2: the groups hold the same 128 rows and take 32 keys of
 // a stage each; their outputs meet at the end.
-// Stages are in a ring of four: at step t a wave fetches its eighth of stage
-// t + 2 into the ring place that stage t - 2 left one half step ago.  The row
+// Stages are in a ring of four: before the weights of step t a wave fetches its
+// eighth of stage t + 2 into the ring place that stage t - 2 left.  The row
 // addresses of four stages are found together, one a lane, at the second step of
 // the four before; their page numbers are requested two steps earlier.
 // Bound by the issue of a stage's work, matrix products (0.5 us a group), weights
@@ -988,9 +988,10 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p
 // compute unit at work, 2.3 with all keys in L2.  One sequence of 64 nodes over
 // 32768 keys, 32 + 8 bf16 heads of 128: 67 us (134 MB, 34 GFLOP, 8 of them in the
 // join); 32 sequences of 64 over 4032: 190 us, 710 TFLOP/s.  Measured and slower:
-// all eight waves in step (75 for 71 us on the first), the loads spread over the
-// products (78) or over the weights (72), chunks for two workgroups a compute unit
-// in turn (89).
+// all eight waves in step (75 for 71 us on the first), the loads before the products
+// (66 for 64; 143 for 132 on 16 ragged sequences), spread over the products (78) or
+// over the weights (72), chunks for two workgroups a compute unit in turn (89), no
+// priority for the products (132 for 130 on the ragged ones) or the weights' (155).
 template <typename Elem, int DP, int KG>
 __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
@@ -1112,14 +1113,15 @@ __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
   };
   auto step = [&](int t, auto tail) __attribute__((always_inline)) {
     const bool more = t + 2 < nt, ask = more && (t & 3) == 3;
-    if (more) load_stage(t + 2);
     if (ask) fetch_ids((t >> 2) + 2);
+    __builtin_amdgcn_s_setprio(1);
     multiply(t, t > 0, true, tail);
+    __builtin_amdgcn_s_setprio(0);
     // this wave's part of stage t + 1, and what was asked for before this step
-    if (ask) wait_loads<2 * NL + 1>();
-    else if (more) wait_loads<2 * NL>();
+    if (ask) wait_loads<1>();
     else wait_loads<0>();
     lds_barrier();
+    if (more) load_stage(t + 2);
     soften(t, tail);
     if (more && (t & 3) == 1) find_rows((t >> 2) + 1, ahead);
     lds_barrier();
