@@ -676,11 +676,11 @@ __device__ __forceinline__ const char* piece_of(const AttendParams& p, const cha
 // during the next scores; page numbers come through LDS three blocks ahead,
 // addresses are found two blocks ahead.
 // Bound by memory: 256 sequences of 128 to 4096 keys, 32 + 8 bf16 heads of 128
-// (2.2 GB): 352 us, 6.3 TB/s.  One workgroup a compute unit, 16 KB in flight a
+// (2.2 GB): 350 us, 6.3 TB/s.  One workgroup a compute unit, 16 KB in flight a
 // wave; two push each other's rows out of L2 (4.9 TB/s).  Loads are non-temporal,
 // each row is read once.  fp32 heads of 64 have too little in flight in one
 // workgroup and run two a compute unit: 33 us for 36 (8 sequences of 46 to 1500
-// keys).  Heads of 256 elements spill some registers: 64 x 8192 keys (1.07 GB) 263 us.
+// keys).  Heads of 256 elements spill some registers: 64 x 8192 keys (1.07 GB) 253 us.
 template <typename Elem, int DP, int NW>
 __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void attend_narrow_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
@@ -846,7 +846,8 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
 // 136), whose outputs leave no registers for the kernel below: four waves of 32
 // rows share tiles of KT keys, double buffered; a wave fetches a quarter of each
 // tile's rows.  One workgroup a compute unit.  Bound by the matrix cores and the
-// weights in turn.
+// weights in turn, heads of 256 elements by spilled registers too (fp32: 228 a
+// lane; 3 sequences of 12 nodes over 1949 keys, 32 + 8 fp32 heads: 229 us).
 template <typename Elem, int DP, int KT>
 __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
@@ -984,10 +985,10 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p
 // addresses of four stages are found together, one a lane, at the second step of
 // the four before; their page numbers are requested two steps earlier.
 // Bound by the issue of a stage's work, matrix products (0.5 us a group), weights
-// (0.5), the loads' issue and addresses (0.4): 2.8 us a stage of 64 keys with every
-// compute unit at work, 2.3 with all keys in L2.  One sequence of 64 nodes over
-// 32768 keys, 32 + 8 bf16 heads of 128: 67 us (134 MB, 34 GFLOP, 8 of them in the
-// join); 32 sequences of 64 over 4032: 190 us, 710 TFLOP/s.  Measured and slower:
+// (0.5), the loads' issue and addresses (0.4): 2.6 us a stage of 64 keys with every
+// compute unit at work, of which keys in L2 save a fifth.  One sequence of 64 nodes
+// over 32768 keys, 32 + 8 bf16 heads of 128: 63 us (134 MB, 34 GFLOP; 8 us are the
+// join); 32 sequences of 64 over 4032: 178 us, 760 TFLOP/s.  Measured and slower:
 // all eight waves in step (75 for 71 us on the first), the loads before the products
 // (66 for 64; 143 for 132 on 16 ragged sequences), spread over the products (78) or
 // over the weights (72), chunks for two workgroups a compute unit in turn (89), no
