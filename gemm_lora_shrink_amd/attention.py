@@ -122,7 +122,9 @@ def _int_rows(t, name, dev, rows):
     n, cols, ld = _matrix(t, name, _I32, dev)
     if n != rows:
         raise _bad(f"{name} must have {rows} rows (it has {n})")
-    return t.data_ptr(), ld if ld > cols else cols, cols
+    if ld < cols:
+        raise _bad(f"the rows of {name} overlap: {cols} columns, row stride {ld} (an expanded row, say)")
+    return t.data_ptr(), ld, cols
 
 
 _CACHE_FIELDS = struct.Struct("@PP7qi")  # lora_kv_cache
