@@ -15,7 +15,9 @@ adapters' q/k/v projection in a serving step.
 Caches are tensors [n_pages, kv_heads, page_size, head_dim] with unit inner
 stride; a cache kept as [n_pages, page_size, kv_heads, head_dim] is passed as
 its transpose(1, 2).  As in the rest of the package, argument checks raise
-LoraError and every computation runs in the library's HIP kernels.
+LoraError and every computation runs in the library's HIP kernels.  With
+stream= another stream than torch's current one, the tensors that a call
+returns are made on that stream.
 """
 
 import ctypes
@@ -94,6 +96,16 @@ def _gpu(t, name):
 def _stream_of(stream, dev):
     """The stream's handle: `stream`, or the current one of GPU `dev`."""
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _made(stream, make, *args, **kw):
+    """make(*args, **kw), a new tensor, on the stream of the call that it is for:
+    a fill on the current stream would not be ordered with the call on another,
+    and a block that was freed there may still be in use."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
 
 
 def _matrix(t, name, dtype, dev):
@@ -182,7 +194,7 @@ def rope_table(n, rot_dim, *, base=10000.0, scaling=None, frequencies=None, magn
     elif len(frequencies) != rot_dim // 2:
         raise _bad("one frequency for each pair")
     if out is None:
-        out = torch.empty((n, rot_dim), dtype=torch.float32, device=device)
+        out = _made(stream, torch.empty, (n, rot_dim), dtype=_F32, device=device)
     if tuple(out.shape) != (n, rot_dim):
         raise _bad(f"out must be [{n}, {rot_dim}]")
     dev = _gpu(out, "the table")
@@ -295,19 +307,19 @@ def build_tree(parents, q_start, context, *, max_nodes, n_tokens=None, page_tabl
         raise _bad("n_tokens is needed where parents is None")
     words = 0
     if parents is not None and mask is None:
-        mask = torch.zeros((T, max(-(-max_nodes // 64), 1)), dtype=_I64, device=device)
+        mask = _made(stream, torch.zeros, (T, max(-(-max_nodes // 64), 1)), dtype=_I64, device=device)
     if mask is not None:
         if mask.dim() != 2 or mask.size(0) != T:
             raise _bad(f"mask must have {T} rows")
         _vector(mask, "mask", _I64, dev, mask.numel())
         words = mask.size(1)
     if positions is None:
-        positions = torch.full((T,), -1, dtype=_I32, device=device)
+        positions = _made(stream, torch.full, (T,), -1, dtype=_I32, device=device)
     table = (None, 0, 0)
     if page_table is not None:
         table = _int_rows(page_table, "page_table", dev, B)
         if cache_rows is None:
-            cache_rows = torch.full((T,), -1, dtype=_I32, device=device)
+            cache_rows = _made(stream, torch.full, (T,), -1, dtype=_I32, device=device)
     elif cache_rows is not None:
         raise _bad("cache_rows needs a page_table")
     _check(_lib().lora_build_tree(
@@ -357,7 +369,7 @@ def tree_attention(q, k_cache, v_cache, page_table, context, q_start, *, max_nod
         raise _bad(f"q must be rows of whole heads of {d}")
     q_heads = width // d
     if out is None:
-        out = torch.empty((T, width), dtype=dtype, device=q.device)
+        out = _made(stream, torch.empty, (T, width), dtype=dtype, device=q.device)
     To, wo, ldo = _matrix(out, "out", dtype, dev)
     if To != T or wo != width:
         raise _bad("out must have q's shape")

@@ -1,5 +1,9 @@
 """What the binding of include/lora_attention.h makes of its arguments before
-they reach the library: strides of integer matrices."""
+they reach the library: strides of integer matrices, and the streams of the
+tensors it makes itself."""
+
+from contextlib import contextmanager
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -55,3 +59,87 @@ def test_calls_with_overlapping_rows_are_refused():
             with pytest.raises(glsa.LoraError, match="overlap"):
                 call()
     glsa.keep_path(k, v, good, context, path, kept)
+
+
+# ---- tensors that the binding makes: on the call's stream ----------------------
+
+class _NoLibrary:
+    """Every entry point succeeds and does nothing."""
+
+    def __getattr__(self, name):
+        return lambda *args: glsa.LORA_OK
+
+
+@pytest.fixture
+def made_on(monkeypatch):
+    """The binding without a GPU; lists the stream that each new tensor is made on."""
+    streams, made = [None], []
+
+    @contextmanager
+    def stream(s):
+        streams.append(s)
+        yield
+        streams.pop()
+
+    def recorded(make):
+        def call(*args, **kw):
+            made.append(streams[-1])
+            return make(*args, **kw)
+        return call
+
+    for name in ("empty", "zeros", "full"):
+        monkeypatch.setattr(torch, name, recorded(getattr(torch, name)))
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(A, "_gpu", lambda t, name: HOST)
+    monkeypatch.setattr(A, "_bound", _NoLibrary())
+    monkeypatch.setattr(A, "_lib", lambda: A._bound)
+    return made
+
+
+def test_tensors_are_made_on_the_stream_of_the_call(made_on):
+    """A fill on the current stream would not be ordered with the kernel on another."""
+    side = SimpleNamespace(cuda_stream=1)
+    ints = torch.tensor([0, 2], dtype=torch.int32)
+    table, context = torch.tensor([[0]], dtype=torch.int32), torch.tensor([3], dtype=torch.int32)
+    q, cache = torch.ones(2, 8), torch.ones(1, 1, 8, 8)
+    glsa.build_tree(ints - 1, ints, context, max_nodes=2, page_table=table, n_pages=1, page_size=8, stream=side)
+    assert made_on == [side] * 3
+    del made_on[:]
+    glsa.tree_attention(q, cache, cache, table, context, ints, max_nodes=2, stream=side)
+    assert made_on == [side]
+    del made_on[:]
+    glsa.rope_table(4, 8, frequencies=[1.0] * 4, device="cpu", stream=side)
+    assert made_on == [side]
+
+
+@pytest.mark.gpu
+def test_calls_on_a_stream_beside_a_busy_one():
+    """Work queued on the current stream before a call on another one has no part
+    in what the call gives."""
+    B, n, hq, d, page = 2, 5, 2, 64, 8
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    parents, start, context = ints([-1, 0, 0, 2, 1] * B), ints([0, n, 2 * n]), ints([9, 20])
+    pages = ints([[0, 1, 2, 3], [4, 5, 6, 7]])
+    g = torch.Generator("cuda").manual_seed(0)
+    q = torch.randn(B * n, hq * d, device="cuda", generator=g)
+    k, v = (torch.randn(8, 1, page, d, device="cuda", generator=g) for _ in range(2))
+    big = torch.ones(8192, 8192, device="cuda", dtype=torch.bfloat16)
+    side = torch.cuda.Stream()
+
+    def step(stream):
+        mask, pos, rows = glsa.build_tree(parents, start, context, max_nodes=n, page_table=pages, n_pages=8,
+                                          page_size=page, stream=stream)
+        out = glsa.tree_attention(q, k, v, pages, context, start, max_nodes=n, mask=mask, stream=stream)
+        return mask, pos, rows, out, glsa.rope_table(64, 32, stream=stream)
+
+    want = [t.cpu() for t in step(None)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for _ in range(40):
+            busy = big @ big  # some 40 ms of the current stream
+        got = step(side)
+        with torch.cuda.stream(side):
+            got = [t.cpu() for t in got]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert bool((want[0] != 0).all() and (want[1] >= 0).all() and (want[2] >= 0).all()) and busy.numel()
