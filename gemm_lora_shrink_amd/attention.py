@@ -332,12 +332,15 @@ def build_tree(parents, q_start, context, *, max_nodes, n_tokens=None, page_tabl
 
 
 def attention_workspace_bytes(n_seqs, n_tokens, max_nodes, max_context, q_heads, kv_heads, head_dim):
+    """Bytes that suffice for every tree_attention call of these heads, of any
+    type, with at most n_seqs sequences, n_tokens rows, max_nodes and max_context."""
     return int(_lib().lora_tree_attention_workspace_bytes(n_seqs, n_tokens, max_nodes, max_context, q_heads, kv_heads,
                                                           head_dim))
 
 
 def alloc_attention_workspace(n_seqs, n_tokens, max_nodes, max_context, q_heads, kv_heads, head_dim, device):
-    """A workspace for tree_attention calls of these sizes (uint8, maybe empty)."""
+    """A workspace for tree_attention calls of these sizes or smaller ones of the
+    same heads (uint8, maybe empty)."""
     n = attention_workspace_bytes(n_seqs, n_tokens, max_nodes, max_context, q_heads, kv_heads, head_dim)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     if ws.data_ptr() % 256:
@@ -358,7 +361,8 @@ def tree_attention(q, k_cache, v_cache, page_table, context, q_start, *, max_nod
     defaults to what the page table holds).  scale defaults to
     head_dim ** -0.5.  lse (optional, float32 [T, q_heads]) receives the
     logarithm of the softmax sums.  workspace: from alloc_attention_workspace
-    for these sizes or larger ones of the same heads; None where it is empty."""
+    for these sizes or larger ones of the same heads, so one for the largest batch
+    serves all; None where it is empty."""
     dev, dtype = _gpu(q, "q"), q.dtype
     code = _DTYPES.get(dtype)
     if code is None:

@@ -555,12 +555,17 @@ struct Yes {
 
 __device__ inline float inverse(float l) { return l == 0.f ? 0.f : 1.0f / l; }
 
-// The workspace: for each chunk and row the unnormalised output and (m, l).
+// The workspace: for each chunk and row the unnormalised output and (m, l).  It has
+// part_rows rows a chunk: the call's T, or where T is more than the sequences can
+// have (a padded batch) max_nodes of each sequence.
+__device__ inline int64_t part_row(const AttendParams& p, int b, int64_t start, int node) {
+  return (p.part_rows < p.T ? (int64_t)b * p.max_nodes : start) + node;
+}
 __device__ inline float* part_o(const AttendParams& p, int split, int64_t row, int head) {
-  return p.part + (((int64_t)split * p.T + row) * p.hq + head) * p.d;
+  return p.part + (((int64_t)split * p.part_rows + row) * p.hq + head) * p.d;
 }
 __device__ inline float* part_ml(const AttendParams& p, int split, int64_t row, int head) {
-  return p.part + (int64_t)p.splits * p.T * p.hq * p.d + (((int64_t)split * p.T + row) * p.hq + head) * 2;
+  return p.part + (int64_t)p.splits * p.part_rows * p.hq * p.d + (((int64_t)split * p.part_rows + row) * p.hq + head) * 2;
 }
 
 // Store the rows of a block whose keys are all done: the output where the sequence's
@@ -598,13 +603,13 @@ __device__ __forceinline__ void store_rows(const AttendParams& p, const Work& w,
       if (row >= w.rows || col >= p.d) continue;
       const int node = (int)p.group.div((uint32_t)row), head = w.h * (int)p.group.d + row - node * (int)p.group.d;
       if (whole) rb.store4(p, w.start + node, head, col, x);
-      else *reinterpret_cast<f32x4*>(part_o(p, w.split, w.start + node, head) + col) = x;
+      else *reinterpret_cast<f32x4*>(part_o(p, w.split, part_row(p, w.b, w.start, node), head) + col) = x;
     }
     wait_lds();
   }
   if (rb.row < 0 || rb.hi) return;
   if (!whole) {
-    float* ml = part_ml(p, w.split, rb.row, rb.head);
+    float* ml = part_ml(p, w.split, part_row(p, w.b, w.start, rb.node), rb.head);
     ml[0] = rb.m;
     ml[1] = l;
   } else if (p.lse) {
@@ -828,12 +833,12 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[e] *= inv;
       if (whole) rb.store4(p, rb.row, rb.head, at, sum);
-      else *reinterpret_cast<f32x4*>(part_o(p, w.split, rb.row, rb.head) + at) = sum;
+      else *reinterpret_cast<f32x4*>(part_o(p, w.split, part_row(p, w.b, w.start, rb.node), rb.head) + at) = sum;
     }
   }
   if (wave == 0 && rb.hi == 0) {
     if (!whole) {
-      float* ml = part_ml(p, w.split, rb.row, rb.head);
+      float* ml = part_ml(p, w.split, part_row(p, w.b, w.start, rb.node), rb.head);
       ml[0] = M;
       ml[1] = L;
     } else if (p.lse) {
@@ -1200,14 +1205,14 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendParams p) {
   const int i = r / p.hq, h = r - i * p.hq;
   const int splits = splits_of(p, n, ctx);
   if (i >= n || splits == 1) return;  // one chunk: its workgroup wrote the output
-  const int64_t row = start + i;
+  const int64_t row = start + i, of = part_row(p, b, start, i);
   const int lane = threadIdx.x & 63;
   int lanes = 1;  // lanes of one chunk: a power of two
   while (lanes * 4 < p.d) lanes *= 2;
   const int at = 4 * (lane % lanes);
   const bool ok = at < p.d;
   float M = -INFINITY;
-  for (int s = lane; s < splits; s += 64) M = fmaxf(M, part_ml(p, s, row, h)[0]);
+  for (int s = lane; s < splits; s += 64) M = fmaxf(M, part_ml(p, s, of, h)[0]);
 #pragma unroll
   for (int o = 32; o; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
   const float ms = M == -INFINITY ? 0.f : M;
@@ -1224,10 +1229,10 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendParams p) {
     for (int i = 0; i < kAhead; ++i) {
       const bool there = s + i * step < splits;
       const int si = there ? s + i * step : s;
-      const float* ml = part_ml(p, si, row, h);
+      const float* ml = part_ml(p, si, of, h);
       m[i] = ml[0];
       l[i] = there ? ml[1] : 0.f;
-      x[i] = ldf4_or0(part_o(p, si, row, h) + at, ok);
+      x[i] = ldf4_or0(part_o(p, si, of, h) + at, ok);
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
@@ -1259,7 +1264,23 @@ enum class Kind { kNarrow, kTurns128, kTurns256, kWide };
 struct AttendPlan {
   Kind kind;
   int32_t chunk, splits, row_tiles;
+  int64_t groups;  // workgroups to be had from cutting the keys
 };
+AttendPlan attend_kind(int elem, int32_t nodes, int32_t group, int32_t d) {
+  AttendPlan a{};
+  const int64_t rows = (int64_t)nodes * group;
+  const int row_bytes = elem * (d <= 64 ? 64 : d <= 128 ? 128 : 256);
+  int64_t tile = kBlock;
+  a.groups = 1024;
+  a.kind = Kind::kNarrow;
+  if (rows > kBlock) {
+    a.kind = row_bytes > 256 ? Kind::kWide : rows > 4 * kBlock ? Kind::kTurns256 : Kind::kTurns128;
+    tile = a.kind == Kind::kTurns256 ? 8 * kBlock : 4 * kBlock;
+    a.groups = a.kind == Kind::kWide ? 512 : 256;
+  }
+  a.row_tiles = (int32_t)ceil_div(rows, tile);
+  return a;
+}
 
 // How the keys are cut: even chunks, so long that about `groups` workgroups run
 // in all where every sequence is as long as its bound, and no shorter than
@@ -1268,34 +1289,30 @@ struct AttendPlan {
 // the narrow one (64 x 8192 keys: 175 us, with eight 185; one sequence of 131072:
 // 42, with eight 53).
 constexpr int64_t kMinChunk = 256;
-constexpr int64_t kMaxGroups = (int64_t)1 << 30;
+constexpr int64_t kMaxGroups = (int64_t)1 << 30, kMaxChunk = (int64_t)1 << 30;
 
 AttendPlan attend_plan(int elem, int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
                        int32_t d) {
-  AttendPlan a;
-  const int64_t rows = (int64_t)max_nodes * (hq / hk), keys = (int64_t)max_context + max_nodes;
-  const int row_bytes = elem * (d <= 64 ? 64 : d <= 128 ? 128 : 256);
-  int64_t tile = kBlock, groups = 1024;
-  a.kind = Kind::kNarrow;
-  if (rows > kBlock) {
-    a.kind = row_bytes > 256 ? Kind::kWide : rows > 4 * kBlock ? Kind::kTurns256 : Kind::kTurns128;
-    tile = a.kind == Kind::kTurns256 ? 8 * kBlock : 4 * kBlock;
-    groups = a.kind == Kind::kWide ? 512 : 256;
-  }
-  a.row_tiles = (int32_t)ceil_div(rows, tile);
+  AttendPlan a = attend_kind(elem, max_nodes, hq / hk, d);
+  const int64_t keys = (int64_t)max_context + max_nodes;
   const int64_t units = (int64_t)B * hk * a.row_tiles;
-  int64_t chunk = ceil_div(keys * units, groups);
+  int64_t chunk = ceil_div(keys * units, a.groups);
   if (chunk < kMinChunk) chunk = kMinChunk;
   const int64_t fewest = ceil_div(keys * units, kMaxGroups);
   if (chunk < fewest) chunk = fewest;
   // even chunks of whole stages (128 keys are one block of each narrow wave)
   const int64_t unit = a.kind == Kind::kNarrow ? 4 * kBlock : 2 * kBlock;
   chunk = ceil_div(ceil_div(keys, ceil_div(keys, chunk)), unit) * unit;
-  if (chunk > ((int64_t)1 << 30)) chunk = (int64_t)1 << 30;
+  if (chunk > kMaxChunk) chunk = kMaxChunk;
   a.chunk = (int32_t)chunk;
   a.splits = (int32_t)ceil_div(keys, chunk);
   return a;
 }
+
+int32_t part_rows_of(int32_t B, int32_t T, int32_t max_nodes) {
+  return (int32_t)std::min<int64_t>(T, (int64_t)B * max_nodes);
+}
+int64_t part_bytes(int64_t rows, int32_t hq, int32_t d) { return (rows * hq * (d + 2) * 4 + 255) & ~int64_t(255); }
 
 template <typename Elem, int DP>
 hipError_t launch_d(const AttendParams& p, Kind kind, hipStream_t stream) {
@@ -1322,6 +1339,7 @@ hipError_t launch(AttendParams p, hipStream_t stream) {
   p.chunk = a.chunk;
   p.splits = a.splits;
   p.row_tiles = a.row_tiles;
+  p.part_rows = part_rows_of(p.B, p.T, p.max_nodes);
   p.by_tiles = fast_div((uint32_t)a.row_tiles);
   p.by_splits = fast_div((uint32_t)a.splits);
   p.by_sequences = fast_div((uint32_t)p.B);
@@ -1339,15 +1357,44 @@ hipError_t launch(AttendParams p, hipStream_t stream) {
 
 }  // namespace
 
-int64_t attend_need_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
+int64_t attend_need_bytes(lora_dtype dt, int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq,
+                          int32_t hk, int32_t d) {
+  const int64_t splits = attend_plan(dt == LORA_F32 ? 4 : 2, B, max_nodes, max_context, hq, hk, d).splits;
+  return splits == 1 ? 0 : part_bytes(splits * part_rows_of(B, T, max_nodes), hq, d);
+}
+
+// Fewer sequences or nodes are cut into more chunks, so the bytes of a call do not
+// grow with its sizes; these are the most of any call up to them.  With G workgroups
+// to be had and u = sequences * kv_heads * row tiles a call has at most ceil(keys /
+// kMinChunk) and ceil(G / u) chunks (2^30 keys at most a chunk), both largest at the
+// most keys; rows only grow.  What is left is to try the numbers of sequences and,
+// of the nodes, those that fill their row tiles.
+int64_t attend_most_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
                           int32_t d) {
-  // the same for every type of the call
-  int64_t splits = 1;
-  for (int elem : {2, 4})
-    splits = std::max<int64_t>(splits, attend_plan(elem, B, max_nodes, max_context, hq, hk, d).splits);
-  if (splits == 1) return 0;
-  const int64_t bytes = splits * T * hq * (d + 2) * 4;
-  return (bytes + 255) & ~int64_t(255);
+  const int32_t group = hq / hk;
+  const int64_t keys = (int64_t)max_context + max_nodes, by_keys = ceil_div(keys, kMinChunk);
+  const int64_t uncut = ceil_div(keys, kMaxChunk);
+  int64_t most = uncut > 1 ? uncut * part_rows_of(B, T, max_nodes) : 0;
+  const auto nodes_up_to = [&](int elem, int64_t nodes) {
+    if (nodes < 1) return;
+    nodes = std::min<int64_t>(nodes, max_nodes);
+    const AttendPlan a = attend_kind(elem, (int32_t)nodes, group, d);
+    const int64_t per = (int64_t)hk * a.row_tiles;
+    for (int64_t b = 1; b <= B && b * per < a.groups; ++b) {
+      const int64_t splits = std::max(std::min(by_keys, ceil_div(a.groups, b * per)), uncut);
+      if (splits > 1) most = std::max(most, splits * part_rows_of((int32_t)b, T, (int32_t)nodes));
+    }
+  };
+  for (int elem : {2, 4}) {
+    nodes_up_to(elem, kBlock / group);
+    for (int64_t tiles = 1; tiles * hk < 512; ++tiles) {
+      nodes_up_to(elem, tiles * 4 * kBlock / group);
+      nodes_up_to(elem, tiles * 8 * kBlock / group);
+      if (tiles * 4 * kBlock / group >= max_nodes) break;
+    }
+    nodes_up_to(elem, max_nodes);
+  }
+  return part_bytes(most, hq, d);
 }
 
 hipError_t launch_attend(lora_dtype dt, const AttendParams& p, hipStream_t stream) {

@@ -83,7 +83,7 @@ struct AttendParams {
   FastDiv group;  // by q_heads / kv_heads
   float* part;    // workspace
   // filled by the launcher (AttendPlan)
-  int32_t chunk, splits, row_tiles;
+  int32_t chunk, splits, row_tiles, part_rows;
   FastDiv by_tiles, by_splits, by_sequences, by_heads, by_chunk;
 };
 
@@ -93,8 +93,11 @@ hipError_t launch_rotary(lora_dtype dt, RotaryParams p, hipStream_t stream);
 hipError_t launch_build_tree(const BuildTreeParams& p, hipStream_t stream);
 hipError_t launch_keep_path(const KeepParams& p, int32_t n_layers, int32_t kv_heads, int32_t B, hipStream_t stream);
 hipError_t launch_attend(lora_dtype dt, const AttendParams& p, hipStream_t stream);
-// Bytes of workspace launch_attend needs for these sizes (0: none).
-int64_t attend_need_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
+// Bytes of workspace launch_attend needs for these sizes (0: none), and the most it
+// needs for any type and any sizes up to these.
+int64_t attend_need_bytes(lora_dtype dt, int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq,
+                          int32_t hk, int32_t d);
+int64_t attend_most_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
                           int32_t d);
 
 }  // namespace lora

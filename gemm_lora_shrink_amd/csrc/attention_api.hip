@@ -314,7 +314,7 @@ lora_status check_attend_sizes(int32_t B, int32_t T, int32_t max_nodes, int32_t 
 LORA_EXPORT size_t lora_tree_attention_workspace_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context,
                                                        int32_t q_heads, int32_t kv_heads, int32_t d) {
   if (check_attend_sizes(B, T, max_nodes, max_context, q_heads, kv_heads, d) != LORA_OK) return 0;
-  return (size_t)attend_need_bytes(B, T, max_nodes, max_context, q_heads, kv_heads, d);
+  return (size_t)attend_most_bytes(B, T, max_nodes, max_context, q_heads, kv_heads, d);
 }
 
 LORA_EXPORT lora_status lora_tree_attention(lora_dtype dt, const void* q, int64_t ldq, int32_t T, int32_t B,
@@ -338,11 +338,7 @@ LORA_EXPORT lora_status lora_tree_attention(lora_dtype dt, const void* q, int64_
   const int64_t most = (((int64_t)1 << 32) - 1) / elem_bytes(dt);
   if (cache->k_page > most || cache->v_page > most || cache->k_row > most || cache->v_row > most)
     return fail(LORA_ERR_UNSUPPORTED, "a page or row of the cache spans 4 GiB");
-  const int64_t width = (int64_t)q_heads * d;
-  if ((st = check_rows(dt, "q", q, ldq, width)) != LORA_OK) return st;
-  if ((st = check_rows(dt, "out", out, ldo, width)) != LORA_OK) return st;
-  if (out == q && ldo != ldq) return fail(LORA_ERR_INVALID_ARG, "out is q with another row stride");
-  const int64_t need = attend_need_bytes(B, T, max_nodes, max_context, q_heads, kv_heads, d);
+  const int64_t need = attend_need_bytes(dt, B, T, max_nodes, max_context, q_heads, kv_heads, d);
   if (need > 0) {
     if (!workspace) return fail(LORA_ERR_INVALID_ARG, "workspace is null");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
@@ -351,6 +347,10 @@ LORA_EXPORT lora_status lora_tree_attention(lora_dtype dt, const void* q, int64_
       return fail(LORA_ERR_INVALID_ARG, "workspace has %zu bytes, the call needs %lld", workspace_bytes,
                   (long long)need);
   }
+  const int64_t width = (int64_t)q_heads * d;
+  if ((st = check_rows(dt, "q", q, ldq, width)) != LORA_OK) return st;
+  if ((st = check_rows(dt, "out", out, ldo, width)) != LORA_OK) return st;
+  if (out == q && ldo != ldq) return fail(LORA_ERR_INVALID_ARG, "out is q with another row stride");
   AttendParams p{};
   p.q = q;
   p.out = out;

@@ -208,9 +208,10 @@ lora_status lora_build_tree(const int32_t *parents, int32_t T, int32_t B, const 
  *   max_nodes, max_context   [host] bounds of n_b and context[b]; the closer,
  *               the better the work is spread
  *   workspace   256-byte aligned, of lora_tree_attention_workspace_bytes for
- *               the same sizes; nullable where that is 0.  It needs no
- *               clearing and holds nothing between calls; calls that may
- *               overlap need distinct ones.
+ *               the same heads and sizes B, T, max_nodes and max_context that
+ *               are not smaller than the call's; nullable where that is 0.  It
+ *               needs no clearing and holds nothing between calls; calls that
+ *               may overlap need distinct ones.
  */
 size_t lora_tree_attention_workspace_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context,
                                            int32_t q_heads, int32_t kv_heads, int32_t d);

@@ -1,7 +1,9 @@
 """What the binding of include/lora_attention.h makes of its arguments before
 they reach the library: strides of integer matrices, and the streams of the
-tensors it makes itself."""
+tensors it makes itself.  And the workspace of tree_attention, which a server
+allocates once for its largest batch."""
 
+import random
 from contextlib import contextmanager
 from types import SimpleNamespace
 
@@ -143,3 +145,76 @@ def test_calls_on_a_stream_beside_a_busy_one():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert bool((want[0] != 0).all() and (want[1] >= 0).all() and (want[2] >= 0).all()) and busy.numel()
+
+
+# ---- one workspace for every batch ---------------------------------------------
+
+FAKE = 0x10000  # an aligned, never dereferenced address
+
+
+def _refusal(B, T, nodes, context, hq, hk, d, ws_bytes, dtype=2):
+    """What a call with a workspace of ws_bytes says; without `out` it is refused
+    for that at the latest, so nothing is launched."""
+    cache = A._CACHE_FIELDS.pack(FAKE, FAKE, 0, 0, 0, 0, 0, 0, 4, 16)
+    st = A._lib().lora_tree_attention(dtype, FAKE, hq * d, T, B, hq, hk, d, cache, FAKE, 4, 4, FAKE, FAKE, nodes, context,
+                                      None, 0, 0.1, None, hq * d, None, FAKE, ws_bytes, None)
+    assert st == BAD
+    return glsa.lib().lora_last_error().decode()
+
+
+def test_a_workspace_serves_every_smaller_call():
+    """Fewer sequences or nodes are cut into more chunks, so what a call needs
+    does not grow with its sizes; what is allocated for them must."""
+    rng = random.Random(0)
+    size = lambda most: min(most, int(2 ** rng.uniform(0, most.bit_length())))
+    served = 0
+    for _ in range(300):
+        hk = rng.choice([1, 2, 8, 16, 40])
+        heads = (hk * rng.choice([1, 2, 4, 7]), hk, rng.choice([8, 64, 80, 128, 256]))
+        most = (size(256), size(8192), size(1024), size(131072))
+        have = glsa.attention_workspace_bytes(*most, *heads)
+        for _ in range(30):
+            less = tuple(size(m) for m in most)
+            said = _refusal(*less, *heads, have, rng.choice([0, 1, 2]))
+            assert said == "out is null", f"{less} of {most}, {heads}: {said}"
+            assert glsa.attention_workspace_bytes(*less, *heads) <= have
+            served += _refusal(*less, *heads, 0) != "out is null"
+    assert served > 1000  # calls that do need one
+
+
+def test_a_workspace_has_a_bound():
+    """Rows beyond what the sequences can have (a padded batch) take no room: at
+    most 1024 chunks of 32 rows, 512 of 128 or 256 of 256 are in flight, and a
+    sequence more than an even share of them."""
+    for sizes in [(256, 8192, 512, 131072, 32, 8, 128), (1, 1 << 20, 1, 131072, 32, 8, 128), (64, 1 << 20, 1024, 1 << 20, 8, 1, 256)]:
+        need = glsa.attention_workspace_bytes(*sizes)
+        assert 0 < need <= 2 * 256 * 256 * (sizes[-1] + 2) * 4, sizes
+    assert glsa.attention_workspace_bytes(256, 256, 1, 200, 32, 8, 128) == 0  # never more than one chunk
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_workspace_on_the_gpu(dtype):
+    """Calls of many sizes in a workspace for the largest give what they give in
+    one of their own; rows past the sequences' do not change that."""
+    hq, hk, d, page, B, ctx = 8, 2, 64, 64, 24, 6000
+    g = torch.Generator("cuda").manual_seed(3)
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    per = -(-(ctx + 40) // page)
+    pages = torch.randperm(B * per, generator=g, device="cuda").to(torch.int32).view(B, per)
+    k, v = (torch.empty(B * per, hk, page, d, device="cuda", dtype=dtype).normal_(generator=g) for _ in range(2))
+    shared = glsa.alloc_attention_workspace(B, B * 40 + 100, 40, ctx, hq, hk, d, "cuda")
+    some = 0
+    for n_seqs, nodes, context, pad in [(24, 40, 6000, 0), (24, 1, 6000, 0), (3, 1, 6000, 0), (1, 1, 5000, 0), (2, 40, 6000, 0),
+                                        (1, 9, 6000, 100), (3, 40, 5990, 100), (5, 3, 300, 7)]:
+        T = n_seqs * nodes
+        q = torch.empty(T + pad, hq * d, device="cuda", dtype=dtype).normal_(generator=g)
+        args = (k, v, pages[:n_seqs], ints([context - 13 * b for b in range(n_seqs)]), ints([b * nodes for b in range(n_seqs + 1)]))
+        kw = dict(max_nodes=nodes, max_context=context)
+        own = glsa.alloc_attention_workspace(n_seqs, T, nodes, context, hq, hk, d, "cuda").fill_(0xFF)
+        some += own.numel() > 0
+        want = glsa.tree_attention(q[:T], *args, workspace=own, **kw)
+        out = torch.full((T + pad, hq * d), 99.0, device="cuda", dtype=dtype)
+        glsa.tree_attention(q, *args, out=out, workspace=shared.fill_(0xFF), **kw)
+        assert torch.equal(out[:T], want) and bool((out[T:] == 99).all()) and bool(torch.isfinite(want).all())
+    assert some > 5
