@@ -29,6 +29,7 @@ from . import LORA_ERR_INVALID_ARG, LORA_ERR_UNSUPPORTED, LoraError, _check, _DT
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4}
+MAX_HEAD_DIM = 256
 MAX_TREE_NODES = 1024
 MAX_KEEP_LAYERS = 128
 
@@ -98,6 +99,13 @@ def _stream_of(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _i32(value, name):
+    """A number that the C ABI takes in 32 bits (ctypes would cut it to them)."""
+    if -0x80000000 <= value <= 0x7fffffff:
+        return value
+    raise _bad(f"{name} = {value} is beyond 32 bits")
+
+
 def _made(stream, make, *args, **kw):
     """make(*args, **kw), a new tensor, on the stream of the call that it is for:
     a fill on the current stream would not be ordered with the call on another,
@@ -114,6 +122,8 @@ def _matrix(t, name, dtype, dev):
     if len(shape) != 2 or t.dtype is not dtype or t.get_device() != dev:
         raise _bad(f"{name} must be a matrix of {dtype} on GPU {dev} (it is {t.dtype} of {tuple(shape)} on {t.device})")
     rows, width = shape
+    if rows > 0x7fffffff or width > 0x7fffffff:
+        raise _bad(f"{name} has more rows or columns than 32 bits count")
     ld, inner = t.stride()
     if rows < 2 or width < 1:  # the stride of a single row is no one's
         ld = max(ld, width, 1)
@@ -153,8 +163,8 @@ def _cache(k, v, dtype, dev):
     v_page, v_head, v_row, v_one = v.stride()
     if k_one != 1 or v_one != 1:
         raise _bad("the cache's heads must be contiguous")
-    if shape[2] < 1:
-        raise _bad("the cache's pages hold no rows")
+    if not 0 < shape[2] <= 0x7fffffff or shape[1] > 0x7fffffff:
+        raise _bad("the cache's pages hold no rows, or more rows or heads than 32 bits count")
     return _CACHE_FIELDS.pack(k.data_ptr(), v.data_ptr(), k_page, k_head, k_row, v_page, v_head, v_row, shape[0],
                               shape[2]), shape
 
@@ -177,6 +187,8 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None):
         config = _RopeConfig(_choice(ROPE_SCALINGS, scaling["type"], "rotary scaling"), scaling.get("factor", 1.0),
                              scaling.get("original_max_position", 0.0), scaling.get("low", 0.0),
                              scaling.get("high", 0.0), scaling.get("magnitude", 0.0))
+    if not 0 <= _i32(rot_dim, "rot_dim") <= MAX_HEAD_DIM:
+        raise _bad(f"rot_dim = {rot_dim} must be even, from 2 to {MAX_HEAD_DIM}")
     freq = (ctypes.c_double * max(1, int(rot_dim) // 2))()
     magnitude = ctypes.c_double()
     _check(_lib().lora_rope_frequencies(rot_dim, base, ctypes.byref(config), freq, ctypes.byref(magnitude)))
@@ -191,8 +203,10 @@ def rope_table(n, rot_dim, *, base=10000.0, scaling=None, frequencies=None, magn
     the caller's own in place of base and scaling."""
     if frequencies is None:
         frequencies, magnitude = rope_frequencies(rot_dim, base, scaling)
-    elif len(frequencies) != rot_dim // 2:
+    elif len(frequencies) != _i32(rot_dim, "rot_dim") // 2:
         raise _bad("one frequency for each pair")
+    if not -(1 << 63) <= first < 1 << 63:
+        raise _bad(f"first = {first} is no position")
     if out is None:
         out = _made(stream, torch.empty, (n, rot_dim), dtype=_F32, device=device)
     if tuple(out.shape) != (n, rot_dim):
@@ -209,7 +223,7 @@ def _rotate(norm, q, k, positions, table, head_dim, layout, q_out, k_out, v, k_c
     code = _DTYPES.get(dtype)
     if code is None:
         raise _bad(f"unsupported dtype {dtype}")
-    if head_dim < 1:
+    if _i32(head_dim, "head_dim") < 1:
         raise _bad(f"head_dim = {head_dim} must be >= 1")
     T, qw, ldq = _matrix(q, "q", dtype, dev)
     Tk, kw, ldk = _matrix(k, "k", dtype, dev)
@@ -301,10 +315,13 @@ def build_tree(parents, q_start, context, *, max_nodes, n_tokens=None, page_tabl
     [T, ceil(max_nodes / 64)], bit j = sees node j."""
     dev = _gpu(context, "context")
     device = context.device
-    B = context.numel()
+    B = _i32(context.numel(), "the number of sequences")
     T = parents.numel() if parents is not None else n_tokens
     if T is None:
         raise _bad("n_tokens is needed where parents is None")
+    _i32(T, "the number of tokens")
+    _i32(max_nodes, "max_nodes")
+    _i32(page_size, "page_size")
     words = 0
     if parents is not None and mask is None:
         mask = _made(stream, torch.zeros, (T, max(-(-max_nodes // 64), 1)), dtype=_I64, device=device)
@@ -334,8 +351,8 @@ def build_tree(parents, q_start, context, *, max_nodes, n_tokens=None, page_tabl
 def attention_workspace_bytes(n_seqs, n_tokens, max_nodes, max_context, q_heads, kv_heads, head_dim):
     """Bytes that suffice for every tree_attention call of these heads, of any
     type, with at most n_seqs sequences, n_tokens rows, max_nodes and max_context."""
-    return int(_lib().lora_tree_attention_workspace_bytes(n_seqs, n_tokens, max_nodes, max_context, q_heads, kv_heads,
-                                                          head_dim))
+    sizes = (n_seqs, n_tokens, max_nodes, max_context, q_heads, kv_heads, head_dim)
+    return int(_lib().lora_tree_attention_workspace_bytes(*(_i32(n, "a size") for n in sizes)))
 
 
 def alloc_attention_workspace(n_seqs, n_tokens, max_nodes, max_context, q_heads, kv_heads, head_dim, device):
@@ -377,10 +394,13 @@ def tree_attention(q, k_cache, v_cache, page_table, context, q_start, *, max_nod
     To, wo, ldo = _matrix(out, "out", dtype, dev)
     if To != T or wo != width:
         raise _bad("out must have q's shape")
-    B = context.numel()
+    B = _i32(context.numel(), "the number of sequences")
     table, ld_table, n_table = _int_rows(page_table, "page_table", dev, B)
-    if max_context is None:
-        max_context = n_table * page
+    _i32(max_nodes, "max_nodes")
+    if max_context is None:  # of what positions and their nodes go up to
+        max_context = max(0, min(n_table * page, 0x7fffffff - max_nodes))
+    else:
+        _i32(max_context, "max_context")
     mask_at = lse_at = ws = None
     words = ws_bytes = 0
     if mask is not None:
@@ -425,7 +445,7 @@ def keep_path(k_caches, v_caches, page_table, context, path, n_kept, *, stream=N
             for c in caches:
                 if c.shape != shape or c.stride() != strides or c.dtype is not dtype or c.get_device() != dev:
                     raise _bad("the layers' caches must be alike in shape, strides, type and GPU")
-    B = context.numel()
+    B = _i32(context.numel(), "the number of sequences")
     table = _int_rows(page_table, "page_table", dev, B)
     steps = _int_rows(path, "path", dev, B)
     kept, at = _vector(n_kept, "n_kept", _I32, dev, B), _vector(context, "context", _I32, dev, B)

@@ -1,6 +1,6 @@
 """What the binding of include/lora_attention.h makes of its arguments before
-they reach the library: strides of integer matrices, and the streams of the
-tensors it makes itself.  And the workspace of tree_attention, which a server
+they reach the library: strides of integer matrices, the streams of the
+tensors it makes itself, and numbers past the 32 bits of the C ABI.  And the workspace of tree_attention, which a server
 allocates once for its largest batch."""
 
 import random
@@ -66,15 +66,28 @@ def test_calls_with_overlapping_rows_are_refused():
 # ---- tensors that the binding makes: on the call's stream ----------------------
 
 class _NoLibrary:
-    """Every entry point succeeds and does nothing."""
+    """Every entry point succeeds and does nothing but keep its arguments."""
 
     def __getattr__(self, name):
-        return lambda *args: glsa.LORA_OK
+        def call(*args):
+            self.args = args
+            return glsa.LORA_OK
+        return call
 
 
 @pytest.fixture
-def made_on(monkeypatch):
-    """The binding without a GPU; lists the stream that each new tensor is made on."""
+def no_library(monkeypatch):
+    """The binding without a GPU, on host tensors."""
+    monkeypatch.setattr(A, "_gpu", lambda t, name: HOST)
+    monkeypatch.setattr(A, "_stream_of", lambda stream, dev: stream)
+    monkeypatch.setattr(A, "_bound", _NoLibrary())
+    monkeypatch.setattr(A, "_lib", lambda: A._bound)
+    return A._bound
+
+
+@pytest.fixture
+def made_on(monkeypatch, no_library):
+    """Lists the stream that each new tensor is made on."""
     streams, made = [None], []
 
     @contextmanager
@@ -92,9 +105,6 @@ def made_on(monkeypatch):
     for name in ("empty", "zeros", "full"):
         monkeypatch.setattr(torch, name, recorded(getattr(torch, name)))
     monkeypatch.setattr(torch.cuda, "stream", stream)
-    monkeypatch.setattr(A, "_gpu", lambda t, name: HOST)
-    monkeypatch.setattr(A, "_bound", _NoLibrary())
-    monkeypatch.setattr(A, "_lib", lambda: A._bound)
     return made
 
 
@@ -218,3 +228,47 @@ def test_one_workspace_on_the_gpu(dtype):
         glsa.tree_attention(q, *args, out=out, workspace=shared.fill_(0xFF), **kw)
         assert torch.equal(out[:T], want) and bool((out[T:] == 99).all()) and bool(torch.isfinite(want).all())
     assert some > 5
+
+
+# ---- numbers that the C ABI has 32 bits for --------------------------------------
+
+def _attend_args(page=8, columns=4):
+    ints = torch.tensor([0, 2], dtype=torch.int32)
+    cache = torch.ones(1, 1, page, 8)
+    return torch.ones(2, 8), cache, cache, torch.zeros(1, columns, dtype=torch.int32), ints[:1], ints
+
+
+def test_a_wide_page_table_bounds_no_context_away(no_library):
+    """The default max_context is what the table holds, as far as positions go: cut
+    to its low 32 bits it made contexts of none."""
+    for page, columns, nodes, want in [(8, 4, 2, 32), (4096, 1 << 20, 2, (1 << 31) - 3), (4096, 1 << 19, 7, (1 << 31) - 8),
+                                       (4096, (1 << 19) - 1, 1, (1 << 31) - 4096)]:
+        glsa.tree_attention(*_attend_args(page, columns), max_nodes=nodes)
+        assert no_library.args[14:16] == (nodes, want)
+
+
+@pytest.mark.parametrize("number", [1 << 32, (1 << 32) + 64, -(1 << 32) + 64, 1 << 31, 1 << 64])
+def test_numbers_past_32_bits_are_refused(number):
+    """ctypes would pass their low 32 bits on."""
+    calls = [lambda: glsa.rope_frequencies(number), lambda: glsa.rope_table(4, number)]
+    calls += [lambda i=i: glsa.attention_workspace_bytes(*[number if j == i else 64 for j in range(7)]) for i in range(7)]
+    for call in calls:
+        with pytest.raises(glsa.LoraError) as e:
+            call()
+        assert e.value.status == BAD
+
+
+@pytest.mark.parametrize("number", [1 << 32, (1 << 32) + 64, -(1 << 32) + 64, 1 << 31])
+def test_numbers_past_32_bits_are_refused_by_the_calls(number, no_library):
+    q, cache, _, table, context, ints = _attend_args()
+    for call in (lambda: glsa.tree_attention(q, cache, cache, table, context, ints, max_nodes=number),
+                 lambda: glsa.tree_attention(q, cache, cache, table, context, ints, max_nodes=2, max_context=number),
+                 lambda: glsa.build_tree(None, ints, context, max_nodes=number, n_tokens=2),
+                 lambda: glsa.build_tree(None, ints, context, max_nodes=2, n_tokens=number, positions=ints),
+                 lambda: glsa.build_tree(None, ints, context, max_nodes=2, n_tokens=2, page_table=table, n_pages=1,
+                                         page_size=number),
+                 lambda: glsa.rotary(q[:, :0], q[:, :0], ints, q, head_dim=number),
+                 lambda: glsa.rope_table(1, 8, frequencies=[1.0] * 4, first=number << 32, device="cpu")):
+        with pytest.raises(glsa.LoraError) as e:
+            call()
+        assert e.value.status == BAD
