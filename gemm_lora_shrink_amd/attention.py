@@ -302,7 +302,7 @@ def qk_norm_rotary(q, k, q_weight, k_weight, positions, table, *, head_dim, eps=
 
 # ---- trees of drafted tokens -------------------------------------------------
 
-def build_tree(parents, q_start, context, *, max_nodes, n_tokens=None, page_table=None, n_pages=0, page_size=1,
+def build_tree(parents, q_start, context, *, max_nodes, n_tokens=None, page_table=None, n_pages=None, page_size=None,
                mask=None, positions=None, cache_rows=None, stream=None):
     """What a step's layers share, from the trees of its sequences:
     (mask, positions, cache_rows), computed once.
@@ -311,8 +311,9 @@ def build_tree(parents, q_start, context, *, max_nodes, n_tokens=None, page_tabl
     than its own) or -1 where it follows the context; None: chains of
     n_tokens tokens in all, whose mask is None.  q_start: int32 [B + 1], rows
     of each sequence; context: int32 [B], its tokens in the cache.  page_table:
-    int32 [B, pages]; without it cache_rows is None.  mask: int64
-    [T, ceil(max_nodes / 64)], bit j = sees node j."""
+    int32 [B, pages], with the n_pages and page_size of the cache; without it
+    cache_rows is None.  mask: int64 [T, ceil(max_nodes / 64)], bit j = sees
+    node j."""
     dev = _gpu(context, "context")
     device = context.device
     B = _i32(context.numel(), "the number of sequences")
@@ -321,7 +322,6 @@ def build_tree(parents, q_start, context, *, max_nodes, n_tokens=None, page_tabl
         raise _bad("n_tokens is needed where parents is None")
     _i32(T, "the number of tokens")
     _i32(max_nodes, "max_nodes")
-    _i32(page_size, "page_size")
     words = 0
     if parents is not None and mask is None:
         mask = _made(stream, torch.zeros, (T, max(-(-max_nodes // 64), 1)), dtype=_I64, device=device)
@@ -334,11 +334,16 @@ def build_tree(parents, q_start, context, *, max_nodes, n_tokens=None, page_tabl
         positions = _made(stream, torch.full, (T,), -1, dtype=_I32, device=device)
     table = (None, 0, 0)
     if page_table is not None:
+        if n_pages is None or page_size is None:
+            raise _bad("a page_table takes the cache's n_pages and page_size")
+        _i32(page_size, "page_size")
         table = _int_rows(page_table, "page_table", dev, B)
         if cache_rows is None:
             cache_rows = _made(stream, torch.full, (T,), -1, dtype=_I32, device=device)
-    elif cache_rows is not None:
-        raise _bad("cache_rows needs a page_table")
+    else:
+        if cache_rows is not None:
+            raise _bad("cache_rows needs a page_table")
+        n_pages, page_size = 0, 1
     _check(_lib().lora_build_tree(
         None if parents is None else _vector(parents, "parents", _I32, dev, T), T, B,
         _vector(q_start, "q_start", _I32, dev, B + 1), _vector(context, "context", _I32, dev, B), max_nodes, *table,

@@ -272,3 +272,15 @@ def test_numbers_past_32_bits_are_refused_by_the_calls(number, no_library):
         with pytest.raises(glsa.LoraError) as e:
             call()
         assert e.value.status == BAD
+
+
+def test_cache_rows_take_the_caches_sizes(no_library):
+    """Without them every row would come out as missing, and rotary would then place
+    nothing in the cache."""
+    _, _, _, table, context, ints = _attend_args()
+    for sizes in ({}, dict(n_pages=4), dict(page_size=8)):
+        with pytest.raises(glsa.LoraError, match="n_pages and page_size"):
+            glsa.build_tree(None, ints, context, max_nodes=2, n_tokens=2, page_table=table, **sizes)
+    glsa.build_tree(None, ints, context, max_nodes=2, n_tokens=2, page_table=table, n_pages=4, page_size=8)
+    assert no_library.args[9:11] == (4, 8)
+    glsa.build_tree(None, ints, context, max_nodes=2, n_tokens=2)
