@@ -1283,8 +1283,11 @@ enum class Kind { kNarrow, kTurns128, kTurns256, kWide };
 struct AttendPlan {
   Kind kind;
   int32_t chunk, splits, row_tiles;
+  int32_t block;   // threads of a workgroup
   int64_t groups;  // workgroups to be had from cutting the keys
+  int64_t grid;
 };
+constexpr int narrow_waves(int row_bytes) { return row_bytes <= 512 ? 4 : 2; }
 AttendPlan attend_kind(int elem, int32_t nodes, int32_t group, int32_t d) {
   AttendPlan a{};
   const int64_t rows = (int64_t)nodes * group;
@@ -1292,10 +1295,12 @@ AttendPlan attend_kind(int elem, int32_t nodes, int32_t group, int32_t d) {
   int64_t tile = kBlock;
   a.groups = 1024;
   a.kind = Kind::kNarrow;
+  a.block = 64 * narrow_waves(row_bytes);
   if (rows > kBlock) {
     a.kind = row_bytes > 256 ? Kind::kWide : rows > 4 * kBlock ? Kind::kTurns256 : Kind::kTurns128;
     tile = a.kind == Kind::kTurns256 ? 8 * kBlock : 4 * kBlock;
     a.groups = a.kind == Kind::kWide ? 512 : 256;
+    a.block = a.kind == Kind::kWide ? kThreads : 512;
   }
   a.row_tiles = (int32_t)ceil_div(rows, tile);
   return a;
@@ -1308,25 +1313,26 @@ AttendPlan attend_kind(int elem, int32_t nodes, int32_t group, int32_t d) {
 // the narrow one (64 x 8192 keys: 175 us, with eight 185; one sequence of 131072:
 // 42, with eight 53).
 constexpr int64_t kMinChunk = 256;
-constexpr int64_t kMaxGroups = (int64_t)1 << 30, kMaxChunk = (int64_t)1 << 30;
+constexpr int64_t kMaxChunk = (int64_t)1 << 30;
 
 AttendPlan attend_plan(int elem, int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
                        int32_t d) {
   AttendPlan a = attend_kind(elem, max_nodes, hq / hk, d);
   const int64_t keys = (int64_t)max_context + max_nodes;
   const int64_t units = (int64_t)B * hk * a.row_tiles;
-  int64_t chunk = ceil_div(keys * units, a.groups);
+  int64_t chunk = units < a.groups ? ceil_div(keys * units, a.groups) : keys;
   if (chunk < kMinChunk) chunk = kMinChunk;
-  const int64_t fewest = ceil_div(keys * units, kMaxGroups);
-  if (chunk < fewest) chunk = fewest;
   // even chunks of whole stages (128 keys are one block of each narrow wave)
   const int64_t unit = a.kind == Kind::kNarrow ? 4 * kBlock : 2 * kBlock;
   chunk = ceil_div(ceil_div(keys, ceil_div(keys, chunk)), unit) * unit;
   if (chunk > kMaxChunk) chunk = kMaxChunk;
   a.chunk = (int32_t)chunk;
   a.splits = (int32_t)ceil_div(keys, chunk);
+  a.grid = ceil_div((int64_t)B * hk * a.splits, kXcds) * kXcds * a.row_tiles;
   return a;
 }
+
+int64_t join_grid(int32_t max_nodes, int32_t hq) { return ceil_div((int64_t)max_nodes * hq, kThreads / 64); }
 
 int32_t part_rows_of(int32_t B, int32_t T, int32_t max_nodes) {
   return (int32_t)std::min<int64_t>(T, (int64_t)B * max_nodes);
@@ -1334,20 +1340,17 @@ int32_t part_rows_of(int32_t B, int32_t T, int32_t max_nodes) {
 int64_t part_bytes(int64_t rows, int32_t hq, int32_t d) { return (rows * hq * (d + 2) * 4 + 255) & ~int64_t(255); }
 
 template <typename Elem, int DP>
-hipError_t launch_d(const AttendParams& p, Kind kind, hipStream_t stream) {
+hipError_t launch_d(const AttendParams& p, const AttendPlan& a, hipStream_t stream) {
   constexpr int kRow = DP * (int)sizeof(Elem);
-  const int64_t grid = ceil_div((int64_t)p.B * p.hk * p.splits, kXcds) * kXcds * p.row_tiles;
-  if (grid > (int64_t)0x7fffffff) return hipErrorInvalidConfiguration;
-  const dim3 g((unsigned)grid);
-  if (kind == Kind::kNarrow) {
-    constexpr int NW = kRow <= 512 ? 4 : 2;
-    hipLaunchKernelGGL((attend_narrow_kernel<Elem, DP, NW>), g, dim3(NW * 64), 0, stream, p);
+  const dim3 g((unsigned)a.grid), b((unsigned)a.block);
+  if (a.kind == Kind::kNarrow) {
+    hipLaunchKernelGGL((attend_narrow_kernel<Elem, DP, narrow_waves(kRow)>), g, b, 0, stream, p);
   } else if constexpr (kRow > 256) {
-    hipLaunchKernelGGL((attend_wide_kernel<Elem, DP, 32>), g, dim3(kThreads), 0, stream, p);
-  } else if (kind == Kind::kTurns256) {
-    hipLaunchKernelGGL((attend_turns_kernel<Elem, DP, 1>), g, dim3(512), 0, stream, p);
+    hipLaunchKernelGGL((attend_wide_kernel<Elem, DP, 32>), g, b, 0, stream, p);
+  } else if (a.kind == Kind::kTurns256) {
+    hipLaunchKernelGGL((attend_turns_kernel<Elem, DP, 1>), g, b, 0, stream, p);
   } else {
-    hipLaunchKernelGGL((attend_turns_kernel<Elem, DP, 2>), g, dim3(512), 0, stream, p);
+    hipLaunchKernelGGL((attend_turns_kernel<Elem, DP, 2>), g, b, 0, stream, p);
   }
   return hipGetLastError();
 }
@@ -1364,17 +1367,22 @@ hipError_t launch(AttendParams p, hipStream_t stream) {
   p.by_sequences = fast_div((uint32_t)p.B);
   p.by_heads = fast_div((uint32_t)p.hk);
   p.by_chunk = fast_div((uint32_t)a.chunk);
-  hipError_t e = p.d <= 64    ? launch_d<Elem, 64>(p, a.kind, stream)
-                 : p.d <= 128 ? launch_d<Elem, 128>(p, a.kind, stream)
-                              : launch_d<Elem, 256>(p, a.kind, stream);
+  hipError_t e = p.d <= 64    ? launch_d<Elem, 64>(p, a, stream)
+                 : p.d <= 128 ? launch_d<Elem, 128>(p, a, stream)
+                              : launch_d<Elem, 256>(p, a, stream);
   if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t rows = (int64_t)p.max_nodes * p.hq;
-  hipLaunchKernelGGL(attend_join_kernel<Elem>, dim3((unsigned)ceil_div(rows, kThreads / 64), (unsigned)p.B),
+  hipLaunchKernelGGL(attend_join_kernel<Elem>, dim3((unsigned)join_grid(p.max_nodes, p.hq), (unsigned)p.B),
                      dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
 }  // namespace
+
+bool attend_fits(lora_dtype dt, int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk, int32_t d) {
+  const AttendPlan a = attend_plan(dt == LORA_F32 ? 4 : 2, B, max_nodes, max_context, hq, hk, d);
+  const int64_t most = ((int64_t)1 << 32) - 1;  // threads in a dimension of a grid
+  return a.grid <= most / a.block && (a.splits == 1 || join_grid(max_nodes, hq) <= most / kThreads);
+}
 
 int64_t attend_need_bytes(lora_dtype dt, int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq,
                           int32_t hk, int32_t d) {

@@ -93,6 +93,8 @@ hipError_t launch_rotary(lora_dtype dt, RotaryParams p, hipStream_t stream);
 hipError_t launch_build_tree(const BuildTreeParams& p, hipStream_t stream);
 hipError_t launch_keep_path(const KeepParams& p, int32_t n_layers, int32_t kv_heads, int32_t B, hipStream_t stream);
 hipError_t launch_attend(lora_dtype dt, const AttendParams& p, hipStream_t stream);
+// Whether launch_attend's grids hold the work of these sizes.
+bool attend_fits(lora_dtype dt, int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk, int32_t d);
 // Bytes of workspace launch_attend needs for these sizes (0: none), and the most it
 // needs for any type and any sizes up to these.
 int64_t attend_need_bytes(lora_dtype dt, int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq,

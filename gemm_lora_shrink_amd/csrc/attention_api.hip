@@ -338,6 +338,8 @@ LORA_EXPORT lora_status lora_tree_attention(lora_dtype dt, const void* q, int64_
   const int64_t most = (((int64_t)1 << 32) - 1) / elem_bytes(dt);
   if (cache->k_page > most || cache->v_page > most || cache->k_row > most || cache->v_row > most)
     return fail(LORA_ERR_UNSUPPORTED, "a page or row of the cache spans 4 GiB");
+  if (!attend_fits(dt, B, max_nodes, max_context, q_heads, kv_heads, d))
+    return fail(LORA_ERR_UNSUPPORTED, "B = %d sequences of up to %d nodes are more than a launch holds", B, max_nodes);
   const int64_t need = attend_need_bytes(dt, B, T, max_nodes, max_context, q_heads, kv_heads, d);
   if (need > 0) {
     if (!workspace) return fail(LORA_ERR_INVALID_ARG, "workspace is null");

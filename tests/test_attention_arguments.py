@@ -162,13 +162,13 @@ def test_calls_on_a_stream_beside_a_busy_one():
 FAKE = 0x10000  # an aligned, never dereferenced address
 
 
-def _refusal(B, T, nodes, context, hq, hk, d, ws_bytes, dtype=2):
+def _refusal(B, T, nodes, context, hq, hk, d, ws_bytes, dtype=2, status=BAD):
     """What a call with a workspace of ws_bytes says; without `out` it is refused
     for that at the latest, so nothing is launched."""
     cache = A._CACHE_FIELDS.pack(FAKE, FAKE, 0, 0, 0, 0, 0, 0, 4, 16)
     st = A._lib().lora_tree_attention(dtype, FAKE, hq * d, T, B, hq, hk, d, cache, FAKE, 4, 4, FAKE, FAKE, nodes, context,
                                       None, 0, 0.1, None, hq * d, None, FAKE, ws_bytes, None)
-    assert st == BAD
+    assert st == status
     return glsa.lib().lora_last_error().decode()
 
 
@@ -284,3 +284,24 @@ def test_cache_rows_take_the_caches_sizes(no_library):
     glsa.build_tree(None, ints, context, max_nodes=2, n_tokens=2, page_table=table, n_pages=4, page_size=8)
     assert no_library.args[9:11] == (4, 8)
     glsa.build_tree(None, ints, context, max_nodes=2, n_tokens=2)
+
+
+# ---- bounds past what a launch holds ---------------------------------------------
+
+@pytest.mark.parametrize("sizes", [
+    (65535, 4, 1 << 26, (1 << 31) - (1 << 26) - 2, 1024, 1024, 8),  # keys times workgroups pass 64 bits
+    (65535, 4, 1 << 20, 4096, 32, 8, 128), (8192, 8192, 65536, 0, 16, 16, 256),
+    (1, 4, 1 << 26, (1 << 31) - (1 << 26) - 2, 1, 1, 8),            # two chunks, too many rows to join in one launch
+    (65535, 65535, 1, 100, 1024, 1024, 8)])
+def test_bounds_past_a_launch_are_refused(sizes):
+    """A launch holds fewer than 2^32 threads in a dimension of its grid."""
+    for dtype in (0, 1, 2):
+        assert "launch" in _refusal(*sizes, 1 << 60, dtype, glsa.LORA_ERR_UNSUPPORTED)
+
+
+@pytest.mark.parametrize("sizes", [(256, 8192, 512, 131072, 32, 8, 128), (1, 1, 1, (1 << 31) - 2, 32, 8, 128),
+                                   (4096, 8192, 512, 131072, 32, 8, 128), (65535, 65535, 1, 4096, 32, 8, 128),
+                                   (1, 65536, 65536, 0, 64, 8, 128)])
+def test_large_bounds_are_served(sizes):
+    for dtype in (0, 1, 2):
+        assert _refusal(*sizes, 1 << 60, dtype) == "out is null"
