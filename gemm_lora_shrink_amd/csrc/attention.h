@@ -89,6 +89,8 @@ struct AttendParams {
 
 hipError_t launch_rope_table(const double* inv_freq, int32_t rot, double magnitude, int64_t first, int64_t n,
                              float* table, hipStream_t stream);
+// Whether launch_rotary's grid holds T tokens of `heads` heads (q, k and cached v).
+bool rotary_fits(int32_t T, int heads, int32_t d, int32_t rot);
 hipError_t launch_rotary(lora_dtype dt, RotaryParams p, hipStream_t stream);
 hipError_t launch_build_tree(const BuildTreeParams& p, hipStream_t stream);
 hipError_t launch_keep_path(const KeepParams& p, int32_t n_layers, int32_t kv_heads, int32_t B, hipStream_t stream);

@@ -99,6 +99,8 @@ lora_status rotary_impl(bool norm, lora_dtype dt, const void* q, int64_t ldq, co
     return fail(LORA_ERR_UNSUPPORTED, "q_weight and k_weight must be 16-byte aligned");
   if ((int64_t)T * (q_heads + 2 * (int64_t)kv_heads) >= kMaxPositions)
     return fail(LORA_ERR_UNSUPPORTED, "T times the heads reaches 2^31");
+  if (!rotary_fits(T, q_heads + (cache ? 2 : 1) * kv_heads, d, rot_dim))
+    return fail(LORA_ERR_UNSUPPORTED, "T = %d tokens of these heads are more than a launch holds", T);
   RotaryParams p{};
   if (cache) {
     if ((st = check_cache(dt, *cache)) != LORA_OK) return st;

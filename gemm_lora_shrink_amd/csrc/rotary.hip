@@ -308,24 +308,39 @@ void launch_units(const RotaryParams& p, unsigned blocks, hipStream_t stream) {
   else hipLaunchKernelGGL((rotary_kernel<Elem, HPG, false, false>), g, b, 0, stream, p);
 }
 
+// How a call's heads (q, k and v) are laid over threads.
+struct RotaryPlan {
+  bool pieces;  // 16-byte pieces
+  int lane_shift, heads_of_group, groups;
+  int64_t threads;
+};
+RotaryPlan rotary_plan(int32_t T, int heads, int32_t d, int32_t rot) {
+  RotaryPlan a{};
+  a.pieces = d % 16 == 0 && rot % 16 == 0;
+  a.heads_of_group = 1;
+  a.lane_shift = 4;
+  if (a.pieces) {
+    a.lane_shift = 0;
+    while ((16 << a.lane_shift) < d) ++a.lane_shift;
+    const int64_t lanes = ((int64_t)T * heads) << a.lane_shift;
+    if (lanes >= (int64_t)kThreads * 4096) a.heads_of_group = 4;
+  }
+  a.groups = (heads + a.heads_of_group - 1) / a.heads_of_group;
+  a.threads = ((int64_t)T * a.groups) << a.lane_shift;
+  return a;
+}
+
 template <typename Elem>
 hipError_t launch(RotaryParams& p, hipStream_t stream) {
-  const int heads = p.hq + p.hk + (p.cache.k ? p.hk : 0);
-  if (p.d % 16 == 0 && p.rot % 16 == 0) {
+  const RotaryPlan a = rotary_plan(p.T, p.hq + p.hk + (p.cache.k ? p.hk : 0), p.d, p.rot);
+  const unsigned blocks = (unsigned)ceil_div(a.threads, kThreads);
+  p.groups = fast_div((uint32_t)a.groups);
+  if (a.pieces) {
     p.units = p.d / 16;
-    p.lane_shift = 0;
-    while ((1 << p.lane_shift) < p.units) ++p.lane_shift;
-    const int64_t lanes = ((int64_t)p.T * heads) << p.lane_shift;
-    const int hpg = lanes >= (int64_t)kThreads * 4096 ? 4 : 1;
-    const int groups = (heads + hpg - 1) / hpg;
-    p.groups = fast_div((uint32_t)groups);
-    const int64_t threads = ((int64_t)p.T * groups) << p.lane_shift;
-    const unsigned blocks = (unsigned)ceil_div(threads, kThreads);
-    if (hpg == 4) launch_units<Elem, 4>(p, blocks, stream);
+    p.lane_shift = a.lane_shift;
+    if (a.heads_of_group == 4) launch_units<Elem, 4>(p, blocks, stream);
     else launch_units<Elem, 1>(p, blocks, stream);
   } else {
-    p.groups = fast_div((uint32_t)heads);
-    const unsigned blocks = (unsigned)ceil_div((int64_t)p.T * heads * 16, kThreads);
     if (p.norm) hipLaunchKernelGGL((rotary_pairs_kernel<Elem, true>), dim3(blocks), dim3(kThreads), 0, stream, p);
     else hipLaunchKernelGGL((rotary_pairs_kernel<Elem, false>), dim3(blocks), dim3(kThreads), 0, stream, p);
   }
@@ -333,6 +348,10 @@ hipError_t launch(RotaryParams& p, hipStream_t stream) {
 }
 
 }  // namespace
+
+bool rotary_fits(int32_t T, int heads, int32_t d, int32_t rot) {
+  return rotary_plan(T, heads, d, rot).threads <= ((int64_t)1 << 32) - kThreads;
+}
 
 hipError_t launch_rotary(lora_dtype dt, RotaryParams p, hipStream_t stream) {
   switch (dt) {

@@ -305,3 +305,14 @@ def test_bounds_past_a_launch_are_refused(sizes):
 def test_large_bounds_are_served(sizes):
     for dtype in (0, 1, 2):
         assert _refusal(*sizes, 1 << 60, dtype) == "out is null"
+
+
+@pytest.mark.parametrize("T,hq,hk,d,rot,refused", [
+    (1 << 28, 1, 1, 8, 8, True), (1 << 25, 32, 8, 256, 256, True), (1 << 25, 32, 8, 80, 20, True),
+    (1 << 23, 32, 8, 256, 256, False), (1 << 22, 32, 8, 80, 20, False), (1 << 25, 32, 8, 64, 64, False)])
+def test_rotations_past_a_launch_are_refused(T, hq, hk, d, rot, refused):
+    cache = A._CACHE_FIELDS.pack(FAKE, FAKE, 0, 0, 0, 0, 0, 0, 4, 16)
+    st = A._lib().lora_rotary(1, FAKE, hq * d, FAKE, hk * d, FAKE, hk * d, T, hq, hk, d, 0, rot, FAKE, 16, FAKE, FAKE, hq * d,
+                              FAKE, hk * d, cache, None, None)  # without cache_rows: refused at the latest for that
+    said = glsa.lib().lora_last_error().decode()
+    assert (st, "launch" in said) == ((glsa.LORA_ERR_UNSUPPORTED, True) if refused else (BAD, False)), said
