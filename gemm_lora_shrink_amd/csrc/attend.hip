@@ -381,9 +381,7 @@ template <typename Elem, int DP> struct RowBlock {
   // weights.  c > 0 turns scores into powers of two.  m is moved only where a weight
   // would pass 2^kMost, and then below the score by kBelow: most tiles leave the
   // output as it is, and sums and weights stay clear of overflow.
-  // `between` is called with 0 .. 3 at four places among the work, for loads to be
-  // issued there: a wave that issues several at once waits for each.
-  template <int NS, typename F> __device__ __forceinline__ void weigh(f32x16 (&s)[NS], float c, F between) {
+  template <int NS> __device__ __forceinline__ void weigh(f32x16 (&s)[NS], float c) {
     constexpr float kBelow = Mma32<Elem>::kBelow, kMost = Mma32<Elem>::kMost;
     // four chains each for the maximum and the sum: an operation waits twice its
     // own time for the one before it
@@ -393,7 +391,6 @@ template <typename Elem, int DP> struct RowBlock {
 #pragma unroll
       for (int i = b ? 0 : 4; i < 16; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[b][i]);
     float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-    between(0);
     mx = half_max(mx) * c;
     if (__any(mx - m > kMost)) {
       float mn = mx - kBelow;
@@ -413,7 +410,6 @@ template <typename Elem, int DP> struct RowBlock {
     for (int b = 0; b < NS; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        if (16 * b + i > 0 && (16 * b + i) % (4 * NS) == 0) between((16 * b + i) / (4 * NS));
         s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, -ms));
         sum[i & 3] += s[b][i];
       }
@@ -788,7 +784,7 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
     uint32_t seen = valid;
     if constexpr (kTail) seen &= rb.sees(p, w, (int)first_key(t));
     if (__any(seen != ~0u)) rb.mask_scores(s[0], seen);
-    rb.weigh(s, c, [](int) {});
+    rb.weigh(s, c);
     if (more) wait_loads<NL + 1>();
     else wait_loads<0>();
     if (kTail && __any(seen != valid) && rb.any_odd(vbuf, kBlock)) {
@@ -868,14 +864,14 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
 
 // More rows of more than 256 bytes (fp32 heads from 72 elements, 16-bit ones from
 // 136), whose outputs leave no registers for the kernel below: four waves of 32
-// rows share tiles of KT keys, double buffered; a wave fetches a quarter of each
+// rows share tiles of 32 keys, double buffered; a wave fetches a quarter of each
 // tile's rows.  One workgroup a compute unit.  Bound by the matrix cores and the
 // weights in turn, heads of 256 elements by spilled registers too (fp32: 228 a
 // lane; 3 sequences of 12 nodes over 1949 keys, 32 + 8 fp32 heads: 229 us).
-template <typename Elem, int DP, int KT>
+template <typename Elem, int DP>
 __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
-  constexpr int NS = KT / kBlock;
+  constexpr int KT = kBlock;
   constexpr int kTile = KT * R::kBytes;
   constexpr int kMine = KT / 4;  // rows a wave fetches of K, and of V
   constexpr int NL = kMine * R::kBytes / 1024;
@@ -947,37 +943,24 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p
       fetch_ids(t + 3, ahead[1]);
     }
     if (!idle) {
-      f32x16 s[NS];
-      uint32_t seen[NS], valid[NS];
-      s[0] = rb.template scores<0>();
-      if constexpr (NS == 2) s[1] = rb.template scores<kBlock>();
+      f32x16 s[1] = {rb.template scores<0>()};
+      uint32_t valid = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) valid |= s_valid[t & 3][i] << (i * kMine);
+      uint32_t seen = valid;
       bool uneven = false;
-#pragma unroll
-      for (int b = 0; b < NS; ++b) {
-        valid[b] = 0;
-#pragma unroll
-        for (int i = 0; i < 4 / NS; ++i) valid[b] |= s_valid[t & 3][b * (4 / NS) + i] << (i * kMine);
-        seen[b] = valid[b];
-        if constexpr (kTail) {
-          seen[b] &= rb.sees(p, w, w.k0 + t * KT + b * kBlock);
-          uneven |= __any(seen[b] != valid[b]);
-        }
+      if constexpr (kTail) {
+        seen &= rb.sees(p, w, w.k0 + t * KT);
+        uneven = __any(seen != valid);
       }
-#pragma unroll
-      for (int b = 0; b < NS; ++b)
-        if (__any(seen[b] != ~0u)) rb.mask_scores(s[b], seen[b]);
-      rb.weigh(s, c, [](int) {});
+      if (__any(seen != ~0u)) rb.mask_scores(s[0], seen);
+      rb.weigh(s, c);
       const char* vb = s_kv[t & 1] + kTile;
       if (kTail && uneven && rb.any_odd(vb, KT)) {
         rb.template add_values<kTail, 0>(rb.pack(s[0]));
-        rb.add_odd(vb, seen[0]);
-        if constexpr (NS == 2) {
-          rb.template add_values<kTail, kBlock>(rb.pack(s[1]));
-          rb.add_odd(vb + kBlock * R::kBytes, seen[1]);
-        }
+        rb.add_odd(vb, seen);
       } else {
         rb.template add_values<false, 0>(rb.pack(s[0]));
-        if constexpr (NS == 2) rb.template add_values<false, kBlock>(rb.pack(s[1]));
       }
     }
     rb.move_keys(2 * kTile);
@@ -1130,7 +1113,7 @@ __global__ __launch_bounds__(512, 2) void attend_turns_kernel(AttendParams p) {
         rb.mask_scores(s[b], valid);
       }
     }
-    rb.weigh(s, c, [](int) {});
+    rb.weigh(s, c);
 #pragma unroll
     for (int b = 0; b < NS; ++b) weights[b] = rb.pack(s[b]);
     if constexpr (decltype(tail)::value)
@@ -1346,7 +1329,7 @@ hipError_t launch_d(const AttendParams& p, const AttendPlan& a, hipStream_t stre
   if (a.kind == Kind::kNarrow) {
     hipLaunchKernelGGL((attend_narrow_kernel<Elem, DP, narrow_waves(kRow)>), g, b, 0, stream, p);
   } else if constexpr (kRow > 256) {
-    hipLaunchKernelGGL((attend_wide_kernel<Elem, DP, 32>), g, b, 0, stream, p);
+    hipLaunchKernelGGL((attend_wide_kernel<Elem, DP>), g, b, 0, stream, p);
   } else if (a.kind == Kind::kTurns256) {
     hipLaunchKernelGGL((attend_turns_kernel<Elem, DP, 1>), g, b, 0, stream, p);
   } else {

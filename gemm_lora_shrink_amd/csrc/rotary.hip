@@ -101,11 +101,10 @@ template <typename Elem> __device__ inline Eight<Elem> rounded(const float* f) {
 }
 template <typename Elem> __device__ inline Elem one_rounded(float f) { return static_cast<Elem>(f); }
 
-// Where head h of token t comes from and goes to: up to two destinations, the
-// out rows and the cache.
+// Where head h of token t comes from and its place in the out rows (null: none).
 template <typename Elem> struct HeadPtrs {
   const Elem* in;
-  Elem *out, *cache;
+  Elem* out;
   bool turns;  // a q or k head
 };
 template <typename Elem>
@@ -113,7 +112,6 @@ __device__ inline HeadPtrs<Elem> head_ptrs(const RotaryParams& p, int64_t t, int
   HeadPtrs<Elem> r;
   const int kv = h < p.hq ? 0 : (h < p.hq + p.hk ? h - p.hq : h - p.hq - p.hk);
   r.turns = h < p.hq + p.hk;
-  r.cache = nullptr;
   if (h < p.hq) {
     r.in = static_cast<const Elem*>(p.q) + t * p.ldq + (int64_t)h * p.d;
     r.out = static_cast<Elem*>(p.q_out) + t * p.ldqo + (int64_t)h * p.d;
