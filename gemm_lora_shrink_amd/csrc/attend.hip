@@ -391,7 +391,7 @@ template <typename Elem, int DP> struct RowBlock {
 #pragma unroll
       for (int i = b ? 0 : 4; i < 16; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[b][i]);
     float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-    mx = half_max(mx) * c;
+    mx = __fmul_rn(half_max(mx), c);
     if (__any(mx - m > kMost)) {
       float mn = mx - kBelow;
       if (kBelow > 0.f && mx - mn > kMost) mn = mx;  // a score that has no units left
@@ -405,6 +405,16 @@ template <typename Elem, int DP> struct RowBlock {
       m = mn;
     }
     const float ms = m == -INFINITY ? 0.f : m;
+    // s c - m is taken without rounding s c, as m's product was: by up to half a step of
+    // m the difference may pass kMost, or leave no weight at all.  Where that is more
+    // than a sixteenth of a power of two, s c is rounded too.
+    if (__builtin_expect(__any(fabsf(ms) >= 0x1p20f), 0)) {
+#pragma unroll
+      for (int b = 0; b < NS; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] = __fmul_rn(s[b][i], c);
+      c = 1.0f;
+    }
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int b = 0; b < NS; ++b)

@@ -67,3 +67,30 @@ def test_many_small_weights(B, L, place, gap, spread, heads, d, size, dtype):
     assert worst <= 1.0, worst
     near = (lse[0].double().cpu() - torch.logsumexp(s, -1)).abs()
     assert float((near / (rel[:, 0] + 4 * U * (math.log(L) + z[:, 0]))).max()) <= 1.0
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("heads,d", [(4, 64), (40, 128), (136, 64), (40, 256)])
+@pytest.mark.parametrize("power", [14, 15, 16, 17, 18, 19, 22, 30, 60])
+def test_scores_whose_units_are_large(power, heads, d, dtype):
+    """Scores so large that a step of fp32 passes the range of the weights: the key
+    with the largest one is all that is left, whichever tile it is in."""
+    dt, L, page = TYPES[dtype], 512, 64
+    k = torch.zeros(L, d, device="cuda", dtype=dt)
+    k[:, 0] = torch.randperm(L, generator=torch.Generator().manual_seed(power)).cuda() % 251  # exact in every type
+    k[77, 0] = 252.0
+    v = torch.randn(L, d, device="cuda", generator=torch.Generator("cuda").manual_seed(power)).to(dt)
+    q = torch.zeros(1, heads * d, device="cuda", dtype=dt)
+    q[0, ::d] = 16.0
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    lse = torch.empty(1, heads, device="cuda")
+    cache = [c.view(L // page, 1, page, d) for c in (k, v)]
+    out = glsa.tree_attention(q, *cache, ints([list(range(L // page))]), ints([L - 1]), ints([0, 1]), max_nodes=1,
+                              max_context=L - 1, scale=2.0 ** power, lse=lse,
+                              workspace=glsa.alloc_attention_workspace(1, 1, 1, L - 1, heads, 1, d, "cuda"))
+    # one weight and its value, over that weight: the weight's and the output's rounding
+    # to the type, and three in fp32 (exponential, reciprocal, product)
+    h = torch.finfo(dt).eps / 2
+    off = (8 * U if dtype == "f32" else 2 * h + 8 * U) * v[77].double().abs()
+    assert bool(((out.view(heads, d).double() - v[77].double()).abs() <= off).all())
+    assert torch.allclose(lse, torch.full_like(lse, 16.0 * 252.0 * 2.0 ** power), rtol=8 * U)
