@@ -373,7 +373,8 @@ def alloc_attention_workspace(n_seqs, n_tokens, max_nodes, max_context, q_heads,
 def tree_attention(q, k_cache, v_cache, page_table, context, q_start, *, max_nodes, max_context=None, mask=None,
                    scale=None, out=None, lse=None, workspace=None, stream=None):
     """Attention of the step's tokens over the context and the drafted tokens of
-    their own sequence.  Returns out ([T, q_heads * head_dim]).
+    their own sequence.  Returns out ([T, q_heads * head_dim]); rows of no sequence
+    are not written, so in an out of the call's own making they hold anything.
 
     q: [T, q_heads * head_dim], any row stride.  The tokens' own k and v are in
     the cache already (rotary puts them there).  page_table: int32 [B, pages];

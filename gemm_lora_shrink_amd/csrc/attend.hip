@@ -206,13 +206,13 @@ __device__ inline int splits_of(const AttendParams& p, int n, int ctx) {
 
 // Units of work are (chunk, sequence, head), in that order.
 // SPREAD: they go to the XCDs (b % 8) in turn.  The first chunks, the long ones
-// where contexts differ, are on all XCDs from the start: 24.9 us for 33 with the
+// where contexts differ, are on all XCDs from the start: 25.5 us for 33.5 with the
 // order below for 8 fp32 sequences of 46 to 1500 keys, 351 for 359 for 256 bf16
 // ones of 128 to 4096.
 // Else an XCD takes a contiguous range of the order sequence, head, chunk: heads
 // side by side in memory are read through one L2, which is worth more where the
-// matrix cores bound the time: 148 us for 156 for 16 sequences of 256 to 8192
-// keys and 23 to 45 nodes, 65.5 for 68.7 for one of 32768 keys and 64 nodes.
+// matrix cores bound the time: 132.8 us for 134.6 for 16 sequences of 256 to 8192
+// keys and 23 to 45 nodes (one of 32768 keys and 64 nodes: 65 either way).
 // Either way the row tiles of a unit follow one another on one XCD.
 template <int ROWS, bool SPREAD>
 __device__ inline Work work_of(const AttendParams& p) {
@@ -709,8 +709,9 @@ __device__ __forceinline__ const char* piece_of(const AttendParams& p, const cha
 // (2.2 GB): 350 us, 6.3 TB/s.  One workgroup a compute unit, 16 KB in flight a
 // wave; two push each other's rows out of L2 (4.9 TB/s).  Loads are non-temporal,
 // each row is read once.  fp32 heads of 64 have too little in flight in one
-// workgroup and run two a compute unit: 33 us for 36 (8 sequences of 46 to 1500
-// keys).  Heads of 256 elements spill some registers: 64 x 8192 keys (1.07 GB) 253 us.
+// workgroup and run two a compute unit: 25.5 us for 29.8 (8 sequences of 46 to 1500
+// keys).  Heads of 256 elements spill some registers: 64 sequences of 4096 keys, 16
+// + 4 bf16 heads (1.07 GB), 254 us.
 template <typename Elem, int DP, int NW>
 __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void attend_narrow_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
@@ -876,8 +877,9 @@ __global__ __launch_bounds__(NW * 64, (Rows<Elem, DP>::kNarrowWaves)) void atten
 // 136), whose outputs leave no registers for the kernel below: four waves of 32
 // rows share tiles of 32 keys, double buffered; a wave fetches a quarter of each
 // tile's rows.  One workgroup a compute unit.  Bound by the matrix cores and the
-// weights in turn, heads of 256 elements by spilled registers too (fp32: 228 a
-// lane; 3 sequences of 12 nodes over 1949 keys, 32 + 8 fp32 heads: 229 us).
+// weights in turn, heads of 256 elements by spilled registers too (fp32 234 a lane,
+// 16-bit 74): 3 sequences of 12 nodes over 1949 keys, 32 + 8 fp32 heads of 256, 228
+// us; 4 of 32 nodes over 8224, 16 + 4 bf16 heads of 256 (135 MB, 17 GFLOP), 113 us.
 template <typename Elem, int DP>
 __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p) {
   using R = Rows<Elem, DP>;
@@ -1002,10 +1004,11 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_kernel(AttendParams p
 // addresses of four stages are found together, one a lane, at the second step of
 // the four before; their page numbers are requested two steps earlier.
 // Bound by the issue of a stage's work, matrix products (0.5 us a group), weights
-// (0.5), the loads' issue and addresses (0.4): 2.6 us a stage of 64 keys with every
-// compute unit at work, of which keys in L2 save a fifth.  One sequence of 64 nodes
-// over 32768 keys, 32 + 8 bf16 heads of 128: 63 us (134 MB, 34 GFLOP; 8 us are the
-// join); 32 sequences of 64 over 4032: 178 us, 760 TFLOP/s.  Measured and slower:
+// (0.5), the loads' issue and addresses (0.4): 2.3 to 2.6 us a stage of 64 keys with
+// every compute unit at work, of which keys in L2 save a fifth.  One sequence of 64
+// nodes over 32768 keys, 32 + 8 bf16 heads of 128: 61 to 65 us (134 MB, 34 GFLOP; 8
+// are the join); 32 fp16 sequences of 64 over 4032: 185 us, 730 TFLOP/s.  Measured and
+// slower, each against the kernel as it was then:
 // all eight waves in step (75 for 71 us on the first), the loads before the products
 // (66 for 64; 143 for 132 on 16 ragged sequences), spread over the products (78) or
 // over the weights (72), chunks for two workgroups a compute unit in turn (89), no
@@ -1231,7 +1234,7 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendParams p) {
   float L = 0.f;
   f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
   // four chunks' loads at a time: one by one, each waited for the one before it
-  // (13.3 -> 8.1 us for 2048 rows of 32 chunks, 33 MB)
+  // (13.3 -> 8.1 us for 2048 rows of 31 chunks, 33 MB)
   constexpr int kAhead = 4;
   const int step = 64 / lanes;
   for (int s = lane / lanes; s < splits; s += kAhead * step) {
@@ -1302,9 +1305,10 @@ AttendPlan attend_kind(int elem, int32_t nodes, int32_t group, int32_t d) {
 // How the keys are cut: even chunks, so long that about `groups` workgroups run
 // in all where every sequence is as long as its bound, and no shorter than
 // kMinChunk keys.  One workgroup a compute unit of the kernel with turns, whose
-// prologue, last join and parts cost 25 us a workgroup; two of the wide one; four of
-// the narrow one (64 x 8192 keys: 175 us, with eight 185; one sequence of 131072:
-// 42, with eight 53).
+// prologue, parts and join cost some 24 us (one sequence of 32768 keys and 64 nodes:
+// 65 us, with two 84); two of the wide one; four of the narrow one (64 sequences of
+// 4096 keys, 32 + 8 bf16 heads of 128: 176 us, with eight 188; one of 32768: 43, with
+// eight 54).
 constexpr int64_t kMinChunk = 256;
 constexpr int64_t kMaxChunk = (int64_t)1 << 30;
 

