@@ -389,8 +389,8 @@ def _own(s, case):
                                              max_nodes=case["nodes"], max_context=case["ctx"], mask=s["mask"],
                                              out=s["out"], workspace=s["workspace"])
     refs, table, page = s["refs"].copy_(s["refs_at_start"]), s["table"].copy_(s["table_at_start"]), case["page"]
-    if "tensors" not in s:  # a server keeps the list
-        s["tensors"] = [t for layer in s["caches"] for t in layer]
+    if "tensors" not in s:  # a server keeps both
+        s["tensors"] = glsa.PagedTensors(t for layer in s["caches"] for t in layer)
         s["workspace"] = glsa.alloc_pages_workspace(refs.numel(), case["B"], refs.device)
     if op == "fork":
         glsa.fork_sequences(refs, table, s["parents"], s["rows"], s["fork_lengths"], page_size=page, tensors=s["tensors"],
