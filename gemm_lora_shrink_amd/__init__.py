@@ -23,7 +23,9 @@ Entry points (same names as the C ABI):
 
 and, from .attention (include/lora_attention.h), what follows the q/k/v
 projection: rope_table, rotary, qk_norm_rotary, build_tree, tree_attention,
-keep_path.
+keep_path; from .cache (include/lora_cache.h) a cache in 8 bits: store_quantized,
+tree_attention_quantized, keep_path_quantized; and a cache's pages: reserve_pages,
+fork_sequences, release_pages, compact_pages, copy_pages.
 """
 
 import ctypes
@@ -577,3 +579,7 @@ def pack_b_rank_rows(B, ranks_host, *, stream=None):
 from .attention import (  # noqa: E402
     alloc_attention_workspace, attention_workspace_bytes, build_tree, keep_path, qk_norm_rotary, rope_frequencies,
     rope_table, rotary, tree_attention)
+from .cache import (  # noqa: E402
+    PagedTensors, QuantizedCache, alloc_pages_workspace, alloc_quantized_cache, alloc_quantized_workspace, compact_pages,
+    copy_pages, fork_sequences, keep_path_quantized, pages_workspace_bytes, quantized_workspace_bytes, release_pages,
+    reserve_pages, store_quantized, tree_attention_quantized)

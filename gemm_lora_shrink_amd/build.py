@@ -14,7 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblora_mi355x.so")
 SOURCES = ["api.hip", "segments.hip", "shrink.hip", "bgmv.hip", "sgmv.hip", "fused.hip", "embedding.hip", "slots.hip", "mask.hip",
-           "attention_api.hip", "rotary.hip", "tree.hip", "attend.hip"]
+           "attention_api.hip", "rotary.hip", "tree.hip", "attend.hip",
+           "cache_api.hip", "quantized.hip", "attend_quantized.hip", "pages.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

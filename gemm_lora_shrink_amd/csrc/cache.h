@@ -1,0 +1,151 @@
+// Internal definitions of the quantized cache and the pages of a cache
+// (include/lora_cache.h): what a byte holds, the parameter blocks passed to the
+// kernels and the host launchers.
+#pragma once
+
+#include "../../include/lora_cache.h"
+#include "attention.h"
+
+namespace lora {
+
+constexpr int kExpLow = -126;  // the smallest exponent of a block
+
+// What a byte holds.
+struct E4m3 {
+  static constexpr int kTop = 119;         // the largest exponent
+  static constexpr float kLargest = 448.f;  // the largest number, 1.75 * 2^8
+  static constexpr int kLargestExp = 8;
+  static constexpr uint32_t kLargestMantissa = 0x600000u;
+  __device__ static inline void numbers(uint32_t w, float* x) {  // of a word's four bytes
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    x[0] = a[0];
+    x[1] = a[1];
+    x[2] = b[0];
+    x[3] = b[1];
+  }
+  // The nearest numbers, ties to even; |x| beyond the largest becomes it.
+  __device__ static inline uint32_t bytes(const float* x) {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // (the median drops a NaN)
+      y[i] = x[i] != x[i] ? x[i] : __builtin_amdgcn_fmed3f(x[i], -kLargest, kLargest);
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+  }
+};
+struct Int8 {
+  static constexpr int kTop = 121;
+  static constexpr float kLargest = 127.f;  // 1.984375 * 2^6
+  static constexpr int kLargestExp = 6;
+  static constexpr uint32_t kLargestMantissa = 0x7e0000u;
+  __device__ static inline void numbers(uint32_t w, float* x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(w >> (8 * i));
+  }
+  __device__ static inline uint32_t bytes(const float* x) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float y = x[i] != x[i] ? 0.f : __builtin_amdgcn_fmed3f(x[i], -kLargest, kLargest);
+      w |= ((uint32_t)(int)__builtin_rintf(y) & 0xffu) << (8 * i);
+    }
+    return w;
+  }
+};
+
+// 2^e, for e from -126 to 127.
+__device__ inline float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+template <typename F> __device__ inline int exponent_of(int8_t stored) {
+  return stored < kExpLow ? kExpLow : (stored > F::kTop ? F::kTop : stored);
+}
+
+// A layer's quantized cache as the kernels see it (strides in bytes).
+struct QuantizedView {
+  void *k, *v;
+  int8_t *k_exp, *v_exp;
+  int64_t k_page, k_head, k_row, v_page, v_head, v_row;
+  int64_t k_exp_page, k_exp_head, v_exp_page, v_exp_head;
+  int64_t n_pages;
+  FastDiv page, block;  // by the page size, by the rows of a block
+};
+
+struct StoreParams {
+  const void *k, *v;
+  int64_t ldk, ldv;
+  QuantizedView cache;
+  const int32_t* rows;
+  int64_t n_rows;  // n_pages * page_size
+  int32_t T, hk, d;
+  int32_t chunk, lane_shift;  // filled by the launcher: tokens of a workgroup, log2 of the lanes of a row
+};
+
+constexpr int kKeepLayers = 64;  // layers of one launch
+struct KeepQuantizedParams {
+  const int32_t *page_table, *context, *path, *n_kept;
+  int64_t ld_table, ld_path;
+  QuantizedView cache;  // its pointers: unused
+  int32_t n_table, n_path, kv_heads, d;
+  void *k[kKeepLayers], *v[kKeepLayers];
+  int8_t *k_exp[kKeepLayers], *v_exp[kKeepLayers];
+};
+
+struct AttendQuantizedParams {
+  const void* q;
+  void* out;
+  int64_t ldq, ldo;
+  float* lse;  // nullable
+  QuantizedView cache;
+  const int32_t *page_table, *context, *q_start;
+  const uint64_t* mask;  // nullable: a chain
+  int64_t ld_table;
+  float scale;
+  int32_t T, B, hq, hk, d, n_table, max_nodes, max_context, mask_words;
+  FastDiv group;  // by q_heads / kv_heads
+};
+
+struct PoolParams {
+  int32_t* refs;
+  int64_t n_pages;
+  int32_t* table;
+  int64_t ld_table;
+  int32_t n_table, B;
+  FastDiv page;      // by the page size
+  int32_t* scratch;  // the workspace
+};
+struct ForkParams {
+  const int32_t* from;
+  int64_t ld_from;
+  int32_t B_from, n;
+  const int32_t *parents, *children, *lengths;
+  int32_t *source, *target, *missing;  // missing nullable
+};
+
+struct CopyParams {
+  lora_paged_tensor t[LORA_COPY_TENSORS];
+  int64_t n_pages;
+  const int32_t *source, *target, *count;  // count nullable
+  int32_t n, unit;                         // bytes of an access
+};
+
+// Whether launch_store_quantized's grid holds T tokens.
+bool store_quantized_fits(int32_t T);
+hipError_t launch_store_quantized(lora_dtype dt, int format, StoreParams p, hipStream_t stream);
+hipError_t launch_keep_quantized(int format, const KeepQuantizedParams& p, int32_t n_layers, int32_t B,
+                                 hipStream_t stream);
+hipError_t launch_attend_quantized(lora_dtype dt, int format, const AttendQuantizedParams& p, hipStream_t stream);
+bool attend_quantized_fits(lora_dtype dt, int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
+                           int32_t d);
+int64_t attend_quantized_need_bytes(lora_dtype dt, int32_t B, int32_t T, int32_t max_nodes, int32_t max_context,
+                                    int32_t hq, int32_t hk, int32_t d);
+int64_t attend_quantized_most_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq,
+                                    int32_t hk, int32_t d);
+
+int64_t pages_scratch_bytes(int64_t n_pages, int32_t n_seqs);
+hipError_t launch_reserve(const PoolParams& p, const int32_t* lengths, int32_t* missing, hipStream_t stream);
+hipError_t launch_fork(const PoolParams& p, const ForkParams& f, hipStream_t stream);
+hipError_t launch_release(const PoolParams& p, const int32_t* rows, const int32_t* keep, int32_t n, hipStream_t stream);
+hipError_t launch_compact(const PoolParams& p, int32_t* source, int32_t* target, int32_t* n_live, int32_t* n_moves,
+                          hipStream_t stream);
+hipError_t launch_copy_pages(const CopyParams& p, int32_t n_tensors, hipStream_t stream);
+
+}  // namespace lora
