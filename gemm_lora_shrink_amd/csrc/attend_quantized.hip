@@ -1,128 +1,865 @@
-// Attention of a step's tokens over a quantized cache: a wave a row and query
-// head, one key a lane for the scores, four elements a lane for the values.
+// Attention of a step's tokens over a quantized cache: the work, the row blocks
+// and the join of the other attention kernels, with keys and values that lie in
+// memory as bytes with an exponent for each block of rows.
+//
+// A byte's number is a bf16 number, and so is that number times a power of two,
+// so keys and values enter the products exactly, as bf16 (on this chip one
+// instruction makes two of them from two e4m3 bytes and a scale).  q and the
+// softmax weights do too where they are bf16; fp16 ones enter as the sum of two
+// bf16 numbers, fp32 ones of three, each of which has 8 bits of them.
+#include <algorithm>
+
+#include "attend_unit.h"
 #include "cache.h"
 
 namespace lora {
 
 namespace {
 
-constexpr int kThreads = 256, kWaves = 4;
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4_rw;
+typedef __attribute__((address_space(3))) const int lds_int;
+typedef __attribute__((address_space(3))) const f32x4 lds_f32x4;
+typedef __attribute__((address_space(3))) float lds_float_rw;
+typedef __attribute__((address_space(1))) const int8_t global_int8;
+typedef __attribute__((address_space(1))) const int32_t global_int;
 
-template <typename Elem, typename F>
-__global__ __launch_bounds__(kThreads) void attend_quantized_kernel(AttendQuantizedParams p) {
-  warm_args(p);
-  __shared__ float s_q[kWaves][256];
-  __shared__ float s_w[kWaves][64];
-  __shared__ const char* s_row[kWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int b = blockIdx.y, r = (int)blockIdx.x * kWaves + wave;
-  const int i = r / p.hq, h = r - i * p.hq;
-  const int64_t start = p.q_start[b];
-  int64_t n = (int64_t)p.q_start[b + 1] - start;
-  if (start < 0 || start > p.T) return;
-  n = n > p.T - start ? p.T - start : n;
-  n = n > p.max_nodes ? p.max_nodes : n;
-  if (i >= n) return;
-  int64_t ctx = p.context[b];
-  ctx = ctx < 0 ? 0 : (ctx > p.max_context ? p.max_context : ctx);
-  const int64_t row = start + i;
-  const int kv = (int)p.group.div((uint32_t)h);
-  const QuantizedView& c = p.cache;
-  const Elem* q = static_cast<const Elem*>(p.q) + row * p.ldq + (int64_t)h * p.d;
-  for (int e = lane; e < p.d; e += 64) {
-    uint32_t bits;
-    if constexpr (sizeof(Elem) == 4) bits = reinterpret_cast<const uint32_t*>(q)[e];
-    else bits = reinterpret_cast<const uint16_t*>(q)[e];
-    s_q[wave][e] = Traits<Elem>::elem_to_float(bits) * p.scale * kLog2e;
-  }
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  const int64_t end = ctx + (p.mask ? n : i + 1);
-  const int at = 4 * lane;
-  for (int64_t k0 = 0; k0 < end; k0 += 64) {
-    const int64_t pos = k0 + lane;
-    float s = -INFINITY, v_scale = 0.f;
-    const char* v_row = nullptr;
-    bool seen = pos < end;
-    if (seen && pos >= ctx && p.mask) {
-      const int64_t node = pos - ctx;
-      seen = (node >> 6) < p.mask_words && (p.mask[row * p.mask_words + (node >> 6)] >> (node & 63) & 1);
-    }
-    if (seen) {
-      const int64_t col = c.page.div((uint32_t)pos);
-      const int64_t page = col < p.n_table ? p.page_table[b * p.ld_table + col] : -1;
-      seen = page >= 0 && page < c.n_pages;
-      if (seen) {
-        const int place = (int)(pos - col * c.page.d), block = (int)c.block.div((uint32_t)place);
-        const char* k_row = static_cast<const char*>(c.k) + page * c.k_page + kv * c.k_head + place * c.k_row;
-        v_row = static_cast<const char*>(c.v) + page * c.v_page + kv * c.v_head + place * c.v_row;
-        v_scale = power_of_two(exponent_of<F>(c.v_exp[page * c.v_exp_page + kv * c.v_exp_head + block]));
-        float sum = 0.f;
-        for (int e = 0; e < p.d; e += 4) {
-          float x[4];
-          F::numbers(*reinterpret_cast<const uint32_t*>(k_row + e), x);
-          for (int j = 0; j < 4; ++j) sum = __builtin_fmaf(x[j], s_q[wave][e + j], sum);
-        }
-        s = sum * power_of_two(exponent_of<F>(c.k_exp[page * c.k_exp_page + kv * c.k_exp_head + block]));
-      }
-    }
-    float mx = s;
-    for (int x = 32; x; x >>= 1) mx = fmaxf(mx, __shfl_xor(mx, x));
-    const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.f : mn;
-    const float f = __builtin_amdgcn_exp2f(m - ms);
-    const float w = seen ? __builtin_amdgcn_exp2f(s - ms) : 0.f;
-    m = mn;
-    float sum = w;
-    for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
-    l = l * f + sum;
-    for (int e = 0; e < 4; ++e) o[e] *= f;
-    s_w[wave][lane] = w * v_scale;
-    s_row[wave][lane] = v_row;
-    __builtin_amdgcn_wave_barrier();
-    if (at < p.d)
-      for (int j = 0; j < 64; ++j) {
-        const char* vr = s_row[wave][j];
-        if (!vr) continue;
-        float x[4];
-        F::numbers(*reinterpret_cast<const uint32_t*>(vr + at), x);
-        for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(s_w[wave][j], x[e], o[e]);
-      }
-    __builtin_amdgcn_wave_barrier();
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  Elem* out = static_cast<Elem*>(p.out) + row * p.ldo + (int64_t)h * p.d;
-  if (at < p.d)
-    for (int e = 0; e < 4; ++e) out[at + e] = static_cast<Elem>(o[e] * inv);
-  if (p.lse && lane == 0) p.lse[row * p.hq + h] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+// Two words (eight bytes) as eight bf16 numbers, times `scale`.
+template <typename F> __device__ __forceinline__ u32x4 to_bf16(uint32_t w0, uint32_t w1, float scale);
+template <> __device__ __forceinline__ u32x4 to_bf16<E4m3>(uint32_t w0, uint32_t w1, float scale) {
+  return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, true)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, true))};
+}
+template <> __device__ __forceinline__ u32x4 to_bf16<Int8>(uint32_t w0, uint32_t w1, float scale) {
+  float x[8];
+  Int8::numbers(w0, x);
+  Int8::numbers(w1, x + 4);
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = pack2_bf16(x[2 * i] * scale, x[2 * i + 1] * scale);
+  return r;
+}
+// Bit 7 of each byte that is a NaN.
+template <typename F> __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return F::kHasNan ? ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : 0u;
 }
 
-int64_t grid_of(int32_t max_nodes, int32_t hq) { return ceil_div((int64_t)max_nodes * hq, kWaves); }
+// How many bf16 numbers a number of the call's type enters as.
+template <typename Out> constexpr int kTerms = sizeof(Out) == 4 ? 3 : Traits<Out>::kDtype == LORA_F16 ? 2 : 1;
 
-template <typename Elem>
-hipError_t launch(int format, const AttendQuantizedParams& p, hipStream_t stream) {
-  const dim3 grid((unsigned)grid_of(p.max_nodes, p.hq), (unsigned)p.B);
-  if (format == LORA_CACHE_E4M3)
-    hipLaunchKernelGGL((attend_quantized_kernel<Elem, E4m3>), grid, dim3(kThreads), 0, stream, p);
-  else
-    hipLaunchKernelGGL((attend_quantized_kernel<Elem, Int8>), grid, dim3(kThreads), 0, stream, p);
+// A byte to a dword of LDS for each lane.
+__device__ inline void byte_to_lds(const char* g, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_ubyte %2, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(g)
+      : "memory");
+}
+
+// The address of a key's exponent; strides below 2^32 (the host checks).
+struct ExpAt {
+  uint64_t base;
+  uint32_t page;
+  __device__ __forceinline__ uint64_t at(uint32_t id, uint32_t block) const { return base + (uint64_t)id * page + block; }
+};
+__device__ inline ExpAt exp_at(const AttendQuantizedParams& p, int h, bool is_v) {
+  return ExpAt{reinterpret_cast<uint64_t>(is_v ? p.v_exp : p.k_exp) + (uint64_t)h * (uint64_t)(is_v ? p.v_exp_head : p.k_exp_head),
+               (uint32_t)(is_v ? p.v_exp_page : p.k_exp_page)};
+}
+
+// ---- up to 32 rows ----------------------------------------------------------
+
+// A tile of a wave: 8 KB of keys and 8 KB of values, rows of DP bytes in pieces of
+// 16, piece c of row r at c ^ swz(r): 16 consecutive rows at one piece (the keys'
+// reads) and rows 4 i .. 4 i + 3 and 4 i + 8 .. 4 i + 11 at two neighbouring
+// pieces (the values' transposing reads) lie in different banks.
+template <int DP> struct Tile8 {
+  static constexpr int kKeys = 8192 / DP, kBlocks = kKeys / kBlock;
+  static constexpr int kPieces = DP / 16;
+  static constexpr int kPerLoad = 1024 / DP;  // rows of one 64-lane load
+  static constexpr int NL = 8;                // loads of the keys or values
+  static constexpr int NI = (kKeys + 63) / 64;    // loads of page numbers
+  static constexpr int NE = kKeys / 32;           // loads of exponents, keys and values
+  __device__ static inline int swz(int r) {
+    if (DP == 64) return (r >> 2) & 3;
+    if (DP == 128) return (((r >> 3) & 1) << 2) | (((r >> 1) & 1) << 1) | ((r >> 2) & 1);
+    return (((r >> 3) & 1) << 3) | (((r >> 1) & 1) << 2) | ((r & 1) << 1) | ((r >> 2) & 1);
+  }
+};
+
+// Up to 32 rows: four waves hold the same rows and take the chunk's tiles of 8 KB
+// of keys in turn, each through LDS of its own: a wave waits for no other until
+// their outputs meet at the end.  Two tiles are in flight a wave (32 KB): after a
+// tile's scores the keys of the tile after the next take its keys' place, after
+// its products with the values their values.  Page numbers come four tiles ahead.
+// Loads past the chunk's end go to a row of zeros, so that the number of loads in
+// flight is the same in every turn.
+template <typename Out, typename F, int DP>
+__global__ __launch_bounds__(256, 1) void attend_narrow_quantized_kernel(AttendQuantizedParams p) {
+  using L8 = Tile8<DP>;
+  constexpr int NT = kTerms<Out>, NW = 4, KT = L8::kKeys, NB = L8::kBlocks, NL = L8::NL, NI = L8::NI, NE = L8::NE;
+  using Block = RowBlock<bf16_t, DP, Out, NT>;
+  constexpr int kDB = DP / kBlock;
+  __shared__ __attribute__((aligned(1024))) char s_kv[NW][2][2][8192];
+  __shared__ __attribute__((aligned(16))) const char* s_row[NW][2 * KT];
+  __shared__ __attribute__((aligned(16))) int s_exp[NW][2][2 * KT < 64 ? 64 : 2 * KT];
+  __shared__ int s_id[NW][4][NI * 64];
+  __shared__ float s_ml[NW][2][kBlock];
+  warm_args(p);
+  const Work w = work_of<kBlock, true>(p);
+  if (w.none) return;
+  Block rb;
+  rb.template init<true>(p, w, w.row0);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = rb.lane, r32 = rb.r32, hi = rb.hi;
+  const float c = p.scale == 0.f ? 1.0f : fabsf(p.scale) * kLog2e;
+  // this wave's tiles, the first nf of them wholly inside the context
+  const auto tiles = [&](int keys, bool whole) {
+    const int all = keys <= 0 ? 0 : whole ? keys / KT : (keys + KT - 1) / KT;
+    return all > wave ? (all - wave + NW - 1) / NW : 0;
+  };
+  const int nt = tiles(w.k1 - w.k0, false), nf = tiles(min(w.ctx, w.k1) - w.k0, true);
+  const auto first_key = [&](int t) { return (int64_t)w.k0 + ((int64_t)wave + (int64_t)NW * t) * KT; };
+  const HeadAt hk = head_at<uint8_t>(p, w.h, false), hv = head_at<uint8_t>(p, w.h, true);
+  const ExpAt ek = exp_at(p, w.h, false), ev = exp_at(p, w.h, true);
+
+  const auto fetch_ids = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      int col;
+      const PageAt a = page_at(p, first_key(t) + 64 * i + lane % KT, w.k1, col);
+      word_to_lds(entry_of(p, w.b, a, col), (uint32_t)(uintptr_t)&s_id[wave][t & 3][64 * i]);
+    }
+  };
+  // The rows' addresses to LDS, the exponents on their way; returns which rows are keys.
+  const char* exps[NE];
+  struct Valid {
+    uint32_t of[NB];
+  };
+  const auto find_rows = [&](int t) {
+    Valid v;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      int col;
+      const PageAt a = page_at(p, first_key(t) + 64 * i + lane % KT, w.k1, col);
+      const uint32_t id = (uint32_t)s_id[wave][t & 3][64 * i + lane];
+      const bool valid = a.in_table && id < (uint64_t)p.cache.n_pages && (int)id >= 0;
+      const uint32_t block = p.block.div((uint32_t)a.place);
+      const char* none = reinterpret_cast<const char*>(g_zero_row);
+      const char* k = valid ? reinterpret_cast<const char*>(hk.row_at(id, a.place)) : none;
+      const char* v_row = valid ? reinterpret_cast<const char*>(hv.row_at(id, a.place)) : none;
+      const char* ke = valid ? reinterpret_cast<const char*>(ek.at(id, block)) : none;
+      const char* ve = valid ? reinterpret_cast<const char*>(ev.at(id, block)) : none;
+      if constexpr (KT >= 64) {
+        s_row[wave][64 * i + lane] = k;
+        s_row[wave][KT + 64 * i + lane] = v_row;
+        exps[2 * i] = ke;
+        exps[2 * i + 1] = ve;
+      } else {
+        s_row[wave][lane] = hi ? v_row : k;
+        exps[0] = hi ? ve : ke;
+      }
+      const uint64_t all = __ballot(valid);
+      v.of[(2 * i) % NB] = (uint32_t)all;
+      if constexpr (NB > 1) v.of[2 * i + 1] = (uint32_t)(all >> 32);
+    }
+    return v;
+  };
+  const auto load = [&](int which, int t) __attribute__((always_inline)) {
+    const uint32_t lds = (uint32_t)(uintptr_t)s_kv[wave][t & 1][which];
+    const char* a[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int r = i * L8::kPerLoad + lane / L8::kPieces;
+      const int piece = (lane % L8::kPieces) ^ L8::swz(r);
+      const char* row = s_row[wave][which * KT + r];
+      if (p.d != DP && piece * 16 >= p.d) row = reinterpret_cast<const char*>(g_zero_row);
+      a[i] = row + 16 * piece;
+    }
+#pragma unroll
+    for (int i = 0; i < NL; i += 2) two_rows_to_lds<true>(a[i], a[i + 1], lds + 1024 * i);
+  };
+  // s_exp: of the keys at [key], of the values at [KT + key]
+  const auto load_exps = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      byte_to_lds(exps[i], (uint32_t)(uintptr_t)&s_exp[wave][t & 1][KT >= 64 ? (i % 2) * KT + (i / 2) * 64 : 0]);
+  };
+
+  Valid valid[2];  // of this tile and the next
+  if (nt > 0) {
+    fetch_ids(0);
+    fetch_ids(1);
+    wait_loads<0>();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      valid[t] = find_rows(t);
+      load(0, t);
+      load_exps(t);
+      fetch_ids(t + 2);
+      load(1, t);
+    }
+  }
+  const auto tile = [&](int t, auto tail) __attribute__((always_inline)) {
+    constexpr bool kTail = decltype(tail)::value;
+    // in flight, in order: K E (t), I (t + 2), V (t), K E (t + 1), I (t + 3), V (t + 1)
+    wait_loads<3 * NL + NE + 2 * NI>();
+    const uint32_t keys = (uint32_t)(uintptr_t)s_kv[wave][t & 1][0];
+    const char* const values = s_kv[wave][t & 1][1];
+    const uint32_t exp_lds = (uint32_t)(uintptr_t)s_exp[wave][t & 1];
+    f32x16 s[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int key = 32 * b + r32;
+      const float ks = power_of_two(exponent_of<F>((int8_t)*(lds_int*)(lds_byte*)(uintptr_t)(exp_lds + 4 * key)));
+      u32x4 raw[DP / 32];
+#pragma unroll
+      for (int j = 0; j < DP / 32; ++j)
+        raw[j] = *(lds_u32x4*)(lds_byte*)(uintptr_t)(keys + key * DP + (((2 * j + hi) ^ L8::swz(key)) << 4));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < DP / 32; ++j) {
+        const uint32_t w0 = raw[j][0], w1 = raw[j][1], w2 = raw[j][2], w3 = raw[j][3];
+        const u32x4 a0 = to_bf16<F>(w0, w1, ks), a1 = to_bf16<F>(w2, w3, ks);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          s[b] = Mma32<bf16_t>::mma(a0, rb.q[n][2 * j], s[b]);
+          s[b] = Mma32<bf16_t>::mma(a1, rb.q[n][2 * j + 1], s[b]);
+        }
+      }
+    }
+    // the values' exponents become factors
+    if constexpr (KT >= 64) {
+#pragma unroll
+      for (int i = 0; i < KT / 64; ++i) {
+        int* e = &s_exp[wave][t & 1][KT + 64 * i + lane];
+        *reinterpret_cast<float*>(e) = power_of_two(exponent_of<F>((int8_t)*e));
+      }
+    } else if (hi) {
+      int* e = &s_exp[wave][t & 1][lane];
+      *reinterpret_cast<float*>(e) = power_of_two(exponent_of<F>((int8_t)*e));
+    }
+    wait_lds();
+    wait_loads<3 * NL + NE + NI>();  // page numbers of t + 2
+    Valid now = valid[0];
+    valid[0] = valid[1];
+    valid[1] = find_rows(t + 2);
+    load(0, t + 2);
+    // exponents of t + 2 would take the place of the factors: they wait in registers for their turn
+
+    uint32_t seen[NB];
+    bool uneven = false;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      seen[b] = now.of[b];
+      if constexpr (kTail) {
+        seen[b] &= rb.sees(p, w, (int)(first_key(t) + 32 * b));
+        uneven |= __any(seen[b] != now.of[b]);
+      }
+      if (__any(seen[b] != ~0u)) rb.mask_scores(s[b], seen[b]);
+    }
+    rb.weigh(s, c);
+    typename Block::Weights weights[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 f = *(lds_f32x4*)(lds_byte*)(uintptr_t)(exp_lds + 4 * (KT + 32 * b + 8 * g + 4 * hi));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[b][4 * g + e] *= f[e];
+      }
+      weights[b] = rb.pack(s[b]);
+    }
+    wait_lds();
+    load_exps(t + 2);
+    wait_loads<3 * NL + 2 * NE + NI>();  // values of t
+    bool odd = false;
+    if constexpr (kTail && F::kHasNan) {
+      if (uneven) {
+        uint32_t any = 0;
+        for (int i = lane; i < 2048; i += 64) any |= nan_bytes<F>(reinterpret_cast<const uint32_t*>(values)[i]);
+        odd = __any(any != 0);
+      }
+    }
+    const auto add_values = [&](auto leave_out) __attribute__((always_inline)) {
+      const int j = lane & 15, g1 = (lane >> 4) & 1, i = j >> 1;
+      const int row = (i < 4 ? i : i + 4) + 4 * hi;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int key = 32 * b + 16 * u + row;
+          i32x2 v[kDB];
+#pragma unroll
+          for (int db = 0; db < kDB; ++db)
+            v[db] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                (lds_i32x2*)(lds_byte*)(uintptr_t)((uint32_t)(uintptr_t)values + key * DP +
+                                                   (((2 * db + g1) ^ L8::swz(key)) << 4) + 8 * (j & 1)));
+#pragma unroll
+          for (int db = 0; db < kDB; ++db) {
+            uint32_t w0 = (uint32_t)v[db][0], w1 = (uint32_t)v[db][1];
+            if constexpr (decltype(leave_out)::value) {
+              w0 &= ~((nan_bytes<F>(w0) >> 7) * 0xffu);
+              w1 &= ~((nan_bytes<F>(w1) >> 7) * 0xffu);
+            }
+            const u32x4 a = to_bf16<F>(w0, w1, 1.0f);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) rb.o[db] = Mma32<bf16_t>::mma(a, weights[b].w[n][u], rb.o[db]);
+          }
+        }
+    };
+    if (kTail && odd) {
+      add_values(Yes{});
+      // NaN reaches the rows that see its key; in the product it would have met a masked weight of 0
+#pragma unroll 1
+      for (int k = 0; k < KT; ++k) {
+        uint32_t seen_k = 0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          if (k / 32 == b) seen_k = seen[b];
+        const bool mine = (seen_k >> (k % 32)) & 1;
+#pragma unroll
+        for (int db = 0; db < kDB; ++db)
+#pragma unroll
+          for (int qd = 0; qd < 4; ++qd) {
+            const int at = rb.element(db, qd);
+            const uint32_t nan = nan_bytes<F>(
+                *reinterpret_cast<const uint32_t*>(values + k * DP + (((at >> 4) ^ L8::swz(k)) << 4) + (at & 15)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (mine && (nan >> (8 * e + 7)) & 1) rb.o[db][4 * qd + e] = NAN;
+          }
+      }
+    } else {
+      add_values(No{});
+    }
+    wait_lds();
+    fetch_ids(t + 4);
+    load(1, t + 2);
+  };
+  int t = 0;
+  for (; t < nf; ++t) tile(t, No{});
+  for (; t < nt; ++t) tile(t, Yes{});
+  wait_loads<0>();
+
+  // the waves' outputs meet: weights to their common maximum, then block db of
+  // the output is summed and stored by wave db % NW
+  const float l = half_sum(rb.l);
+  if (hi == 0) {
+    s_ml[wave][0][r32] = rb.m;
+    s_ml[wave][1][r32] = l;
+  }
+  f32x4* red = reinterpret_cast<f32x4*>(&s_kv[wave][0][0][0]);
+#pragma unroll
+  for (int db = 0; db < kDB; ++db)
+#pragma unroll
+    for (int qd = 0; qd < 4; ++qd)
+      red[(db * 4 + qd) * 64 + lane] =
+          f32x4{rb.o[db][4 * qd], rb.o[db][4 * qd + 1], rb.o[db][4 * qd + 2], rb.o[db][4 * qd + 3]};
+  __syncthreads();
+  float M = -INFINITY, L = 0.f, f[NW];
+#pragma unroll
+  for (int i = 0; i < NW; ++i) M = fmaxf(M, s_ml[i][0][r32]);
+  const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    f[i] = __builtin_amdgcn_exp2f(s_ml[i][0][r32] - ms);
+    L += s_ml[i][1][r32] * f[i];
+  }
+  if (rb.row < 0) return;
+  const bool whole = w.whole;
+  const float inv = whole ? inverse(L) : 1.0f;
+  for (int db = wave; db < kDB; db += NW) {
+#pragma unroll
+    for (int qd = 0; qd < 4; ++qd) {
+      const int at = rb.element(db, qd);
+      if (at >= p.d) continue;
+      f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const f32x4 x = reinterpret_cast<const f32x4*>(&s_kv[i][0][0][0])[(db * 4 + qd) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(x[e], f[i], sum[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] *= inv;
+      if (whole) rb.store4(p, rb.row, rb.head, at, sum);
+      else *reinterpret_cast<f32x4*>(part_o(p, w.split, part_row(p, w.b, w.start, rb.node), rb.head) + at) = sum;
+    }
+  }
+  if (wave == 0 && hi == 0) {
+    if (!whole) {
+      float* ml = part_ml(p, w.split, part_row(p, w.b, w.start, rb.node), rb.head);
+      ml[0] = M;
+      ml[1] = L;
+    } else if (p.lse) {
+      p.lse[rb.row * p.hq + rb.head] = (M + __builtin_amdgcn_logf(L)) * kLn2;
+    }
+  }
+}
+
+// ---- more rows --------------------------------------------------------------
+
+// The bytes of a stage of KT keys and values on their way from memory through a
+// thread's registers to bf16 tiles in LDS: piece q of the stage's 2 * KT * DP / 16
+// belongs to thread q % THREADS.  A thread's pieces are of one row of the keys
+// (and, where a stage has more pieces than threads, of the same row of the values
+// or of rows a fixed step further).
+template <typename F, int DP, int KT, int THREADS> struct Staging {
+  using R = Rows<bf16_t, DP>;
+  static constexpr int kPieces = DP / 16;               // of a row of bytes
+  static constexpr int kOf = KT * kPieces;              // of the keys, and of the values
+  static constexpr int NP = 2 * kOf / THREADS;          // pieces of a thread
+  static constexpr int NR = kOf < THREADS ? 1 : kOf / THREADS;  // rows it has to find
+  static_assert(NP >= 1 && NP * THREADS == 2 * kOf && THREADS % kPieces == 0, "");
+  u32x4 data[NP];
+  int8_t exps[NP];
+  int id[NR];
+
+  __device__ __forceinline__ static int row(int i) { return ((int)threadIdx.x + i * THREADS) % kOf / kPieces; }
+  __device__ __forceinline__ static int piece() { return (int)threadIdx.x % kPieces; }
+  __device__ __forceinline__ static bool is_v(int i) { return (int)threadIdx.x + i * THREADS >= kOf; }
+
+  // The page numbers of the stage whose first key is k0.
+  __device__ __forceinline__ void ask(const AttendQuantizedParams& p, const Work& w, int64_t k0) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      int col;
+      const PageAt a = page_at(p, k0 + row(i), w.k1, col);
+      id[i] = *(global_int*)(entry_of(p, w.b, a, col));
+    }
+  }
+  // The stage's bytes and exponents; its rows that are keys are marked in ok [KT].
+  __device__ __forceinline__ void load(const AttendQuantizedParams& p, const Work& w, int64_t k0, uint8_t* ok) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      int col;
+      const PageAt a = page_at(p, k0 + row(i), w.k1, col);
+      const uint32_t of = (uint32_t)id[i % NR];
+      const bool valid = a.in_table && of < (uint64_t)p.cache.n_pages && (int)of >= 0;
+      const bool v = is_v(i);
+      const HeadAt h = head_at<uint8_t>(p, w.h, v);
+      const ExpAt e = exp_at(p, w.h, v);
+      data[i] = ld16_or0(reinterpret_cast<const char*>(h.row_at(of, a.place)) + 16 * piece(), valid && 16 * piece() < p.d);
+      exps[i] = *(global_int8*)(valid ? reinterpret_cast<const char*>(e.at(of, p.block.div((uint32_t)a.place)))
+                                      : reinterpret_cast<const char*>(g_zero_row));
+      if (!v && piece() == 0) ok[row(i)] = valid;
+    }
+  }
+  // As bf16 to the tiles: keys at `to`, values behind them.
+  __device__ __forceinline__ void store(char* to) const {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int r = row(i);
+      const float scale = power_of_two(exponent_of<F>(exps[i]));
+      char* at = to + (is_v(i) ? KT * R::kBytes : 0) + r * R::kBytes;
+      const uint32_t w0 = data[i][0], w1 = data[i][1], w2 = data[i][2], w3 = data[i][3];
+      const u32x4 x[2] = {to_bf16<F>(w0, w1, scale), to_bf16<F>(w2, w3, scale)};
+      // odd rows begin with their second piece: two rows of a write then lie in different banks
+      const bool odd = r & 1;
+      const int c = 2 * piece(), s = R::swz(r);
+      *reinterpret_cast<u32x4*>(at + (((c + (odd ? 1 : 0)) ^ s) << 4)) = odd ? x[1] : x[0];
+      *reinterpret_cast<u32x4*>(at + (((c + (odd ? 0 : 1)) ^ s) << 4)) = odd ? x[0] : x[1];
+    }
+  }
+};
+
+// Heads up to 128 elements (fp32: 64): eight waves in two groups of four that take
+// turns on the matrix cores and the vector unit, over a ring of four stages of 64
+// keys, as the kernel for 16-bit caches does; here a stage's bytes pass through
+// registers, are converted once for all waves, and lie in LDS as bf16.  In step t
+// stage t + 2, loaded in step t - 1, is converted into the place that stage t - 2
+// left, and stage t + 3 is loaded.
+template <typename Out, typename F, int DP, int KG>
+__global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQuantizedParams p) {
+  constexpr int NT = kTerms<Out>;
+  using R = Rows<bf16_t, DP>;
+  using Block = RowBlock<bf16_t, DP, Out, NT>;
+  constexpr int KT = 64, NS = 2 / KG, kRing = 4;
+  constexpr int kTile = KT * R::kBytes, kStage = 2 * kTile;
+  // (aligned to its size, so that an XOR changes stages)
+  __shared__ __attribute__((aligned(kRing * kStage))) char s_kv[kRing][kStage];
+  __shared__ uint8_t s_ok[8][KT];
+  warm_args(p);
+  const Work w = work_of<32 * 8 / KG, false>(p);
+  if (w.none) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int late = wave >> 2;  // the group that runs behind
+  const int block = KG == 1 ? wave : wave & 3, part = KG == 1 ? 0 : late;
+  Block rb;
+  rb.init(p, w, w.row0 + block * kBlock);
+  const bool idle = w.row0 + block * kBlock >= w.rows;  // a wave without rows only fetches
+  const int lane = rb.lane;
+  const float c = p.scale == 0.f ? 1.0f : fabsf(p.scale) * kLog2e;
+  const int keys = w.k1 - w.k0, inside = min(w.ctx, w.k1) - w.k0;
+  const int nt = keys > 0 ? (keys + KT - 1) / KT : 0, nf = inside > 0 ? inside / KT : 0;
+  Staging<F, DP, KT, 512> stage;
+  const auto first_key = [&](int t) { return (int64_t)w.k0 + (int64_t)t * KT; };
+
+  f32x16 s[NS];
+  typename Block::Weights weights[NS];
+  uint32_t seen[NS];
+  bool odd = false;
+  uint32_t keys_in = 0, values_in = 0;  // ring places that the operand addresses are at
+  auto multiply = [&](int t, bool values, bool scores, auto tail) __attribute__((always_inline)) {
+    if (idle) return;
+    if (values) {
+      const uint32_t at = (uint32_t)(t - 1) % kRing;
+      rb.move_values((values_in ^ at) * kStage);
+      values_in = at;
+      if (decltype(tail)::value && odd) {
+        const char* vb = s_kv[at] + kTile + part * kBlock * R::kBytes;
+        rb.template add_values<decltype(tail)::value, 0>(weights[0]);
+        rb.add_odd(vb, seen[0]);
+        if constexpr (NS == 2) {
+          rb.template add_values<decltype(tail)::value, kBlock>(weights[1]);
+          rb.add_odd(vb + kBlock * R::kBytes, seen[1]);
+        }
+      } else {
+        rb.template add_values<false, 0>(weights[0]);
+        if constexpr (NS == 2) rb.template add_values<false, kBlock>(weights[1]);
+      }
+    }
+    if (scores) {
+      const uint32_t at = (uint32_t)t % kRing;
+      rb.move_keys((keys_in ^ at) * kStage);
+      keys_in = at;
+      s[0] = rb.template scores<0>();
+      if constexpr (NS == 2) s[1] = rb.template scores<kBlock>();
+    }
+  };
+  auto soften = [&](int t, auto tail) __attribute__((always_inline)) {
+    if (idle) return;
+    const uint64_t all = __ballot(s_ok[t & 7][lane] != 0);
+    bool uneven = false;
+#pragma unroll
+    for (int b = 0; b < NS; ++b) {
+      const uint32_t valid = (uint32_t)(all >> (32 * (part + b)));
+      seen[b] = valid;
+      if constexpr (decltype(tail)::value) {
+        seen[b] &= rb.sees(p, w, (int)first_key(t) + (part + b) * kBlock);
+        uneven |= __any(seen[b] != valid);
+        if (__any(seen[b] != ~0u)) rb.mask_scores(s[b], seen[b]);
+      } else if (valid != ~0u) {
+        rb.mask_scores(s[b], valid);
+      }
+    }
+    rb.weigh(s, c);
+#pragma unroll
+    for (int b = 0; b < NS; ++b) weights[b] = rb.pack(s[b]);
+    if constexpr (decltype(tail)::value && F::kHasNan)
+      odd = uneven && rb.any_odd(s_kv[t % kRing] + kTile + part * kBlock * R::kBytes, NS * kBlock);
+  };
+  auto step = [&](int t, auto tail) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_setprio(1);
+    multiply(t, t > 0, true, tail);
+    __builtin_amdgcn_s_setprio(0);
+    lds_barrier();
+    if (t + 2 < nt) {
+      stage.store(s_kv[(t + 2) % kRing]);
+      if (t + 3 < nt) {
+        stage.load(p, w, first_key(t + 3), s_ok[(t + 3) & 7]);
+        stage.ask(p, w, first_key(t + 4));
+      }
+    }
+    soften(t, tail);
+    lds_barrier();
+  };
+
+  if (nt > 0) {
+    stage.ask(p, w, first_key(0));
+#pragma unroll 1
+    for (int t = 0; t < 3; ++t) {
+      if (t > 0) stage.store(s_kv[t - 1]);
+      stage.load(p, w, first_key(t), s_ok[t]);
+      stage.ask(p, w, first_key(t + 1));
+    }
+    rb.place((uint32_t)(uintptr_t)s_kv[0] + part * kBlock * R::kBytes,
+             (uint32_t)(uintptr_t)s_kv[0] + kTile + part * kBlock * R::kBytes);
+    lds_barrier();
+    if (late) lds_barrier();
+    int t = 0;
+    for (; t < nf; ++t) step(t, No{});
+    for (; t < nt; ++t) step(t, Yes{});
+    multiply(nt, true, false, Yes{});
+    if (!late) lds_barrier();
+  }
+
+  constexpr int kOut = (R::kDB * 4 + 1) * 1024;  // a block's outputs, maxima and sums in LDS
+  static_assert((KG == 1 ? 8 * kStoreBytes<DP> : 4 * kOut) <= kRing * kStage && kStoreBytes<DP> <= kOut, "");
+  float l = half_sum(rb.l);
+  if constexpr (KG == 2) {
+    // the second group's outputs pass through LDS
+    __syncthreads();
+    f32x4* red = reinterpret_cast<f32x4*>(&s_kv[0][0] + block * kOut);
+    if (late) {
+#pragma unroll
+      for (int db = 0; db < R::kDB; ++db)
+#pragma unroll
+        for (int qd = 0; qd < 4; ++qd)
+          red[(db * 4 + qd) * 64 + lane] =
+              f32x4{rb.o[db][4 * qd], rb.o[db][4 * qd + 1], rb.o[db][4 * qd + 2], rb.o[db][4 * qd + 3]};
+      red[R::kDB * 4 * 64 + lane] = f32x4{rb.m, l, 0.f, 0.f};
+    }
+    __syncthreads();
+    if (late) return;
+    const f32x4 ml = red[R::kDB * 4 * 64 + lane];
+    const float M = fmaxf(rb.m, ml[0]), ms = M == -INFINITY ? 0.f : M;
+    const float f = __builtin_amdgcn_exp2f(rb.m - ms), g = __builtin_amdgcn_exp2f(ml[0] - ms);
+    l = l * f + ml[1] * g;
+    rb.m = M;
+#pragma unroll
+    for (int db = 0; db < R::kDB; ++db)
+#pragma unroll
+      for (int qd = 0; qd < 4; ++qd) {
+        const f32x4 x = red[(db * 4 + qd) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rb.o[db][4 * qd + e] = rb.o[db][4 * qd + e] * f + x[e] * g;
+      }
+  }
+  if constexpr (KG == 1) __syncthreads();
+  store_rows<DP>(p, w, rb, l, w.row0 + block * kBlock, &s_kv[0][0] + block * (KG == 1 ? kStoreBytes<DP> : kOut));
+}
+
+// The heads that leave the kernel above no registers: four waves of 32 rows share
+// stages of 32 keys, double buffered.  A stage's bytes are in registers during the
+// stage before it and converted into the other place at its end.
+template <typename Out, typename F, int DP>
+__global__ __launch_bounds__(kThreads, 1) void attend_wide_quantized_kernel(AttendQuantizedParams p) {
+  constexpr int NT = kTerms<Out>;
+  using R = Rows<bf16_t, DP>;
+  constexpr int KT = kBlock;
+  constexpr int kTile = KT * R::kBytes;
+  constexpr int kLds = kTile < kStoreBytes<DP> ? 4 * kStoreBytes<DP> : 4 * kTile;
+  // (aligned to its two stages, so that an XOR changes them)
+  __shared__ __attribute__((aligned(4 * kTile))) char s_kv[kLds];
+  const auto place = [&](int t) { return s_kv + (t & 1) * 2 * kTile; };
+  __shared__ uint8_t s_ok[4][KT];
+  warm_args(p);
+  const Work w = work_of<4 * kBlock, true>(p);
+  if (w.none) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowBlock<bf16_t, DP, Out, NT> rb;
+  rb.init(p, w, w.row0 + wave * kBlock);
+  const bool idle = w.row0 + wave * kBlock >= w.rows;  // a wave without rows only fetches
+  const float c = p.scale == 0.f ? 1.0f : fabsf(p.scale) * kLog2e;
+  const int keys = w.k1 - w.k0, inside = min(w.ctx, w.k1) - w.k0;
+  const int nt = keys > 0 ? (keys + KT - 1) / KT : 0, nf = inside > 0 ? inside / KT : 0;
+  Staging<F, DP, KT, kThreads> stage;
+  const auto first_key = [&](int t) { return (int64_t)w.k0 + (int64_t)t * KT; };
+  if (nt > 0) {
+    stage.ask(p, w, first_key(0));
+    stage.load(p, w, first_key(0), s_ok[0]);
+    stage.ask(p, w, first_key(1));
+    stage.store(place(0));
+    stage.load(p, w, first_key(1), s_ok[1]);
+    stage.ask(p, w, first_key(2));
+  }
+  auto tile = [&](int t, auto tail) __attribute__((always_inline)) {
+    constexpr bool kTail = decltype(tail)::value;
+    lds_barrier();  // everyone's part of stage t is there, and everyone is done with stage t - 1
+    if (t + 1 < nt) {
+      stage.store(place(t + 1));
+      if (t + 2 < nt) {
+        stage.load(p, w, first_key(t + 2), s_ok[(t + 2) & 3]);
+        stage.ask(p, w, first_key(t + 3));
+      }
+    }
+    if (!idle) {
+      f32x16 s[1] = {rb.template scores<0>()};
+      const uint32_t valid = (uint32_t)__ballot(s_ok[t & 3][rb.r32] != 0);
+      uint32_t seen = valid;
+      bool uneven = false;
+      if constexpr (kTail) {
+        seen &= rb.sees(p, w, (int)first_key(t));
+        uneven = __any(seen != valid);
+      }
+      if (__any(seen != ~0u)) rb.mask_scores(s[0], seen);
+      rb.weigh(s, c);
+      const char* vb = place(t) + kTile;
+      if (kTail && F::kHasNan && uneven && rb.any_odd(vb, KT)) {
+        rb.template add_values<kTail, 0>(rb.pack(s[0]));
+        rb.add_odd(vb, seen);
+      } else {
+        rb.template add_values<false, 0>(rb.pack(s[0]));
+      }
+    }
+    rb.move_keys(2 * kTile);
+    rb.move_values(2 * kTile);
+  };
+  rb.place((uint32_t)(uintptr_t)s_kv, (uint32_t)(uintptr_t)s_kv + kTile);
+  int t = 0;
+  for (; t < nf; ++t) tile(t, No{});
+  for (; t < nt; ++t) tile(t, Yes{});
+
+  __syncthreads();
+  store_rows<DP>(p, w, rb, half_sum(rb.l), w.row0 + wave * kBlock, s_kv + wave * kStoreBytes<DP>);
+}
+
+// ---- host -------------------------------------------------------------------
+
+// Which kernel takes a call, by the rows of a (sequence, key/value head): up to 32
+// the narrow one; else the one whose waves take turns, or the wide one where a
+// head (fp32: more than 64 elements, else more than 128) leaves it no registers.
+enum class Kind { kNarrow, kTurns128, kTurns256, kWide };
+struct Plan {
+  Kind kind;
+  int32_t chunk, splits, row_tiles;
+  int32_t block;   // threads of a workgroup
+  int64_t groups;  // workgroups to be had from cutting the keys
+  int64_t unit;    // keys that a chunk is a multiple of
+  int64_t grid;
+};
+int padded(int32_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+Plan plan_kind(bool fp32, int32_t nodes, int32_t group, int32_t d) {
+  Plan a{};
+  const int64_t rows = (int64_t)nodes * group;
+  const int dp = padded(d);
+  int64_t tile = kBlock;
+  a.groups = 1024;
+  a.kind = Kind::kNarrow;
+  a.block = kThreads;
+  a.unit = 4 * 8192 / dp;
+  if (rows > kBlock) {
+    a.kind = dp > (fp32 ? 64 : 128) ? Kind::kWide : rows > 4 * kBlock ? Kind::kTurns256 : Kind::kTurns128;
+    tile = a.kind == Kind::kTurns256 ? 8 * kBlock : 4 * kBlock;
+    a.groups = a.kind == Kind::kWide ? 512 : 256;
+    a.block = a.kind == Kind::kWide ? kThreads : 512;
+    a.unit = 64;
+  }
+  a.row_tiles = (int32_t)ceil_div(rows, tile);
+  return a;
+}
+
+// How the keys are cut: even chunks, so long that about `groups` workgroups run in
+// all where every sequence is as long as its bound, and no shorter than kMinChunk.
+constexpr int64_t kMinChunk = 256;
+constexpr int64_t kMaxChunk = (int64_t)1 << 30;
+
+Plan plan_of(bool fp32, int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk, int32_t d) {
+  Plan a = plan_kind(fp32, max_nodes, hq / hk, d);
+  const int64_t keys = (int64_t)max_context + max_nodes;
+  const int64_t units = (int64_t)B * hk * a.row_tiles;
+  int64_t chunk = units < a.groups ? ceil_div(keys * units, a.groups) : keys;
+  if (chunk < kMinChunk) chunk = kMinChunk;
+  chunk = ceil_div(ceil_div(keys, ceil_div(keys, chunk)), a.unit) * a.unit;
+  if (chunk > kMaxChunk) chunk = kMaxChunk;
+  a.chunk = (int32_t)chunk;
+  a.splits = (int32_t)ceil_div(keys, chunk);
+  a.grid = ceil_div((int64_t)B * hk * a.splits, kXcds) * kXcds * a.row_tiles;
+  return a;
+}
+
+int64_t join_grid(int32_t max_nodes, int32_t hq) { return ceil_div((int64_t)max_nodes * hq, kThreads / 64); }
+int32_t part_rows_of(int32_t B, int32_t T, int32_t max_nodes) {
+  return (int32_t)std::min<int64_t>(T, (int64_t)B * max_nodes);
+}
+int64_t part_bytes(int64_t rows, int32_t hq, int32_t d) { return (rows * hq * (d + 2) * 4 + 255) & ~int64_t(255); }
+
+template <typename Out, typename F, int DP>
+hipError_t launch_d(const AttendQuantizedParams& p, const Plan& a, hipStream_t stream) {
+  const dim3 g((unsigned)a.grid), b((unsigned)a.block);
+  if (a.kind == Kind::kNarrow) {
+    hipLaunchKernelGGL((attend_narrow_quantized_kernel<Out, F, DP>), g, b, 0, stream, p);
+  } else if constexpr (DP > (sizeof(Out) == 4 ? 64 : 128)) {
+    hipLaunchKernelGGL((attend_wide_quantized_kernel<Out, F, DP>), g, b, 0, stream, p);
+  } else if (a.kind == Kind::kTurns256) {
+    hipLaunchKernelGGL((attend_turns_quantized_kernel<Out, F, DP, 1>), g, b, 0, stream, p);
+  } else {
+    hipLaunchKernelGGL((attend_turns_quantized_kernel<Out, F, DP, 2>), g, b, 0, stream, p);
+  }
+  return hipGetLastError();
+}
+
+template <typename Out, typename F>
+hipError_t launch(AttendQuantizedParams p, hipStream_t stream) {
+  const Plan a = plan_of(sizeof(Out) == 4, p.B, p.max_nodes, p.max_context, p.hq, p.hk, p.d);
+  p.chunk = a.chunk;
+  p.splits = a.splits;
+  p.row_tiles = a.row_tiles;
+  p.part_rows = part_rows_of(p.B, p.T, p.max_nodes);
+  p.by_tiles = fast_div((uint32_t)a.row_tiles);
+  p.by_splits = fast_div((uint32_t)a.splits);
+  p.by_sequences = fast_div((uint32_t)p.B);
+  p.by_heads = fast_div((uint32_t)p.hk);
+  p.by_chunk = fast_div((uint32_t)a.chunk);
+  const int dp = padded(p.d);
+  const hipError_t e = dp == 64    ? launch_d<Out, F, 64>(p, a, stream)
+                       : dp == 128 ? launch_d<Out, F, 128>(p, a, stream)
+                                   : launch_d<Out, F, 256>(p, a, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL(attend_join_kernel<Out>, dim3((unsigned)join_grid(p.max_nodes, p.hq), (unsigned)p.B), dim3(kThreads), 0,
+                     stream, static_cast<const AttendParams&>(p));
   return hipGetLastError();
 }
 
 }  // namespace
 
-bool attend_quantized_fits(lora_dtype, int32_t, int32_t max_nodes, int32_t, int32_t hq, int32_t, int32_t) {
-  return grid_of(max_nodes, hq) <= (((int64_t)1 << 32) - 1) / kThreads;
+bool attend_quantized_fits(lora_dtype dt, int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
+                           int32_t d) {
+  const Plan a = plan_of(dt == LORA_F32, B, max_nodes, max_context, hq, hk, d);
+  const int64_t most = ((int64_t)1 << 32) - 1;  // threads in a dimension of a grid
+  return a.grid <= most / a.block && (a.splits == 1 || join_grid(max_nodes, hq) <= most / kThreads);
 }
-int64_t attend_quantized_need_bytes(lora_dtype, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t) {
-  return 0;
-}
-int64_t attend_quantized_most_bytes(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
 
-hipError_t launch_attend_quantized(lora_dtype dt, int format, const AttendQuantizedParams& p, hipStream_t stream) {
+int64_t attend_quantized_need_bytes(lora_dtype dt, int32_t B, int32_t T, int32_t max_nodes, int32_t max_context,
+                                    int32_t hq, int32_t hk, int32_t d) {
+  const int64_t splits = plan_of(dt == LORA_F32, B, max_nodes, max_context, hq, hk, d).splits;
+  return splits == 1 ? 0 : part_bytes(splits * part_rows_of(B, T, max_nodes), hq, d);
+}
+
+// Fewer sequences or nodes are cut into more chunks, so the bytes of a call do not
+// grow with its sizes; these are the most of any call up to them.  With G workgroups
+// to be had and u = sequences * kv_heads * row tiles a call has at most ceil(keys /
+// kMinChunk) and ceil(G / u) chunks (2^30 keys at most a chunk), both largest at the
+// most keys; rows only grow.  What is left is to try the numbers of sequences and,
+// of the nodes, those that fill their row tiles.
+int64_t attend_quantized_most_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
+                                    int32_t d) {
+  const int32_t group = hq / hk;
+  const int64_t keys = (int64_t)max_context + max_nodes, by_keys = ceil_div(keys, kMinChunk);
+  const int64_t uncut = ceil_div(keys, kMaxChunk);
+  int64_t most = uncut > 1 ? uncut * part_rows_of(B, T, max_nodes) : 0;
+  const auto nodes_up_to = [&](bool fp32, int64_t nodes) {
+    if (nodes < 1) return;
+    nodes = std::min<int64_t>(nodes, max_nodes);
+    const Plan a = plan_kind(fp32, (int32_t)nodes, group, d);
+    const int64_t per = (int64_t)hk * a.row_tiles;
+    for (int64_t b = 1; b <= B && b * per < a.groups; ++b) {
+      const int64_t splits = std::max(std::min(by_keys, ceil_div(a.groups, b * per)), uncut);
+      if (splits > 1) most = std::max(most, splits * part_rows_of((int32_t)b, T, (int32_t)nodes));
+    }
+  };
+  for (const bool fp32 : {false, true}) {
+    nodes_up_to(fp32, kBlock / group);
+    for (int64_t tiles = 1; tiles * hk < 512; ++tiles) {
+      nodes_up_to(fp32, tiles * 4 * kBlock / group);
+      nodes_up_to(fp32, tiles * 8 * kBlock / group);
+      if (tiles * 4 * kBlock / group >= max_nodes) break;
+    }
+    nodes_up_to(fp32, max_nodes);
+  }
+  return part_bytes(most, hq, d);
+}
+
+template <typename Out> static hipError_t launch_format(int format, const AttendQuantizedParams& p, hipStream_t stream) {
+  return format == LORA_CACHE_E4M3 ? launch<Out, E4m3>(p, stream) : launch<Out, Int8>(p, stream);
+}
+
+hipError_t launch_attend_quantized(lora_dtype dt, int format, AttendQuantizedParams p, hipStream_t stream) {
   switch (dt) {
-    case LORA_F32: return launch<float>(format, p, stream);
-    case LORA_F16: return launch<half_t>(format, p, stream);
-    case LORA_BF16: return launch<bf16_t>(format, p, stream);
+    case LORA_F32: return launch_format<float>(format, p, stream);
+    case LORA_F16: return launch_format<half_t>(format, p, stream);
+    case LORA_BF16: return launch_format<bf16_t>(format, p, stream);
   }
   return hipErrorInvalidValue;
 }

@@ -12,7 +12,8 @@ constexpr int kExpLow = -126;  // the smallest exponent of a block
 
 // What a byte holds.
 struct E4m3 {
-  static constexpr int kTop = 119;         // the largest exponent
+  static constexpr bool kHasNan = true;
+  static constexpr int kTop = 119;          // the largest exponent
   static constexpr float kLargest = 448.f;  // the largest number, 1.75 * 2^8
   static constexpr int kLargestExp = 8;
   static constexpr uint32_t kLargestMantissa = 0x600000u;
@@ -34,6 +35,7 @@ struct E4m3 {
   }
 };
 struct Int8 {
+  static constexpr bool kHasNan = false;
   static constexpr int kTop = 121;
   static constexpr float kLargest = 127.f;  // 1.984375 * 2^6
   static constexpr int kLargestExp = 6;
@@ -89,18 +91,11 @@ struct KeepQuantizedParams {
   int8_t *k_exp[kKeepLayers], *v_exp[kKeepLayers];
 };
 
-struct AttendQuantizedParams {
-  const void* q;
-  void* out;
-  int64_t ldq, ldo;
-  float* lse;  // nullable
-  QuantizedView cache;
-  const int32_t *page_table, *context, *q_start;
-  const uint64_t* mask;  // nullable: a chain
-  int64_t ld_table;
-  float scale;
-  int32_t T, B, hq, hk, d, n_table, max_nodes, max_context, mask_words;
-  FastDiv group;  // by q_heads / kv_heads
+// The attention's parameters, with the cache's strides in bytes.
+struct AttendQuantizedParams : AttendParams {
+  const int8_t *k_exp, *v_exp;
+  int64_t k_exp_page, k_exp_head, v_exp_page, v_exp_head;
+  FastDiv block;  // by the rows of a block
 };
 
 struct PoolParams {
@@ -132,7 +127,7 @@ bool store_quantized_fits(int32_t T);
 hipError_t launch_store_quantized(lora_dtype dt, int format, StoreParams p, hipStream_t stream);
 hipError_t launch_keep_quantized(int format, const KeepQuantizedParams& p, int32_t n_layers, int32_t B,
                                  hipStream_t stream);
-hipError_t launch_attend_quantized(lora_dtype dt, int format, const AttendQuantizedParams& p, hipStream_t stream);
+hipError_t launch_attend_quantized(lora_dtype dt, int format, AttendQuantizedParams p, hipStream_t stream);
 bool attend_quantized_fits(lora_dtype dt, int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
                            int32_t d);
 int64_t attend_quantized_need_bytes(lora_dtype dt, int32_t B, int32_t T, int32_t max_nodes, int32_t max_context,

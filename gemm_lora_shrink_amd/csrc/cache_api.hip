@@ -218,7 +218,15 @@ LORA_EXPORT lora_status lora_tree_attention_quantized(lora_dtype dt, const void*
   p.ldq = ldq;
   p.ldo = ldo;
   p.lse = lse;
-  p.cache = view_of(*cache);
+  p.cache = CacheView{cache->k,      cache->v,     cache->k_page, cache->k_head, cache->k_row,
+                      cache->v_page, cache->v_head, cache->v_row, cache->n_pages, fast_div((uint32_t)cache->page_size)};
+  p.k_exp = cache->k_exp;
+  p.v_exp = cache->v_exp;
+  p.k_exp_page = cache->k_exp_page;
+  p.k_exp_head = cache->k_exp_head;
+  p.v_exp_page = cache->v_exp_page;
+  p.v_exp_head = cache->v_exp_head;
+  p.block = fast_div((uint32_t)cache->block);
   p.page_table = page_table;
   p.context = context;
   p.q_start = q_start;
@@ -235,6 +243,7 @@ LORA_EXPORT lora_status lora_tree_attention_quantized(lora_dtype dt, const void*
   p.max_context = max_context;
   p.mask_words = mask_words;
   p.group = fast_div((uint32_t)(q_heads / kv_heads));
+  p.part = static_cast<float*>(workspace);
   const hipError_t e = launch_attend_quantized(dt, cache->format, p, stream);
   if (e != hipSuccess) return hip_fail(e, "quantized tree attention launch");
   return LORA_OK;

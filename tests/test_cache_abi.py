@@ -106,6 +106,16 @@ def test_attention_of_nothing():
     assert _attend(B=0, q=None, out=None) == OK
 
 
+def test_attention_refuses_workspaces():
+    sizes = dict(B=1, T=1, hq=32, hk=8, d=128, nodes=1, ctx=100000, ldq=4096, ldo=4096, n_table=12501, ld=12501)
+    most = glsa.quantized_workspace_bytes(1, 1, 1, 100000, 32, 8, 128)
+    assert most > 0
+    cache = _cache(k_head=1024, k_row=128, v_head=1024, v_row=128, k_page=8192, v_page=8192)
+    assert _attend(cache, **sizes, ws=None) == BAD
+    assert _attend(cache, **sizes, ws=FAKE + 128) == BAD
+    assert _attend(cache, **sizes, ws_bytes=256) == BAD
+
+
 def test_workspace_bytes_grow_with_their_sizes():
     """One for the largest call suffices for every smaller one: what any smaller call asks for is no more."""
     for hq, hk, d in ((32, 8, 128), (8, 8, 64), (16, 1, 256)):
