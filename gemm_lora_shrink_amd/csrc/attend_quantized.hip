@@ -18,10 +18,7 @@ namespace {
 
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
-typedef __attribute__((address_space(3))) u32x4 lds_u32x4_rw;
 typedef __attribute__((address_space(3))) const int lds_int;
-typedef __attribute__((address_space(3))) const f32x4 lds_f32x4;
-typedef __attribute__((address_space(3))) float lds_float_rw;
 typedef __attribute__((address_space(1))) const int8_t global_int8;
 typedef __attribute__((address_space(1))) const int32_t global_int;
 
@@ -42,6 +39,16 @@ template <> __device__ __forceinline__ u32x4 to_bf16<Int8>(uint32_t w0, uint32_t
   for (int i = 0; i < 4; ++i) r[i] = pack2_bf16(x[2 * i] * scale, x[2 * i + 1] * scale);
   return r;
 }
+// Eight bytes' numbers as fp16 ones.
+template <typename F> __device__ __forceinline__ u32x4 to_f16(uint32_t w0, uint32_t w1) {
+  float x[8];
+  F::numbers(w0, x);
+  F::numbers(w1, x + 4);
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = pack2_f16(x[2 * i], x[2 * i + 1]);
+  return r;
+}
 // Bit 7 of each byte that is a NaN.
 template <typename F> __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return F::kHasNan ? ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : 0u;
@@ -49,6 +56,16 @@ template <typename F> __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) 
 
 // How many bf16 numbers a number of the call's type enters as.
 template <typename Out> constexpr int kTerms = sizeof(Out) == 4 ? 3 : Traits<Out>::kDtype == LORA_F16 ? 2 : 1;
+// The kernels of many rows, which the matrix cores bound, have fp16 tiles for an fp16
+// q, which then enters as it is, and so do its weights.
+template <typename Out> struct Tiles {
+  using Elem = bf16_t;
+  static constexpr int NT = kTerms<Out>;
+};
+template <> struct Tiles<half_t> {
+  using Elem = half_t;
+  static constexpr int NT = 1;
+};
 
 // A byte to a dword of LDS for each lane.
 __device__ inline void byte_to_lds(const char* g, uint32_t lds) {
@@ -78,15 +95,18 @@ __device__ inline ExpAt exp_at(const AttendQuantizedParams& p, int h, bool is_v)
 
 // ---- up to 32 rows ----------------------------------------------------------
 
-// A tile of a wave: 8 KB of keys and 8 KB of values, rows of DP bytes in pieces of
-// 16, piece c of row r at c ^ swz(r): 16 consecutive rows at one piece (the keys'
+// A tile of a wave: 4 KB of keys and 4 KB of values (rows of 256 bytes: 8 and 8, as a
+// matrix block has 32 keys), rows of DP bytes in pieces of 16, piece c of row r at
+// c ^ swz(r): 16 consecutive rows at one piece (the keys'
 // reads) and rows 4 i .. 4 i + 3 and 4 i + 8 .. 4 i + 11 at two neighbouring
 // pieces (the values' transposing reads) lie in different banks.
 template <int DP> struct Tile8 {
-  static constexpr int kKeys = 8192 / DP, kBlocks = kKeys / kBlock;
+  static constexpr int kBytes = DP == 256 ? 8192 : 4096;
+  static constexpr int kKeys = kBytes / DP, kBlocks = kKeys / kBlock;
   static constexpr int kPieces = DP / 16;
   static constexpr int kPerLoad = 1024 / DP;  // rows of one 64-lane load
-  static constexpr int NL = 8;                // loads of the keys or values
+  static constexpr int NL = kBytes / 1024;    // loads of the keys or values
+  static constexpr int kGroups = DP == 256 ? 1 : 2;  // workgroups of a compute unit
   static constexpr int NI = (kKeys + 63) / 64;    // loads of page numbers
   static constexpr int NE = kKeys / 32;           // loads of exponents, keys and values
   __device__ static inline int swz(int r) {
@@ -96,20 +116,28 @@ template <int DP> struct Tile8 {
   }
 };
 
-// Up to 32 rows: four waves hold the same rows and take the chunk's tiles of 8 KB
-// of keys in turn, each through LDS of its own: a wave waits for no other until
-// their outputs meet at the end.  Two tiles are in flight a wave (32 KB): after a
-// tile's scores the keys of the tile after the next take its keys' place, after
-// its products with the values their values.  Page numbers come four tiles ahead.
-// Loads past the chunk's end go to a row of zeros, so that the number of loads in
-// flight is the same in every turn.
+// Up to 32 rows: four waves hold the same rows and take the chunk's tiles in turn,
+// each through LDS of its own: a wave waits for no other until their outputs meet
+// at the end.  Two tiles are in flight a wave (16 KB): after a tile's scores the keys
+// of the tile after the next take its keys' place, after its products with the
+// values their values.  Page numbers come four tiles ahead.  Loads past the chunk's
+// end go to a row of zeros, so that the number of loads in flight is the same in
+// every turn.
+// Bound by memory: 256 sequences of 128 to 4096 keys, 32 + 8 bf16 heads of 128, e4m3
+// (1.1 GB): 197 us, 5.5 TB/s; 64 sequences of 4096 (0.54 GB): 92 us, 5.9 TB/s.  Two
+// workgroups a compute unit, one of which is at its first loads while the other
+// reads (260 us on the first with one of twice the tiles, 300 with one of these).
 template <typename Out, typename F, int DP>
-__global__ __launch_bounds__(256, 1) void attend_narrow_quantized_kernel(AttendQuantizedParams p) {
+__global__ __launch_bounds__(256, Tile8<DP>::kGroups) void attend_narrow_quantized_kernel(AttendQuantizedParams p) {
   using L8 = Tile8<DP>;
   constexpr int NT = kTerms<Out>, NW = 4, KT = L8::kKeys, NB = L8::kBlocks, NL = L8::NL, NI = L8::NI, NE = L8::NE;
   using Block = RowBlock<bf16_t, DP, Out, NT>;
   constexpr int kDB = DP / kBlock;
-  __shared__ __attribute__((aligned(1024))) char s_kv[NW][2][2][8192];
+  // Whether the keys' powers of two are taken to the scores: the conversion of a byte
+  // takes one for e4m3, for int8 it costs a product an element (226 us for 213 on 256
+  // sequences of 128 to 4096 keys).
+  constexpr bool kScores = !F::kHasNan;
+  __shared__ __attribute__((aligned(1024))) char s_kv[NW][2][2][L8::kBytes];
   __shared__ __attribute__((aligned(16))) const char* s_row[NW][2 * KT];
   __shared__ __attribute__((aligned(16))) int s_exp[NW][2][2 * KT < 64 ? 64 : 2 * KT];
   __shared__ int s_id[NW][4][NI * 64];
@@ -219,7 +247,8 @@ __global__ __launch_bounds__(256, 1) void attend_narrow_quantized_kernel(AttendQ
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int key = 32 * b + r32;
-      const float ks = power_of_two(exponent_of<F>((int8_t)*(lds_int*)(lds_byte*)(uintptr_t)(exp_lds + 4 * key)));
+      const float ks =
+          kScores ? 1.0f : power_of_two(exponent_of<F>((int8_t)*(lds_int*)(lds_byte*)(uintptr_t)(exp_lds + 4 * key)));
       u32x4 raw[DP / 32];
 #pragma unroll
       for (int j = 0; j < DP / 32; ++j)
@@ -237,17 +266,24 @@ __global__ __launch_bounds__(256, 1) void attend_narrow_quantized_kernel(AttendQ
         }
       }
     }
-    // the values' exponents become factors
-    if constexpr (KT >= 64) {
+    // the exponents (bf16 keys: the values') become factors
 #pragma unroll
-      for (int i = 0; i < KT / 64; ++i) {
-        int* e = &s_exp[wave][t & 1][KT + 64 * i + lane];
-        *reinterpret_cast<float*>(e) = power_of_two(exponent_of<F>((int8_t)*e));
-      }
-    } else if (hi) {
-      int* e = &s_exp[wave][t & 1][lane];
-      *reinterpret_cast<float*>(e) = power_of_two(exponent_of<F>((int8_t)*e));
+    for (int i = 0; i < (KT >= 64 ? 2 * KT / 64 : 1); ++i) {
+      if (!kScores && KT >= 64 && i < KT / 64) continue;
+      int* e = &s_exp[wave][t & 1][64 * i + lane];
+      if (kScores || KT >= 64 || hi) *reinterpret_cast<float*>(e) = power_of_two(exponent_of<F>((int8_t)*e));
     }
+    const auto times = [&](f32x16& x, int first) __attribute__((always_inline)) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 f = *(lds_f32x4*)(lds_byte*)(uintptr_t)(exp_lds + 4 * (first + 8 * g + 4 * hi));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * g + e] *= f[e];
+      }
+    };
+    if constexpr (kScores)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) times(s[b], 32 * b);
     wait_lds();
     wait_loads<3 * NL + NE + NI>();  // page numbers of t + 2
     Valid now = valid[0];
@@ -271,12 +307,7 @@ __global__ __launch_bounds__(256, 1) void attend_narrow_quantized_kernel(AttendQ
     typename Block::Weights weights[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 f = *(lds_f32x4*)(lds_byte*)(uintptr_t)(exp_lds + 4 * (KT + 32 * b + 8 * g + 4 * hi));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[b][4 * g + e] *= f[e];
-      }
+      times(s[b], KT + 32 * b);
       weights[b] = rb.pack(s[b]);
     }
     wait_lds();
@@ -286,7 +317,7 @@ __global__ __launch_bounds__(256, 1) void attend_narrow_quantized_kernel(AttendQ
     if constexpr (kTail && F::kHasNan) {
       if (uneven) {
         uint32_t any = 0;
-        for (int i = lane; i < 2048; i += 64) any |= nan_bytes<F>(reinterpret_cast<const uint32_t*>(values)[i]);
+        for (int i = lane; i < L8::kBytes / 4; i += 64) any |= nan_bytes<F>(reinterpret_cast<const uint32_t*>(values)[i]);
         odd = __any(any != 0);
       }
     }
@@ -409,66 +440,125 @@ __global__ __launch_bounds__(256, 1) void attend_narrow_quantized_kernel(AttendQ
 
 // ---- more rows --------------------------------------------------------------
 
-// The bytes of a stage of KT keys and values on their way from memory through a
-// thread's registers to bf16 tiles in LDS: piece q of the stage's 2 * KT * DP / 16
-// belongs to thread q % THREADS.  A thread's pieces are of one row of the keys
-// (and, where a stage has more pieces than threads, of the same row of the values
-// or of rows a fixed step further).
-template <typename F, int DP, int KT, int THREADS> struct Staging {
-  using R = Rows<bf16_t, DP>;
-  static constexpr int kPieces = DP / 16;               // of a row of bytes
-  static constexpr int kOf = KT * kPieces;              // of the keys, and of the values
-  static constexpr int NP = 2 * kOf / THREADS;          // pieces of a thread
-  static constexpr int NR = kOf < THREADS ? 1 : kOf / THREADS;  // rows it has to find
-  static_assert(NP >= 1 && NP * THREADS == 2 * kOf && THREADS % kPieces == 0, "");
+// The bytes of stages of KT keys and values on their way from memory through
+// registers to 16-bit tiles in LDS.  Each of the KT / 8 waves brings 8 rows of the
+// keys and 8 of the values of a stage.  Where the rows and exponents of four stages
+// lie is found together: lane 16 i + 8 v + r finds row r of the i-th stage, of the
+// keys (v = 0) or the values, three calls apart: ask() requests page numbers, find()
+// turns them into addresses and requests exponents, settle() makes factors of them.
+// Both requests go to LDS, and each call says how many loads of the wave may be newer
+// than the request it needs: held in registers they were waited for where the steps
+// that make them meet those that do not, with every load in flight (216 us for 165,
+// 16 sequences of 256 to 8192 keys and 23 to 45 nodes).
+// fp16 tiles hold the numbers without their powers of two, which have no room in
+// fp16; a stage's `factors` are then, of row k, [k] the key's times c, [KT + k] the
+// value's exponent, [2 KT + k] 2^-exponent.  bf16 tiles hold the values.
+template <typename Elem, typename F, int DP, int KT> struct Staging {
+  using R = Rows<Elem, DP>;
+  static constexpr bool kFactors = Traits<Elem>::kDtype == LORA_F16;
+  static constexpr int kWaves = KT / 8, kPieces = DP / 16;  // pieces: of a row of bytes
+  static constexpr int NP = kPieces < 8 ? 1 : kPieces / 4;  // pieces of a lane: of K, then of V (DP = 64: of either)
+  static constexpr int kRing = 8;  // stages that valid[] and factors[] hold
+  // in LDS
+  struct Shared {
+    const char* row[kWaves][64];
+    int id[kWaves][64], exponent[kWaves][64];
+    float scale[kWaves][2][kFactors ? 1 : 64];
+    float factors[kRing][kFactors ? 3 * KT : 1];
+    __attribute__((aligned(8))) uint8_t valid[kRing][kWaves];
+  };
+  Shared* sh;
+  int wave, lane;
+  int64_t k0;
   u32x4 data[NP];
-  int8_t exps[NP];
-  int id[NR];
 
-  __device__ __forceinline__ static int row(int i) { return ((int)threadIdx.x + i * THREADS) % kOf / kPieces; }
-  __device__ __forceinline__ static int piece() { return (int)threadIdx.x % kPieces; }
-  __device__ __forceinline__ static bool is_v(int i) { return (int)threadIdx.x + i * THREADS >= kOf; }
-
-  // The page numbers of the stage whose first key is k0.
-  __device__ __forceinline__ void ask(const AttendQuantizedParams& p, const Work& w, int64_t k0) {
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      int col;
-      const PageAt a = page_at(p, k0 + row(i), w.k1, col);
-      id[i] = *(global_int*)(entry_of(p, w.b, a, col));
+  __device__ __forceinline__ void init(Shared& shared, const Work& w) {
+    sh = &shared;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    lane = threadIdx.x & 63;
+    k0 = w.k0;
+  }
+  __device__ __forceinline__ PageAt place(const AttendQuantizedParams& p, const Work& w, int four, int& col) const {
+    return page_at(p, k0 + ((int64_t)four * 4 + (lane >> 4)) * KT + wave * 8 + (lane & 7), w.k1, col);
+  }
+  __device__ __forceinline__ void ask(const AttendQuantizedParams& p, const Work& w, int four) {
+    int col;
+    const PageAt a = place(p, w, four, col);
+    word_to_lds(entry_of(p, w.b, a, col), (uint32_t)(uintptr_t)sh->id[wave]);
+  }
+  template <int NEWER> __device__ __forceinline__ void find(const AttendQuantizedParams& p, const Work& w, int four) {
+    int col;
+    const PageAt a = place(p, w, four, col);
+    wait_loads<NEWER>();
+    const int id = sh->id[wave][lane];
+    const bool is_v = (lane >> 3) & 1;
+    const HeadAt h = head_at<uint8_t>(p, w.h, is_v);
+    const ExpAt e = exp_at(p, w.h, is_v);
+    const bool ok = a.in_table && (uint32_t)id < (uint64_t)p.cache.n_pages && id >= 0;
+    const char* none = reinterpret_cast<const char*>(g_zero_row);
+    sh->row[wave][lane] = ok ? reinterpret_cast<const char*>(h.row_at((uint32_t)id, a.place)) : none;
+    byte_to_lds(ok ? reinterpret_cast<const char*>(e.at((uint32_t)id, p.block.div((uint32_t)a.place))) : none,
+                (uint32_t)(uintptr_t)sh->exponent[wave]);
+    const uint64_t all = __ballot(ok);
+    if ((lane & 15) == 0) sh->valid[(four * 4 + (lane >> 4)) % kRing][wave] = (uint8_t)(all >> lane);
+  }
+  template <int NEWER> __device__ __forceinline__ void settle(int four, float c) {
+    wait_loads<NEWER>();
+    const int e = exponent_of<F>((int8_t)sh->exponent[wave][lane]);
+    if constexpr (kFactors) {
+      float* f = sh->factors[(four * 4 + (lane >> 4)) % kRing] + wave * 8 + (lane & 7);
+      if ((lane >> 3) & 1) {
+        // Smaller exponents than -60 are taken for it: what they stand for is far below
+        // the smallest fp16 output either way, and the last factor stays finite in sums.
+        const int ev = max(e, -60);
+        f[KT] = (float)ev;
+        f[2 * KT] = power_of_two(-ev);
+      } else {
+        f[0] = fminf(power_of_two(e) * c, 3.0e38f);  // (finite: a score may be 0)
+      }
+    } else {
+      sh->scale[wave][four & 1][lane] = power_of_two(e);
     }
   }
-  // The stage's bytes and exponents; its rows that are keys are marked in ok [KT].
-  __device__ __forceinline__ void load(const AttendQuantizedParams& p, const Work& w, int64_t k0, uint8_t* ok) {
+  // Row and piece of the lane's i-th 16 bytes among the wave's 8 rows of K and 8 of V.
+  struct Mine {
+    int row, piece, is_v;
+  };
+  __device__ __forceinline__ Mine mine(int i) const {
+    constexpr int kLanes = 8 * kPieces;  // pieces of the wave's rows of K
+    const int q = i * 64 + lane;
+    const int v = q >= kLanes, x = v ? q - kLanes : q;
+    return Mine{x / kPieces, x % kPieces, v};
+  }
+  __device__ __forceinline__ void load(const AttendQuantizedParams& p, int t) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      int col;
-      const PageAt a = page_at(p, k0 + row(i), w.k1, col);
-      const uint32_t of = (uint32_t)id[i % NR];
-      const bool valid = a.in_table && of < (uint64_t)p.cache.n_pages && (int)of >= 0;
-      const bool v = is_v(i);
-      const HeadAt h = head_at<uint8_t>(p, w.h, v);
-      const ExpAt e = exp_at(p, w.h, v);
-      data[i] = ld16_or0(reinterpret_cast<const char*>(h.row_at(of, a.place)) + 16 * piece(), valid && 16 * piece() < p.d);
-      exps[i] = *(global_int8*)(valid ? reinterpret_cast<const char*>(e.at(of, p.block.div((uint32_t)a.place)))
-                                      : reinterpret_cast<const char*>(g_zero_row));
-      if (!v && piece() == 0) ok[row(i)] = valid;
+      const Mine m = mine(i);
+      const char* at = sh->row[wave][16 * (t & 3) + 8 * m.is_v + m.row] + 16 * m.piece;
+      if (p.d != DP && 16 * m.piece >= p.d) at = reinterpret_cast<const char*>(g_zero_row);
+      data[i] = *(global_u32x4*)at;
     }
   }
-  // As bf16 to the tiles: keys at `to`, values behind them.
-  __device__ __forceinline__ void store(char* to) const {
+  // To the tiles: keys at `to`, values behind them.
+  __device__ __forceinline__ void store(char* to, int t) const {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int r = row(i);
-      const float scale = power_of_two(exponent_of<F>(exps[i]));
-      char* at = to + (is_v(i) ? KT * R::kBytes : 0) + r * R::kBytes;
+      const Mine m = mine(i);
+      const int r = wave * 8 + m.row;
       const uint32_t w0 = data[i][0], w1 = data[i][1], w2 = data[i][2], w3 = data[i][3];
-      const u32x4 x[2] = {to_bf16<F>(w0, w1, scale), to_bf16<F>(w2, w3, scale)};
-      // odd rows begin with their second piece: two rows of a write then lie in different banks
-      const bool odd = r & 1;
-      const int c = 2 * piece(), s = R::swz(r);
-      *reinterpret_cast<u32x4*>(at + (((c + (odd ? 1 : 0)) ^ s) << 4)) = odd ? x[1] : x[0];
-      *reinterpret_cast<u32x4*>(at + (((c + (odd ? 0 : 1)) ^ s) << 4)) = odd ? x[0] : x[1];
+      u32x4 x0, x1;
+      if constexpr (kFactors) {
+        x0 = to_f16<F>(w0, w1);
+        x1 = to_f16<F>(w2, w3);
+      } else {
+        const float scale = sh->scale[wave][(t >> 2) & 1][16 * (t & 3) + 8 * m.is_v + m.row];
+        x0 = to_bf16<F>(w0, w1, scale);
+        x1 = to_bf16<F>(w2, w3, scale);
+      }
+      char* at = to + (m.is_v * KT + r) * R::kBytes;
+      const int c = 2 * m.piece, sw = R::swz(r);
+      *reinterpret_cast<u32x4*>(at + ((c ^ sw) << 4)) = x0;
+      *reinterpret_cast<u32x4*>(at + (((c + 1) ^ sw) << 4)) = x1;
     }
   }
 };
@@ -481,14 +571,15 @@ template <typename F, int DP, int KT, int THREADS> struct Staging {
 // left, and stage t + 3 is loaded.
 template <typename Out, typename F, int DP, int KG>
 __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQuantizedParams p) {
-  constexpr int NT = kTerms<Out>;
-  using R = Rows<bf16_t, DP>;
-  using Block = RowBlock<bf16_t, DP, Out, NT>;
+  using Elem = typename Tiles<Out>::Elem;
+  using R = Rows<Elem, DP>;
+  using Block = RowBlock<Elem, DP, Out, Tiles<Out>::NT>;
+  using Stage = Staging<Elem, F, DP, 64>;
   constexpr int KT = 64, NS = 2 / KG, kRing = 4;
   constexpr int kTile = KT * R::kBytes, kStage = 2 * kTile;
   // (aligned to its size, so that an XOR changes stages)
   __shared__ __attribute__((aligned(kRing * kStage))) char s_kv[kRing][kStage];
-  __shared__ uint8_t s_ok[8][KT];
+  __shared__ __attribute__((aligned(16))) typename Stage::Shared s_stage;
   warm_args(p);
   const Work w = work_of<32 * 8 / KG, false>(p);
   if (w.none) return;
@@ -502,7 +593,8 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
   const float c = p.scale == 0.f ? 1.0f : fabsf(p.scale) * kLog2e;
   const int keys = w.k1 - w.k0, inside = min(w.ctx, w.k1) - w.k0;
   const int nt = keys > 0 ? (keys + KT - 1) / KT : 0, nf = inside > 0 ? inside / KT : 0;
-  Staging<F, DP, KT, 512> stage;
+  Stage stage;
+  stage.init(s_stage, w);
   const auto first_key = [&](int t) { return (int64_t)w.k0 + (int64_t)t * KT; };
 
   f32x16 s[NS];
@@ -539,7 +631,9 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
   };
   auto soften = [&](int t, auto tail) __attribute__((always_inline)) {
     if (idle) return;
-    const uint64_t all = __ballot(s_ok[t & 7][lane] != 0);
+    const uint64_t at_all = *reinterpret_cast<const uint64_t*>(s_stage.valid[t % Stage::kRing]);
+    const uint64_t all = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at_all >> 32)) << 32) |
+                         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at_all);
     bool uneven = false;
 #pragma unroll
     for (int b = 0; b < NS; ++b) {
@@ -548,40 +642,56 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
       if constexpr (decltype(tail)::value) {
         seen[b] &= rb.sees(p, w, (int)first_key(t) + (part + b) * kBlock);
         uneven |= __any(seen[b] != valid);
-        if (__any(seen[b] != ~0u)) rb.mask_scores(s[b], seen[b]);
-      } else if (valid != ~0u) {
-        rb.mask_scores(s[b], valid);
       }
+      if (!Stage::kFactors && __any(seen[b] != ~0u)) rb.mask_scores(s[b], seen[b]);
     }
-    rb.weigh(s, c);
+    if constexpr (Stage::kFactors) {
+      const uint32_t at = (uint32_t)(uintptr_t)s_stage.factors[t % Stage::kRing] + 4 * part * kBlock;
+      rb.weigh_scaled(s, seen, at, at + 4 * KT, at + 8 * KT);
+    } else {
+      rb.weigh(s, c);
+    }
 #pragma unroll
     for (int b = 0; b < NS; ++b) weights[b] = rb.pack(s[b]);
     if constexpr (decltype(tail)::value && F::kHasNan)
       odd = uneven && rb.any_odd(s_kv[t % kRing] + kTile + part * kBlock * R::kBytes, NS * kBlock);
   };
+  // Short heads bring and convert a stage among the end of the products, longer ones
+  // after the barrier: 43 us for 49 with heads of 64 (8 sequences of 4096 keys and 48
+  // nodes), 194 for 165 the other way with heads of 128 (16 ragged ones of up to 8192).
+  constexpr bool kEarly = DP <= 64;
+  auto fetch = [&](int t) __attribute__((always_inline)) {
+    if (t + 2 < nt) {
+      stage.store(s_kv[(t + 2) % kRing], t + 2);
+      if (t + 3 < nt) {
+        stage.load(p, t + 3);
+        // the rows of stages 4 k + 4 .. 4 k + 7 in step 4 k, once those of the four before are on their way
+        if ((t & 3) == 0) stage.template find<Stage::NP>(p, w, (t >> 2) + 1);
+        if ((t & 3) == 1) stage.template settle<Stage::NP>((t >> 2) + 1, c);
+        if ((t & 3) == 2) stage.ask(p, w, (t >> 2) + 2);
+      }
+    }
+  };
   auto step = [&](int t, auto tail) __attribute__((always_inline)) {
     __builtin_amdgcn_s_setprio(1);
     multiply(t, t > 0, true, tail);
     __builtin_amdgcn_s_setprio(0);
+    if (kEarly) fetch(t);
     lds_barrier();
-    if (t + 2 < nt) {
-      stage.store(s_kv[(t + 2) % kRing]);
-      if (t + 3 < nt) {
-        stage.load(p, w, first_key(t + 3), s_ok[(t + 3) & 7]);
-        stage.ask(p, w, first_key(t + 4));
-      }
-    }
+    if (!kEarly) fetch(t);
     soften(t, tail);
     lds_barrier();
   };
 
   if (nt > 0) {
-    stage.ask(p, w, first_key(0));
+    stage.ask(p, w, 0);
+    stage.template find<0>(p, w, 0);
+    stage.template settle<0>(0, c);
+    stage.ask(p, w, 1);
 #pragma unroll 1
     for (int t = 0; t < 3; ++t) {
-      if (t > 0) stage.store(s_kv[t - 1]);
-      stage.load(p, w, first_key(t), s_ok[t]);
-      stage.ask(p, w, first_key(t + 1));
+      if (t > 0) stage.store(s_kv[t - 1], t - 1);
+      stage.load(p, t);
     }
     rb.place((uint32_t)(uintptr_t)s_kv[0] + part * kBlock * R::kBytes,
              (uint32_t)(uintptr_t)s_kv[0] + kTile + part * kBlock * R::kBytes);
@@ -635,60 +745,72 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
 // stage before it and converted into the other place at its end.
 template <typename Out, typename F, int DP>
 __global__ __launch_bounds__(kThreads, 1) void attend_wide_quantized_kernel(AttendQuantizedParams p) {
-  constexpr int NT = kTerms<Out>;
-  using R = Rows<bf16_t, DP>;
+  using Elem = typename Tiles<Out>::Elem;
+  using R = Rows<Elem, DP>;
   constexpr int KT = kBlock;
+  using Stage = Staging<Elem, F, DP, KT>;
   constexpr int kTile = KT * R::kBytes;
   constexpr int kLds = kTile < kStoreBytes<DP> ? 4 * kStoreBytes<DP> : 4 * kTile;
   // (aligned to its two stages, so that an XOR changes them)
   __shared__ __attribute__((aligned(4 * kTile))) char s_kv[kLds];
   const auto place = [&](int t) { return s_kv + (t & 1) * 2 * kTile; };
-  __shared__ uint8_t s_ok[4][KT];
+  __shared__ __attribute__((aligned(16))) typename Stage::Shared s_stage;
   warm_args(p);
   const Work w = work_of<4 * kBlock, true>(p);
   if (w.none) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  RowBlock<bf16_t, DP, Out, NT> rb;
+  RowBlock<Elem, DP, Out, Tiles<Out>::NT> rb;
   rb.init(p, w, w.row0 + wave * kBlock);
   const bool idle = w.row0 + wave * kBlock >= w.rows;  // a wave without rows only fetches
   const float c = p.scale == 0.f ? 1.0f : fabsf(p.scale) * kLog2e;
   const int keys = w.k1 - w.k0, inside = min(w.ctx, w.k1) - w.k0;
   const int nt = keys > 0 ? (keys + KT - 1) / KT : 0, nf = inside > 0 ? inside / KT : 0;
-  Staging<F, DP, KT, kThreads> stage;
+  Stage stage;
+  stage.init(s_stage, w);
   const auto first_key = [&](int t) { return (int64_t)w.k0 + (int64_t)t * KT; };
   if (nt > 0) {
-    stage.ask(p, w, first_key(0));
-    stage.load(p, w, first_key(0), s_ok[0]);
-    stage.ask(p, w, first_key(1));
-    stage.store(place(0));
-    stage.load(p, w, first_key(1), s_ok[1]);
-    stage.ask(p, w, first_key(2));
+    stage.ask(p, w, 0);
+    stage.template find<0>(p, w, 0);
+    stage.template settle<0>(0, c);
+    stage.ask(p, w, 1);
+    stage.load(p, 0);
+    stage.store(place(0), 0);
+    stage.load(p, 1);
   }
   auto tile = [&](int t, auto tail) __attribute__((always_inline)) {
     constexpr bool kTail = decltype(tail)::value;
     lds_barrier();  // everyone's part of stage t is there, and everyone is done with stage t - 1
     if (t + 1 < nt) {
-      stage.store(place(t + 1));
+      stage.store(place(t + 1), t + 1);
       if (t + 2 < nt) {
-        stage.load(p, w, first_key(t + 2), s_ok[(t + 2) & 3]);
-        stage.ask(p, w, first_key(t + 3));
+        stage.load(p, t + 2);
+        // the rows of stages 4 k + 4 .. 4 k + 7 in step 4 k + 1, once those of the four before are on their way
+        if ((t & 3) == 1) stage.template find<Stage::NP>(p, w, (t >> 2) + 1);
+        if ((t & 3) == 2) stage.template settle<Stage::NP>((t >> 2) + 1, c);
+        if ((t & 3) == 3) stage.ask(p, w, (t >> 2) + 2);
       }
     }
     if (!idle) {
       f32x16 s[1] = {rb.template scores<0>()};
-      const uint32_t valid = (uint32_t)__ballot(s_ok[t & 3][rb.r32] != 0);
-      uint32_t seen = valid;
+      const uint32_t valid =
+          __builtin_amdgcn_readfirstlane(*reinterpret_cast<const uint32_t*>(s_stage.valid[t % Stage::kRing]));
+      uint32_t seen[1] = {valid};
       bool uneven = false;
       if constexpr (kTail) {
-        seen &= rb.sees(p, w, (int)first_key(t));
-        uneven = __any(seen != valid);
+        seen[0] &= rb.sees(p, w, (int)first_key(t));
+        uneven = __any(seen[0] != valid);
       }
-      if (__any(seen != ~0u)) rb.mask_scores(s[0], seen);
-      rb.weigh(s, c);
+      if constexpr (Stage::kFactors) {
+        const uint32_t at = (uint32_t)(uintptr_t)s_stage.factors[t % Stage::kRing];
+        rb.weigh_scaled(s, seen, at, at + 4 * KT, at + 8 * KT);
+      } else {
+        if (__any(seen[0] != ~0u)) rb.mask_scores(s[0], seen[0]);
+        rb.weigh(s, c);
+      }
       const char* vb = place(t) + kTile;
       if (kTail && F::kHasNan && uneven && rb.any_odd(vb, KT)) {
         rb.template add_values<kTail, 0>(rb.pack(s[0]));
-        rb.add_odd(vb, seen);
+        rb.add_odd(vb, seen[0]);
       } else {
         rb.template add_values<false, 0>(rb.pack(s[0]));
       }
@@ -725,10 +847,10 @@ Plan plan_kind(bool fp32, int32_t nodes, int32_t group, int32_t d) {
   const int64_t rows = (int64_t)nodes * group;
   const int dp = padded(d);
   int64_t tile = kBlock;
-  a.groups = 1024;
+  a.groups = dp == 256 ? 256 : 512;
   a.kind = Kind::kNarrow;
   a.block = kThreads;
-  a.unit = 4 * 8192 / dp;
+  a.unit = 4 * (dp == 256 ? 8192 : 4096) / dp;
   if (rows > kBlock) {
     a.kind = dp > (fp32 ? 64 : 128) ? Kind::kWide : rows > 4 * kBlock ? Kind::kTurns256 : Kind::kTurns128;
     tile = a.kind == Kind::kTurns256 ? 8 * kBlock : 4 * kBlock;
@@ -741,7 +863,11 @@ Plan plan_kind(bool fp32, int32_t nodes, int32_t group, int32_t d) {
 }
 
 // How the keys are cut: even chunks, so long that about `groups` workgroups run in
-// all where every sequence is as long as its bound, and no shorter than kMinChunk.
+// all where every sequence is as long as its bound, and no shorter than kMinChunk:
+// as many workgroups as the chip holds at once (the wide kernel: two a compute
+// unit).  More cost their first loads and parts: 64 sequences of 4096 keys, 32 + 8
+// bf16 heads of 128, 92 us with 512 workgroups, 99 with 1024, 104 with 2048; one of
+// 32768: 27, 31 and 37.
 constexpr int64_t kMinChunk = 256;
 constexpr int64_t kMaxChunk = (int64_t)1 << 30;
 

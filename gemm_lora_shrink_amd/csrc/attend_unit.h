@@ -14,6 +14,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) const float lds_float;
+typedef __attribute__((address_space(3))) const f32x4 lds_f32x4;
 typedef __attribute__((address_space(3))) char lds_byte;
 
 constexpr int kThreads = 256;
@@ -425,6 +426,63 @@ template <typename Elem, int DP, typename Out = Elem, int NT = 1> struct RowBloc
       for (int i = 0; i < 16; ++i) {
         s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, -ms));
         sum[i & 3] += s[b][i];
+      }
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  }
+
+  // The same where keys and values lie in the tiles without their powers of two: key
+  // i's score is s a[i], its value's factor 2^b[i].  The factor is part of the
+  // weight, 2^(s a + b - m), so m follows what weights and values are together
+  // and small factors cost a weight no bits; l sums the weights without it, times
+  // c[i] = 2^-b[i].  a, b and c: LDS addresses of the 32 NS keys' numbers; seen:
+  // which keys the row sees.
+  template <int NS>
+  __device__ __forceinline__ void weigh_scaled(f32x16 (&s)[NS], const uint32_t (&seen)[NS], uint32_t a, uint32_t b, uint32_t c) {
+    constexpr float kBelow = Mma32<Elem>::kBelow, kMost = Mma32<Elem>::kMost;
+    const auto four = [&](uint32_t at, int n, int g) {
+      return *((lds_f32x4*)(lds_byte*)(uintptr_t)(at + 16 * hi) + (8 * n + 2 * g));
+    };
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 an = four(a, n, g), bn = four(b, n, g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][4 * g + e] = __builtin_fmaf(s[n][4 * g + e], an[e], bn[e]);
+      }
+      if (__any(seen[n] != ~0u)) mask_scores(s[n], seen[n]);
+    }
+    float mx4[4] = {s[0][0], s[0][1], s[0][2], s[0][3]};
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int i = n ? 0 : 4; i < 16; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[n][i]);
+    const float mx = half_max(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])));
+    if (__any(mx - m > kMost)) {
+      float mn = mx - kBelow;
+      if (kBelow > 0.f && mx - mn > kMost) mn = mx;  // a score that has no units left
+      if (!(mx - m > kMost)) mn = m;
+      const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
+      l *= f;
+#pragma unroll
+      for (int db = 0; db < R::kDB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[db][i] *= f;
+      m = mn;
+    }
+    const float ms = m == -INFINITY ? 0.f : m;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 cn = four(c, n, g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = __builtin_amdgcn_exp2f(s[n][4 * g + e] - ms);
+          s[n][4 * g + e] = w;
+          sum[e] = __builtin_fmaf(w, cn[e], sum[e]);
+        }
       }
     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
   }

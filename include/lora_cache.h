@@ -86,8 +86,8 @@ lora_status lora_store_quantized(lora_dtype dt, const void *k, int64_t ldk, cons
  * workspace rules (the bytes from lora_quantized_workspace_bytes).
  *   dt   of q and out.  Keys and values enter the products as they are held,
  *        exactly.  q is exact too; the softmax weights, times the power of two
- *        of their value's block, are rounded to 8 bits for bf16, 16 for fp16
- *        and 24 for fp32.
+ *        of their value's block, are rounded to 8 bits for bf16, 11 at least
+ *        for fp16 and 24 for fp32.
  */
 size_t lora_quantized_workspace_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t q_heads,
                                       int32_t kv_heads, int32_t d);

@@ -11,9 +11,9 @@ sum |q| |k| (keys and values as the cache holds them, which enter exactly):
    sum of 3 d exact products in fp32: off by ds <= (3 d + 2) u z; every weight's
    exponential by 4 u, and by u times its argument (<= 2 z + ds in absolute
    value), which moves the weighted mean by at most 2 (ds + (4 + 2 z) u) A;
- - a weight enters the product with the values as one (bf16), two (fp16) or
-   three (fp32) numbers of 8 bits, each off by half a step of what the ones
-   before it left: w = 2^-8, 2^-16, 2^-24 of itself, w A;
+ - a weight enters the product with the values as one bf16 number, one fp16
+   number (or two bf16 ones) or, for fp32, three bf16 ones, each off by half a
+   step of what the ones before it left: w = 2^-8, 2^-11, 2^-24 of itself, w A;
  - the sums run over L keys and three numbers a weight: 4 L u A for the
    numerator and the denominator;
  - the output is rounded once: h |o|, or the type's smallest step; it is also
@@ -38,7 +38,7 @@ pytestmark = pytest.mark.gpu
 
 TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 FORMATS = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
-WEIGHT = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -16, torch.float32: 2.0 ** -24}
+WEIGHT = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 U = 2.0 ** -24
 E4M3 = co.e4m3_numbers()
 
