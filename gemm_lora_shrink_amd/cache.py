@@ -67,10 +67,10 @@ def _lib():
         lib.lora_pages_workspace_bytes.restype = sz
         table = [vp, i64, i32, i32]
         lib.lora_reserve_pages.argtypes = [vp, i64, *table, vp, i32, vp, vp, sz, vp]
-        lib.lora_fork_sequences.argtypes = [vp, i64, vp, i64, i32, vp, i64, i32, i32, vp, vp, vp, i32, i32, vp, vp, vp, vp, sz,
-                                            vp]
+        lib.lora_fork_sequences.argtypes = [vp, i64, vp, i64, i32, vp, i64, i32, i32, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32,
+                                            vp, sz, vp]
         lib.lora_release_pages.argtypes = [vp, i64, *table, vp, vp, i32, i32, vp]
-        lib.lora_compact_pages.argtypes = [vp, i64, *table, vp, vp, vp, vp, vp, sz, vp]
+        lib.lora_compact_pages.argtypes = [vp, i64, *table, vp, vp, vp, vp, vp, i32, vp, sz, vp]
         lib.lora_copy_pages.argtypes = [vp, i32, i64, vp, vp, i32, vp, vp]
         for name in ("store_quantized", "tree_attention_quantized", "keep_path_quantized", "reserve_pages",
                      "fork_sequences", "release_pages", "compact_pages", "copy_pages"):
@@ -232,23 +232,26 @@ def keep_path_quantized(caches, page_table, context, path, n_kept, *, stream=Non
     first = caches[0]
     dev = _gpu(first[0], "the cache")
     held, shape = _cache(first, dev)
-    strides, dtype, of = [t.stride() for t in first], first[0].dtype, first[2].shape
-    for c in caches:
-        if len(c) != 4 or c[0].shape != shape or c[1].shape != shape or c[2].shape != of or c[3].shape != of:
-            raise _bad("the layers' caches must be alike in shape")
-        for t, s, dt in zip(c, strides, (dtype, dtype, _I8, _I8)):
-            if t.stride() != s or t.dtype is not dt or t.get_device() != dev:
-                raise _bad("the layers' caches must be alike in strides, type and GPU")
+    if any(len(c) != 4 for c in caches):
+        raise _bad("a quantized cache is k, v, k_exp and v_exp")
+    at = []
+    for t, like in zip(zip(*caches), first):
+        shape_, dtype, stride = like.shape, like.dtype, like.stride()
+        dense = like.is_contiguous()
+        for x in t:
+            if x.shape != shape_ or x.dtype is not dtype or x.get_device() != dev or (
+                    not x.is_contiguous() if dense else x.stride() != stride):
+                raise _bad("the layers' caches must be alike in shape, strides, type and GPU")
+        at.append([x.data_ptr() for x in t])
     B = _i32(context.numel(), "the number of sequences")
     table = _int_rows(page_table, "page_table", dev, B)
     steps = _int_rows(path, "path", dev, B)
-    kept, at = _vector(n_kept, "n_kept", _I32, dev, B), _vector(context, "context", _I32, dev, B)
+    kept, ctx = _vector(n_kept, "n_kept", _I32, dev, B), _vector(context, "context", _I32, dev, B)
     for i in range(0, n, MAX_KEEP_LAYERS):
-        some = caches[i:i + MAX_KEEP_LAYERS]
-        layers = struct.Struct(f"@{len(some)}P")
-        _check(_lib().lora_keep_path_quantized(held, *(layers.pack(*(c[j].data_ptr() for c in some)) for j in range(4)),
-                                               len(some), shape[1], shape[3], B, *table, at, *steps, kept,
-                                               _stream_of(stream, dev)))
+        m = min(n - i, MAX_KEEP_LAYERS)
+        layers = struct.Struct(f"@{m}P")
+        _check(_lib().lora_keep_path_quantized(held, *(layers.pack(*x[i:i + m]) for x in at), m, shape[1], shape[3], B,
+                                               *table, ctx, *steps, kept, _stream_of(stream, dev)))
 
 
 # ---- pages -------------------------------------------------------------------
@@ -305,6 +308,18 @@ class PagedTensors:
 
 def _paged(tensors):
     return tensors if isinstance(tensors, PagedTensors) else PagedTensors(tensors)
+
+
+def _of_pool(tensors, n_pages, dev):
+    """(the C view, the number) of a pool's tensors, of which there may be none."""
+    if not isinstance(tensors, PagedTensors):
+        tensors = tuple(tensors)
+        if not tensors:
+            return None, 0
+        tensors = PagedTensors(tensors)
+    if tensors.n_pages != n_pages or tensors.dev != dev:
+        raise _bad(f"the tensors must have the pool's {n_pages} pages and be on its GPU")
+    return tensors.packed, tensors.n
 
 
 def copy_pages(tensors, source, target, *, count=None, stream=None):
@@ -405,21 +420,13 @@ def fork_sequences(refs, page_table, parents, children, lengths, *, page_size, t
     if to[2] != source[2]:
         raise _bad(f"out_table must have {source[2]} columns (it has {to[2]})")
     m = _i32(parents.numel(), "the number of forks")
-    if len(tensors) if not isinstance(tensors, PagedTensors) else True:
-        tensors = _paged(tensors)
-        if tensors.n_pages != n or tensors.dev != dev:
-            raise _bad(f"the tensors must have the pool's {n} pages and be on its GPU")
-    else:
-        tensors = None
+    packed, n_tensors = _of_pool(tensors, n, dev)
     of, dest, _, ws, ws_bytes, kept = _space(workspace, n, m, refs, dev, stream)
-    s = _stream_of(stream, dev)
-    lib = _lib()
-    _check(lib.lora_fork_sequences(at, n, source[0], source[1], source[3], to[0], to[1], to[3], to[2],
-                                   _vector(parents, "parents", _I32, dev, m), _vector(children, "children", _I32, dev, m),
-                                   _vector(lengths, "lengths", _I32, dev, m), m, _i32(page_size, "page_size"), of, dest,
-                                   None if missing is None else _vector(missing, "missing", _I32, dev, 1), ws, ws_bytes, s))
-    if tensors is not None and m:
-        _check(lib.lora_copy_pages(tensors.packed, tensors.n, n, of, dest, m, None, s))
+    _check(_lib().lora_fork_sequences(
+        at, n, source[0], source[1], source[3], to[0], to[1], to[3], to[2], _vector(parents, "parents", _I32, dev, m),
+        _vector(children, "children", _I32, dev, m), _vector(lengths, "lengths", _I32, dev, m), m,
+        _i32(page_size, "page_size"), of, dest, None if missing is None else _vector(missing, "missing", _I32, dev, 1),
+        packed, n_tensors, ws, ws_bytes, _stream_of(stream, dev)))
     return out_table
 
 
@@ -444,18 +451,10 @@ def compact_pages(refs, page_table, *, tensors=(), n_live=None, workspace=None, 
     table that names pages of the pool has to be in page_table."""
     dev, at, n = _pool(refs)
     table = _table(page_table, "page_table", dev)
-    if len(tensors) if not isinstance(tensors, PagedTensors) else True:
-        tensors = _paged(tensors)
-        if tensors.n_pages != n or tensors.dev != dev:
-            raise _bad(f"the tensors must have the pool's {n} pages and be on its GPU")
-    else:
-        tensors = None
+    packed, n_tensors = _of_pool(tensors, n, dev)
     if n_live is None:
         n_live = _made(stream, torch.empty, (), dtype=_I32, device=refs.device)
     of, dest, moved, ws, ws_bytes, kept = _space(workspace, n, 0, refs, dev, stream)
-    s = _stream_of(stream, dev)
-    lib = _lib()
-    _check(lib.lora_compact_pages(at, n, *table, of, dest, _vector(n_live, "n_live", _I32, dev, 1), moved, ws, ws_bytes, s))
-    if tensors is not None and n > 1:
-        _check(lib.lora_copy_pages(tensors.packed, tensors.n, n, of, dest, n // 2, moved, s))
+    _check(_lib().lora_compact_pages(at, n, *table, of, dest, _vector(n_live, "n_live", _I32, dev, 1), moved, packed,
+                                     n_tensors, ws, ws_bytes, _stream_of(stream, dev)))
     return n_live

@@ -30,8 +30,12 @@ struct E4m3 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)  // (the median drops a NaN)
       y[i] = x[i] != x[i] ? x[i] : __builtin_amdgcn_fmed3f(x[i], -kLargest, kLargest);
-    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+    return bytes_within(y, 1.0f);
+  }
+  // The same of x times a power of two where no |x| passes the largest.
+  __device__ static inline uint32_t bytes_within(const float* x, float by) {
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * by, x[1] * by, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2] * by, x[3] * by, lo, true);
   }
 };
 struct Int8 {
@@ -45,13 +49,20 @@ struct Int8 {
     for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(w >> (8 * i));
   }
   __device__ static inline uint32_t bytes(const float* x) {
-    uint32_t w = 0;
+    float y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float y = x[i] != x[i] ? 0.f : __builtin_amdgcn_fmed3f(x[i], -kLargest, kLargest);
-      w |= ((uint32_t)(int)__builtin_rintf(y) & 0xffu) << (8 * i);
-    }
-    return w;
+    for (int i = 0; i < 4; ++i) y[i] = x[i] != x[i] ? 0.f : __builtin_amdgcn_fmed3f(x[i], -kLargest, kLargest);
+    return bytes_within(y, 1.0f);
+  }
+  // In 1.5 * 2^23 + x the sum's rounding (to the nearest, ties to even) leaves the
+  // whole number x in the low byte.
+  __device__ static inline uint32_t bytes_within(const float* x, float by) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(__builtin_fmaf(x[i], by, 12582912.0f));
+    // (bytes 0 .. 3 of the second operand are 0 .. 3, of the first 4 .. 7)
+    const uint32_t lo = __builtin_amdgcn_perm(w[1], w[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(w[3], w[2], 0x04000c0cu);
+    return lo | hi;
   }
 };
 
@@ -115,12 +126,26 @@ struct ForkParams {
   int32_t *source, *target, *missing;  // missing nullable
 };
 
-struct CopyParams {
-  lora_paged_tensor t[LORA_COPY_TENSORS];
+// A tensor with pages, counted in accesses of `unit` bytes (strides in bytes).
+struct PagedTensor {
+  char* data;
+  int64_t page, outer, inner;
+  uint32_t units, run, n_inner;  // of a page, of a run; runs of the inner dimension
+  uint16_t unit, whole;          // whole: a page is one run
+};
+constexpr int kCopyTensors = 64;
+struct MoveParams {
+  enum Task : int32_t { kNone = 0, kFork = 1, kRename = 2 };
+  PagedTensor t[kCopyTensors];
   int64_t n_pages;
   const int32_t *source, *target, *count;  // count nullable
-  int32_t n, unit;                         // bytes of an access
+  int32_t n, n_tensors;
+  Task task;
+  PoolParams pool;
+  ForkParams fork;        // kFork
+  const int32_t* n_live;  // kRename
 };
+static_assert(sizeof(MoveParams) <= 4096, "a kernel's arguments");
 
 // Whether launch_store_quantized's grid holds T tokens.
 bool store_quantized_fits(int32_t T);
@@ -141,6 +166,7 @@ hipError_t launch_fork(const PoolParams& p, const ForkParams& f, hipStream_t str
 hipError_t launch_release(const PoolParams& p, const int32_t* rows, const int32_t* keep, int32_t n, hipStream_t stream);
 hipError_t launch_compact(const PoolParams& p, int32_t* source, int32_t* target, int32_t* n_live, int32_t* n_moves,
                           hipStream_t stream);
-hipError_t launch_copy_pages(const CopyParams& p, int32_t n_tensors, hipStream_t stream);
+// The copies and, beside them, the rows of p.task.
+hipError_t launch_move(const MoveParams& p, hipStream_t stream);
 
 }  // namespace lora

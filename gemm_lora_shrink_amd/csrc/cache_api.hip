@@ -115,6 +115,42 @@ lora_status check_workspace(const void* workspace, size_t bytes, int64_t n_pages
   return LORA_OK;
 }
 
+lora_status check_tensors(const lora_paged_tensor* tensors, int32_t n_tensors, int64_t n_pages) {
+  if (n_tensors < 0) return fail(LORA_ERR_INVALID_ARG, "n_tensors = %d is negative", n_tensors);
+  if (n_tensors > 0 && !tensors) return fail(LORA_ERR_INVALID_ARG, "tensors is null");
+  for (int i = 0; i < n_tensors; ++i) {
+    const lora_paged_tensor& t = tensors[i];
+    if (!t.data && n_pages > 0) return fail(LORA_ERR_INVALID_ARG, "tensor %d has no data", i);
+    if (t.n_outer < 1 || t.n_inner < 1 || t.run < 1)
+      return fail(LORA_ERR_INVALID_ARG, "the pages of tensor %d hold nothing", i);
+    if (t.page < 0 || t.outer < 0 || t.inner < 0) return fail(LORA_ERR_INVALID_ARG, "a stride of tensor %d is negative", i);
+    if ((double)t.n_outer * t.n_inner * t.run >= 2147483648.0)
+      return fail(LORA_ERR_UNSUPPORTED, "a page of tensor %d has 2 GiB or more", i);
+  }
+  return LORA_OK;
+}
+
+// The widest access that the tensor's addresses and runs allow.
+PagedTensor tensor_of(const lora_paged_tensor& t) {
+  const uint64_t all = reinterpret_cast<uintptr_t>(t.data) | (uint64_t)t.page | (uint64_t)t.run |
+                       (t.n_outer > 1 ? (uint64_t)t.outer : 0) | (t.n_inner > 1 ? (uint64_t)t.inner : 0);
+  const uint32_t unit = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 1, run = (uint32_t)t.run / unit;
+  return PagedTensor{static_cast<char*>(t.data), t.page, t.outer, t.inner, run * t.n_outer * t.n_inner, run,
+                     (uint32_t)t.n_inner, (uint16_t)unit, (uint16_t)(t.n_outer == 1 && t.n_inner == 1)};
+}
+
+// The tensors' copies, kCopyTensors a launch, p.task beside the first of them.
+hipError_t move_all(MoveParams& p, const lora_paged_tensor* tensors, int32_t n_tensors, hipStream_t stream) {
+  int i = 0;
+  do {
+    for (p.n_tensors = 0; p.n_tensors < kCopyTensors && i < n_tensors; ++i) p.t[p.n_tensors++] = tensor_of(tensors[i]);
+    const hipError_t e = launch_move(p, stream);
+    if (e != hipSuccess) return e;
+    p.task = MoveParams::kNone;
+  } while (i < n_tensors);
+  return hipSuccess;
+}
+
 PoolParams pool_of(int32_t* refs, int64_t n_pages, int32_t* table, int64_t ld_table, int32_t n_table, int32_t B,
                    int32_t page_size, void* workspace) {
   return PoolParams{refs, n_pages, table, ld_table, n_table, B, fast_div((uint32_t)page_size),
@@ -327,7 +363,8 @@ LORA_EXPORT lora_status lora_fork_sequences(int32_t* refs, int64_t n_pages, cons
                                             int32_t B_from, int32_t* to_table, int64_t ld_to, int32_t B_to,
                                             int32_t n_table, const int32_t* parents, const int32_t* children,
                                             const int32_t* lengths, int32_t n_forks, int32_t page_size, int32_t* source,
-                                            int32_t* target, int32_t* missing, void* workspace, size_t workspace_bytes,
+                                            int32_t* target, int32_t* missing, const lora_paged_tensor* tensors,
+                                            int32_t n_tensors, void* workspace, size_t workspace_bytes,
                                             hipStream_t stream) {
   clear_error();
   lora_status st = check_pool(refs, n_pages, to_table, ld_to, n_table, B_to);
@@ -339,11 +376,23 @@ LORA_EXPORT lora_status lora_fork_sequences(int32_t* refs, int64_t n_pages, cons
   if (page_size < 1) return fail(LORA_ERR_INVALID_ARG, "page_size = %d must be >= 1", page_size);
   if (n_forks > 0 && (!parents || !children || !lengths || !source || !target))
     return fail(LORA_ERR_INVALID_ARG, "parents, children, lengths, source or target is null");
+  if ((st = check_tensors(tensors, n_tensors, n_pages)) != LORA_OK) return st;
   if (n_forks == 0 && !missing) return LORA_OK;
   if ((st = check_workspace(workspace, workspace_bytes, n_pages, n_forks)) != LORA_OK) return st;
   const PoolParams p = pool_of(refs, n_pages, to_table, ld_to, n_table, B_to, page_size, workspace);
   const ForkParams f{from_table, ld_from, B_from, n_forks, parents, children, lengths, source, target, missing};
-  const hipError_t e = launch_fork(p, f, stream);
+  hipError_t e = launch_fork(p, f, stream);
+  if (e == hipSuccess && n_forks > 0) {
+    MoveParams m{};
+    m.n_pages = n_pages;
+    m.source = source;
+    m.target = target;
+    m.n = n_forks;
+    m.task = MoveParams::kFork;
+    m.pool = p;
+    m.fork = f;
+    e = move_all(m, tensors, n_tensors, stream);
+  }
   if (e != hipSuccess) return hip_fail(e, "fork launch");
   return LORA_OK;
 }
@@ -367,16 +416,30 @@ LORA_EXPORT lora_status lora_release_pages(int32_t* refs, int64_t n_pages, int32
 
 LORA_EXPORT lora_status lora_compact_pages(int32_t* refs, int64_t n_pages, int32_t* page_table, int64_t ld_table,
                                            int32_t n_table, int32_t B, int32_t* source, int32_t* target,
-                                           int32_t* n_live, int32_t* n_moves, void* workspace, size_t workspace_bytes,
+                                           int32_t* n_live, int32_t* n_moves, const lora_paged_tensor* tensors,
+                                           int32_t n_tensors, void* workspace, size_t workspace_bytes,
                                            hipStream_t stream) {
   clear_error();
   lora_status st = check_pool(refs, n_pages, page_table, ld_table, n_table, B);
   if (st != LORA_OK) return st;
   if (!n_live || !n_moves) return fail(LORA_ERR_INVALID_ARG, "n_live or n_moves is null");
   if (n_pages > 1 && (!source || !target)) return fail(LORA_ERR_INVALID_ARG, "source or target is null");
+  if ((st = check_tensors(tensors, n_tensors, n_pages)) != LORA_OK) return st;
   if ((st = check_workspace(workspace, workspace_bytes, n_pages, 0)) != LORA_OK) return st;
   const PoolParams p = pool_of(refs, n_pages, page_table, ld_table, n_table, B, 1, workspace);
-  const hipError_t e = launch_compact(p, source, target, n_live, n_moves, stream);
+  hipError_t e = launch_compact(p, source, target, n_live, n_moves, stream);
+  if (e == hipSuccess) {
+    MoveParams m{};
+    m.n_pages = n_pages;
+    m.source = source;
+    m.target = target;
+    m.count = n_moves;
+    m.n = (int32_t)(n_pages / 2);
+    m.task = B > 0 ? MoveParams::kRename : MoveParams::kNone;
+    m.pool = p;
+    m.n_live = n_live;
+    e = move_all(m, tensors, n_tensors, stream);
+  }
   if (e != hipSuccess) return hip_fail(e, "page compaction launch");
   return LORA_OK;
 }
@@ -385,43 +448,20 @@ LORA_EXPORT lora_status lora_copy_pages(const lora_paged_tensor* tensors, int32_
                                         const int32_t* source, const int32_t* target, int32_t n, const int32_t* count,
                                         hipStream_t stream) {
   clear_error();
-  if (n_tensors < 0 || n < 0) return fail(LORA_ERR_INVALID_ARG, "n_tensors or n is negative");
+  if (n < 0) return fail(LORA_ERR_INVALID_ARG, "n = %d is negative", n);
   if (n_pages < 0 || n_pages > LORA_MAX_POOL_PAGES)
     return fail(LORA_ERR_INVALID_ARG, "n_pages = %lld is not within 0 and %d", (long long)n_pages, LORA_MAX_POOL_PAGES);
-  if (n_tensors > 0 && !tensors) return fail(LORA_ERR_INVALID_ARG, "tensors is null");
-  for (int i = 0; i < n_tensors; ++i) {
-    const lora_paged_tensor& t = tensors[i];
-    if (!t.data && n_pages > 0) return fail(LORA_ERR_INVALID_ARG, "tensor %d has no data", i);
-    if (t.n_outer < 1 || t.n_inner < 1 || t.run < 1)
-      return fail(LORA_ERR_INVALID_ARG, "the pages of tensor %d hold nothing", i);
-    if (t.page < 0 || t.outer < 0 || t.inner < 0) return fail(LORA_ERR_INVALID_ARG, "a stride of tensor %d is negative", i);
-    if ((double)t.n_outer * t.n_inner * t.run > 1e15) return fail(LORA_ERR_UNSUPPORTED, "the pages of tensor %d are too large", i);
-  }
+  const lora_status st = check_tensors(tensors, n_tensors, n_pages);
+  if (st != LORA_OK) return st;
   if (n_tensors == 0 || n == 0 || n_pages == 0) return LORA_OK;
   if (!source || !target) return fail(LORA_ERR_INVALID_ARG, "source or target is null");
-  // tensors of one width of access share a launch, in their order
-  const auto unit_of = [](const lora_paged_tensor& t) {
-    const uint64_t all = reinterpret_cast<uintptr_t>(t.data) | (uint64_t)t.page | (uint64_t)t.run |
-                         (t.n_outer > 1 ? (uint64_t)t.outer : 0) | (t.n_inner > 1 ? (uint64_t)t.inner : 0);
-    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 1;
-  };
-  for (const int unit : {16, 4, 1}) {
-    CopyParams p{};
-    p.n_pages = n_pages;
-    p.source = source;
-    p.target = target;
-    p.count = count;
-    p.n = n;
-    p.unit = unit;
-    int m = 0;
-    for (int i = 0; i <= n_tensors; ++i) {
-      if (m == LORA_COPY_TENSORS || (i == n_tensors && m > 0)) {
-        const hipError_t e = launch_copy_pages(p, m, stream);
-        if (e != hipSuccess) return hip_fail(e, "page copy launch");
-        m = 0;
-      }
-      if (i < n_tensors && unit_of(tensors[i]) == unit) p.t[m++] = tensors[i];
-    }
-  }
+  MoveParams m{};
+  m.n_pages = n_pages;
+  m.source = source;
+  m.target = target;
+  m.count = count;
+  m.n = n;
+  const hipError_t e = move_all(m, tensors, n_tensors, stream);
+  if (e != hipSuccess) return hip_fail(e, "page copy launch");
   return LORA_OK;
 }

@@ -135,6 +135,14 @@ lora_status lora_keep_path_quantized(const lora_quantized_cache *cache, void *co
 #define LORA_MAX_POOL_PAGES (1 << 28)
 size_t lora_pages_workspace_bytes(int64_t n_pages, int32_t n_seqs);
 
+/* A tensor with pages: page p is n_outer x n_inner runs of `run` bytes, the
+ * strides between them in bytes. */
+typedef struct {
+  void *data;
+  int64_t page, outer, inner;
+  int32_t n_outer, n_inner, run;
+} lora_paged_tensor;
+
 /*
  * Pages for sequences to grow into: of each sequence b, the entries of the
  * columns below ceil(lengths[b] / page_size) that are -1 get a free page each
@@ -152,23 +160,25 @@ lora_status lora_reserve_pages(int32_t *refs, int64_t n_pages, int32_t *page_tab
  * tokens of row parents[f] of from_table: it shares the pages that are full
  * (refs + 1) and gets a free page (refs = 1) for one that is filled in part;
  * its other entries become -1.  The free pages go to the forks in their order.
- * What the partly filled pages hold is then copied with lora_copy_pages.
+ * What the partly filled pages hold is copied in every tensor.
  *   from_table, to_table   [B][..], n_table columns each; may be the same where
  *                          no child is a parent of the call.  What a child's row
  *                          held before is overwritten, not released.
  *   parents, children, lengths   [n_forks] int32; children must differ.  A fork
  *                          with a child outside [0, B_to) does nothing, with a
  *                          parent outside [0, B_from) it makes an empty sequence
- *   source, target         [n_forks] int32, written: the page to copy and where
- *                          to, -1 where there is none
+ *   source, target         [n_forks] int32, written: the page that was copied and
+ *                          where to, -1 where there is none
  *   missing                nullable, one int32, written: forks whose partly
  *                          filled page got no free one (their entry is -1)
+ *   tensors                [host] n_tensors of them, maybe none
  */
 lora_status lora_fork_sequences(int32_t *refs, int64_t n_pages, const int32_t *from_table, int64_t ld_from, int32_t B_from,
                                 int32_t *to_table, int64_t ld_to, int32_t B_to, int32_t n_table,
                                 const int32_t *parents, const int32_t *children, const int32_t *lengths,
                                 int32_t n_forks, int32_t page_size, int32_t *source, int32_t *target, int32_t *missing,
-                                void *workspace, size_t workspace_bytes, hipStream_t stream);
+                                const lora_paged_tensor *tensors, int32_t n_tensors, void *workspace,
+                                size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Give pages back: of each row listed, the entries from column
@@ -185,26 +195,16 @@ lora_status lora_release_pages(int32_t *refs, int64_t n_pages, int32_t *page_tab
 /*
  * Make the pages in use the lowest ones: with n_live of them, each page in use
  * whose number is n_live or more moves to a free one below it, both in ascending
- * order.  refs and page_table follow; what the pages hold is then copied with
- * lora_copy_pages(source, target, n_moves as its count).  Every entry that names
- * a page of the pool has to be in this table.
+ * order.  refs and page_table follow, and what the pages hold is copied in every
+ * tensor.  Every entry that names a page of the pool has to be in this table.
  *   source, target     [n_pages / 2] int32, written as far as there are moves
  *   n_live, n_moves    one int32 each, written
+ *   tensors            [host] n_tensors of them, maybe none
  */
 lora_status lora_compact_pages(int32_t *refs, int64_t n_pages, int32_t *page_table, int64_t ld_table, int32_t n_table,
                                int32_t B, int32_t *source, int32_t *target, int32_t *n_live, int32_t *n_moves,
-                               void *workspace, size_t workspace_bytes, hipStream_t stream);
-
-/* A tensor with pages: page p is n_outer x n_inner runs of `run` bytes, the
- * strides between them in bytes. */
-typedef struct {
-  void *data;
-  int64_t page, outer, inner;
-  int32_t n_outer, n_inner, run;
-} lora_paged_tensor;
-
-/* Tensors of one launch; more are taken in several. */
-#define LORA_COPY_TENSORS 64
+                               const lora_paged_tensor *tensors, int32_t n_tensors, void *workspace,
+                               size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Copy page source[i] to page target[i] in every tensor, i < n (or *count, if

@@ -173,11 +173,12 @@ def _reserve(**kw):
 
 def _fork(**kw):
     a = dict(POOL, from_=FAKE, ld_from=4, B_from=3, parents=FAKE, children=FAKE, lengths=FAKE, m=2, page=16, source=FAKE,
-             target=FAKE, missing=None, ws=FAKE, ws_bytes=1 << 30)
+             target=FAKE, missing=None, tensors=None, n_tensors=0, ws=FAKE, ws_bytes=1 << 30)
     a.update(kw)
     return C._lib().lora_fork_sequences(a["refs"], a["n"], a["from_"], a["ld_from"], a["B_from"], a["table"], a["ld"], a["B"],
                                         a["n_table"], a["parents"], a["children"], a["lengths"], a["m"], a["page"],
-                                        a["source"], a["target"], a["missing"], a["ws"], a["ws_bytes"], None)
+                                        a["source"], a["target"], a["missing"], a["tensors"], a["n_tensors"], a["ws"],
+                                        a["ws_bytes"], None)
 
 
 def _release(**kw):
@@ -187,9 +188,10 @@ def _release(**kw):
 
 
 def _compact(**kw):
-    a = dict(POOL, source=FAKE, target=FAKE, live=FAKE, moves=FAKE, ws=FAKE, ws_bytes=1 << 30)
+    a = dict(POOL, source=FAKE, target=FAKE, live=FAKE, moves=FAKE, tensors=None, n_tensors=0, ws=FAKE, ws_bytes=1 << 30)
     a.update(kw)
-    return C._lib().lora_compact_pages(*_pool(a), a["source"], a["target"], a["live"], a["moves"], a["ws"], a["ws_bytes"], None)
+    return C._lib().lora_compact_pages(*_pool(a), a["source"], a["target"], a["live"], a["moves"], a["tensors"],
+                                       a["n_tensors"], a["ws"], a["ws_bytes"], None)
 
 
 @pytest.mark.parametrize("call", [_reserve, _fork, _release, _compact])
@@ -213,7 +215,10 @@ def test_pool_workspaces_refused(call):
     (_fork, dict(lengths=None), BAD), (_fork, dict(source=None), BAD), (_fork, dict(target=None), BAD), (_fork, dict(page=0), BAD),
     (_release, dict(page=0), BAD), (_release, dict(m=-1), BAD), (_release, dict(m=65536), NOT),
     (_release, dict(rows=None, m=2), BAD), (_compact, dict(live=None), BAD), (_compact, dict(moves=None), BAD),
-    (_compact, dict(source=None), BAD), (_compact, dict(target=None), BAD)])
+    (_compact, dict(source=None), BAD), (_compact, dict(target=None), BAD), (_fork, dict(n_tensors=-1), BAD),
+    (_fork, dict(n_tensors=1), BAD), (_compact, dict(n_tensors=1), BAD),
+    (_compact, dict(n_tensors=1, tensors=C._TENSOR_FIELDS.pack(0, 16, 0, 0, 1, 1, 16)), BAD),
+    (_fork, dict(n_tensors=1, tensors=C._TENSOR_FIELDS.pack(FAKE, 16, 0, 0, 1, 0, 16)), BAD)])
 def test_pool_calls_refused(call, kw, status):
     assert call(**kw) == status
 
@@ -239,7 +244,7 @@ def _copy(tensors=None, **kw):
     (dict(n_tensors=-1), BAD), (dict(n=-1), BAD), (dict(n_pages=-1), BAD), (dict(n_pages=(1 << 28) + 1), BAD),
     (dict(data=None), BAD), (dict(n_outer=0), BAD), (dict(n_inner=0), BAD), (dict(run=0), BAD), (dict(page=-1), BAD),
     (dict(outer=-16), BAD), (dict(inner=-16), BAD), (dict(source=None), BAD), (dict(target=None), BAD),
-    (dict(n_outer=2 ** 31 - 1, n_inner=2 ** 31 - 1, run=2 ** 31 - 1), NOT)])
+    (dict(n_outer=2 ** 31 - 1, n_inner=2 ** 31 - 1, run=2 ** 31 - 1), NOT), (dict(n_outer=1 << 11, n_inner=1 << 10, run=1024), NOT)])
 def test_copy_refused(kw, status):
     assert _copy(**kw) == status and glsa.lib().lora_last_error()
 
