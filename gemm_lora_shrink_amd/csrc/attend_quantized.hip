@@ -116,6 +116,92 @@ template <int DP> struct Tile8 {
   }
 };
 
+// ---- the work of a workgroup ---------------------------------------------------
+
+// A unit is one (sequence, key/value head, tile of ROWS rows).  Where there are fewer
+// units than workgroups at once (p.cuts of them), the keys are cut by the lengths that
+// the sequences have, which the host does not know: into chunks of the least number
+// of stages (KEYS keys) with which all chunks of all units run at once, and of which
+// no sequence has more than p.splits.  Lane b of every wave counts for sequence b; a
+// scan over the lanes finds a workgroup's own chunk, and workgroup 0 leaves the
+// chunks' length for the join.  Against even chunks of the bounds: 195 -> 142 us for
+// 16 sequences of 256 to 8192 keys and 23 to 45 nodes (fp16, INT8), 42 -> 37 for one
+// node each, 55.5 -> 32 for 64 nodes over 4096 keys under a bound of 32768; where
+// lengths reach the bounds finding the chunk costs 63.7 -> 64.8 (64 nodes over 32768
+// keys) and 26.2 -> 27.3 (one node).
+// With more units than that, cutting the long ones loses (143 -> 166 us for 32
+// sequences of 128 to 4096 keys, 256 units): work_of's even chunks, most often one.
+constexpr int64_t kMinChunk = 256;
+constexpr int kCutSeqs = 64;  // sequences that this is done for: a lane each
+// Over a wave's lanes, by shifts and broadcasts of the vector unit: the sums of the
+// lanes up to each, the sum, the largest.
+#define LORA_WAVE_STEPS(OP)                                                 \
+  OP(0x111, 0xf) OP(0x112, 0xf) OP(0x114, 0xf) OP(0x118, 0xf) /* row_shr */ \
+      OP(0x142, 0xa) OP(0x143, 0xc)                           /* row_bcast */
+__device__ __forceinline__ int wave_scan(int x) {
+#define LORA_ADD(dpp, rows) x += __builtin_amdgcn_update_dpp(0, x, dpp, rows, 0xf, false);
+  LORA_WAVE_STEPS(LORA_ADD)
+#undef LORA_ADD
+  return x;
+}
+__device__ __forceinline__ uint32_t wave_sum(int x) { return (uint32_t)__builtin_amdgcn_readlane(wave_scan(x), 63); }
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+#define LORA_MAX(dpp, rows) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, dpp, rows, 0xf, false));
+  LORA_WAVE_STEPS(LORA_MAX)
+#undef LORA_MAX
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+#undef LORA_WAVE_STEPS
+__device__ __forceinline__ uint32_t up(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
+template <int ROWS, int KEYS> __device__ __forceinline__ Work work_by_lengths(const AttendQuantizedParams& p) {
+  Work w;
+  const int lane = threadIdx.x & 63;
+  int64_t start = 0;
+  int n = 0, ctx = 0;
+  if (lane < p.B) sequence_of(p, lane, start, n, ctx);
+  const int tiles = (int)(((uint32_t)n * p.group.d + ROWS - 1) / ROWS), per = tiles * p.hk;
+  const uint32_t stages = ((uint32_t)ctx + (uint32_t)n + KEYS - 1) / KEYS;
+  // ceil(x / c) lies between x / c and x / c + 1, so the sum of all chunks tells where
+  // to look: in one place where the units are few
+  const uint32_t longest = wave_max(per ? stages : 0), all = wave_sum(per * stages), units = wave_sum(per);
+  uint32_t lo = max((uint32_t)(kMinChunk + KEYS - 1) / KEYS, max(up(longest, p.splits), up(all, p.cuts)));
+  uint32_t hi = max(lo, min(longest, up(all, p.cuts - units)));
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (wave_sum(per * up(stages, mid)) <= (uint32_t)p.cuts) hi = mid;
+    else lo = mid + 1;
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  if (p.splits > 1 && blockIdx.x == 0 && threadIdx.x == 0) *chunk_of_parts(p) = lo * KEYS;
+  const int splits = max(1u, up(stages, lo)), mine = per * splits, ends = wave_scan(mine);
+  // neighbouring chunks on one XCD: they read the same pages
+  const int total = __builtin_amdgcn_readlane(ends, 63), of_xcd = (total + kXcds - 1) / kXcds;
+  const int j = (int)(blockIdx.x / kXcds), rank = (int)(blockIdx.x % kXcds) * of_xcd + j;
+  w.none = j >= of_xcd || rank >= total;
+  if (w.none) return w;
+  w.b = __builtin_ctzll(__ballot(ends > rank));
+  const auto of_b = [&](int x) { return __builtin_amdgcn_readlane(x, w.b); };
+  const uint32_t r = rank - of_b(ends - mine), nt = of_b(tiles), ns = of_b(splits);
+  w.start = (int64_t)(((uint64_t)(uint32_t)of_b((int)(start >> 32)) << 32) | (uint32_t)of_b((int)start));
+  w.n = of_b(n);
+  w.ctx = of_b(ctx);
+  const uint32_t u = __builtin_amdgcn_readfirstlane(r / nt);
+  w.h = __builtin_amdgcn_readfirstlane(u / ns);
+  w.split = (int)(u - w.h * ns);
+  w.row0 = (int)(r - u * nt) * ROWS;
+  w.rows = w.n * (int)p.group.d;
+  w.whole = ns == 1;
+  const int last = min(w.row0 + ROWS, w.rows) - 1;
+  const int end = w.ctx + (p.mask ? w.n : min(w.n, (int)p.group.div((uint32_t)last) + 1));
+  const int64_t k0 = (int64_t)w.split * lo * KEYS;
+  w.k0 = (int)k0;
+  w.k1 = (int)min(k0 + (int64_t)lo * KEYS, (int64_t)end);
+  return w;
+}
+template <int ROWS, bool SPREAD, int KEYS> __device__ __forceinline__ Work quantized_work(const AttendQuantizedParams& p) {
+  return p.cuts ? work_by_lengths<ROWS, KEYS>(p) : work_of<ROWS, SPREAD>(p);
+}
+
 // Up to 32 rows: four waves hold the same rows and take the chunk's tiles in turn,
 // each through LDS of its own: a wave waits for no other until their outputs meet
 // at the end.  Two tiles are in flight a wave (16 KB): after a tile's scores the keys
@@ -143,7 +229,7 @@ __global__ __launch_bounds__(256, Tile8<DP>::kGroups) void attend_narrow_quantiz
   __shared__ int s_id[NW][4][NI * 64];
   __shared__ float s_ml[NW][2][kBlock];
   warm_args(p);
-  const Work w = work_of<kBlock, true>(p);
+  const Work w = quantized_work<kBlock, true, 4 * Tile8<DP>::kKeys>(p);
   if (w.none) return;
   Block rb;
   rb.template init<true>(p, w, w.row0);
@@ -581,7 +667,7 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
   __shared__ __attribute__((aligned(kRing * kStage))) char s_kv[kRing][kStage];
   __shared__ __attribute__((aligned(16))) typename Stage::Shared s_stage;
   warm_args(p);
-  const Work w = work_of<32 * 8 / KG, false>(p);
+  const Work w = quantized_work<32 * 8 / KG, false, 64>(p);
   if (w.none) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int late = wave >> 2;  // the group that runs behind
@@ -756,7 +842,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_quantized_kernel(Atte
   const auto place = [&](int t) { return s_kv + (t & 1) * 2 * kTile; };
   __shared__ __attribute__((aligned(16))) typename Stage::Shared s_stage;
   warm_args(p);
-  const Work w = work_of<4 * kBlock, true>(p);
+  const Work w = quantized_work<4 * kBlock, true, 64>(p);
   if (w.none) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RowBlock<Elem, DP, Out, Tiles<Out>::NT> rb;
@@ -840,6 +926,7 @@ struct Plan {
   int64_t groups;  // workgroups to be had from cutting the keys
   int64_t unit;    // keys that a chunk is a multiple of
   int64_t grid;
+  int32_t cuts;    // chunks by the lengths, up to so many in all; 0: even chunks of the bounds
 };
 int padded(int32_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 Plan plan_kind(bool fp32, int32_t nodes, int32_t group, int32_t d) {
@@ -862,19 +949,29 @@ Plan plan_kind(bool fp32, int32_t nodes, int32_t group, int32_t d) {
   return a;
 }
 
-// How the keys are cut: even chunks, so long that about `groups` workgroups run in
-// all where every sequence is as long as its bound, and no shorter than kMinChunk:
-// as many workgroups as the chip holds at once (the wide kernel: two a compute
-// unit).  More cost their first loads and parts: 64 sequences of 4096 keys, 32 + 8
-// bf16 heads of 128, 92 us with 512 workgroups, 99 with 1024, 104 with 2048; one of
-// 32768: 27, 31 and 37.
-constexpr int64_t kMinChunk = 256;
+// How the keys are cut: by their lengths where a lane can count for each sequence,
+// else into even chunks, so long that about `groups` workgroups run in all where
+// every sequence is as long as its bound; no shorter than kMinChunk.  groups: as many
+// as the chip holds at once (the wide kernel: two a compute unit).  More cost their
+// first loads and parts: 64 sequences of 4096 keys, 32 + 8 bf16 heads of 128, 92 us
+// with 512 workgroups, 99 with 1024, 104 with 2048; one of 32768: 27, 31 and 37.
 constexpr int64_t kMaxChunk = (int64_t)1 << 30;
+
+// The most chunks of a sequence; even: if all are as long.  Where others may be short
+// a long one gets up to twice as many, at that many parts.
+int64_t most_cuts(int64_t B, int64_t even) { return B > 1 ? 2 * even : even; }
 
 Plan plan_of(bool fp32, int32_t B, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk, int32_t d) {
   Plan a = plan_kind(fp32, max_nodes, hq / hk, d);
   const int64_t keys = (int64_t)max_context + max_nodes;
   const int64_t units = (int64_t)B * hk * a.row_tiles;
+  if (B <= kCutSeqs && units < a.groups && units * ceil_div(keys, 64) < (int64_t)1 << 31) {  // (sums in 32 bits)
+    a.cuts = (int32_t)a.groups;
+    a.chunk = 1;
+    a.splits = (int32_t)std::min(ceil_div(keys, kMinChunk), most_cuts(B, ceil_div(a.groups, units)));
+    a.grid = a.groups;
+    return a;
+  }
   int64_t chunk = units < a.groups ? ceil_div(keys * units, a.groups) : keys;
   if (chunk < kMinChunk) chunk = kMinChunk;
   chunk = ceil_div(ceil_div(keys, ceil_div(keys, chunk)), a.unit) * a.unit;
@@ -911,6 +1008,8 @@ hipError_t launch(AttendQuantizedParams p, hipStream_t stream) {
   const Plan a = plan_of(sizeof(Out) == 4, p.B, p.max_nodes, p.max_context, p.hq, p.hk, p.d);
   p.chunk = a.chunk;
   p.splits = a.splits;
+  p.cuts = a.cuts;
+  if (a.cuts && a.splits > 1) p.part += kChunkBytes / 4;
   p.row_tiles = a.row_tiles;
   p.part_rows = part_rows_of(p.B, p.T, p.max_nodes);
   p.by_tiles = fast_div((uint32_t)a.row_tiles);
@@ -923,8 +1022,12 @@ hipError_t launch(AttendQuantizedParams p, hipStream_t stream) {
                        : dp == 128 ? launch_d<Out, F, 128>(p, a, stream)
                                    : launch_d<Out, F, 256>(p, a, stream);
   if (e != hipSuccess || p.splits == 1) return e;
-  hipLaunchKernelGGL(attend_join_kernel<Out>, dim3((unsigned)join_grid(p.max_nodes, p.hq), (unsigned)p.B), dim3(kThreads), 0,
-                     stream, static_cast<const AttendParams&>(p));
+  const dim3 g((unsigned)join_grid(p.max_nodes, p.hq), (unsigned)p.B);
+  if (p.cuts) {
+    hipLaunchKernelGGL((attend_join_kernel<Out, true>), g, dim3(kThreads), 0, stream, static_cast<const AttendParams&>(p));
+  } else {
+    hipLaunchKernelGGL((attend_join_kernel<Out, false>), g, dim3(kThreads), 0, stream, static_cast<const AttendParams&>(p));
+  }
   return hipGetLastError();
 }
 
@@ -939,16 +1042,17 @@ bool attend_quantized_fits(lora_dtype dt, int32_t B, int32_t max_nodes, int32_t 
 
 int64_t attend_quantized_need_bytes(lora_dtype dt, int32_t B, int32_t T, int32_t max_nodes, int32_t max_context,
                                     int32_t hq, int32_t hk, int32_t d) {
-  const int64_t splits = plan_of(dt == LORA_F32, B, max_nodes, max_context, hq, hk, d).splits;
-  return splits == 1 ? 0 : part_bytes(splits * part_rows_of(B, T, max_nodes), hq, d);
+  const Plan a = plan_of(dt == LORA_F32, B, max_nodes, max_context, hq, hk, d);
+  if (a.splits == 1) return 0;
+  return (a.cuts ? kChunkBytes : 0) + part_bytes(a.splits * (int64_t)part_rows_of(B, T, max_nodes), hq, d);
 }
 
 // Fewer sequences or nodes are cut into more chunks, so the bytes of a call do not
 // grow with its sizes; these are the most of any call up to them.  With G workgroups
 // to be had and u = sequences * kv_heads * row tiles a call has at most ceil(keys /
-// kMinChunk) and ceil(G / u) chunks (2^30 keys at most a chunk), both largest at the
-// most keys; rows only grow.  What is left is to try the numbers of sequences and,
-// of the nodes, those that fill their row tiles.
+// kMinChunk) and most_cuts of ceil(G / u) chunks (2^30 keys at most an even chunk),
+// both largest at the most keys; rows only grow.  What is left is to try the numbers
+// of sequences and, of the nodes, those that fill their row tiles.
 int64_t attend_quantized_most_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t hq, int32_t hk,
                                     int32_t d) {
   const int32_t group = hq / hk;
@@ -961,7 +1065,7 @@ int64_t attend_quantized_most_bytes(int32_t B, int32_t T, int32_t max_nodes, int
     const Plan a = plan_kind(fp32, (int32_t)nodes, group, d);
     const int64_t per = (int64_t)hk * a.row_tiles;
     for (int64_t b = 1; b <= B && b * per < a.groups; ++b) {
-      const int64_t splits = std::max(std::min(by_keys, ceil_div(a.groups, b * per)), uncut);
+      const int64_t splits = std::max(std::min(by_keys, most_cuts(b, ceil_div(a.groups, b * per))), uncut);
       if (splits > 1) most = std::max(most, splits * part_rows_of((int32_t)b, T, (int32_t)nodes));
     }
   };
@@ -974,7 +1078,7 @@ int64_t attend_quantized_most_bytes(int32_t B, int32_t T, int32_t max_nodes, int
     }
     nodes_up_to(fp32, max_nodes);
   }
-  return part_bytes(most, hq, d);
+  return most ? kChunkBytes + part_bytes(most, hq, d) : 0;
 }
 
 template <typename Out> static hipError_t launch_format(int format, const AttendQuantizedParams& p, hipStream_t stream) {

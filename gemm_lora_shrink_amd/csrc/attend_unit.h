@@ -176,6 +176,9 @@ __device__ inline void sequence_of(const AttendParams& p, int b, int64_t& start,
   const int x = p.context[b];
   ctx = x < 0 ? 0 : (x > p.max_context ? p.max_context : x);
 }
+// Where a kernel that finds its chunks' length leaves it: kChunkBytes before the parts.
+constexpr int64_t kChunkBytes = 256;
+__device__ inline int* chunk_of_parts(const AttendParams& p) { return reinterpret_cast<int*>(p.part) - kChunkBytes / 4; }
 __device__ inline int splits_of(const AttendParams& p, int n, int ctx) {
   const int last = ctx + n - 1;
   return last < 0 ? 1 : (int)p.by_chunk.div((uint32_t)last) + 1;
@@ -781,7 +784,8 @@ __device__ __forceinline__ const char* piece_of(const AttendParams& p, const cha
 
 // Join a row's chunks, in their order: one wave a row, 4 elements a lane, the
 // lanes left over by a short head taking every second (fourth, ..) chunk.
-template <typename Elem>
+// FOUND: the chunks' length is the device's (chunk_of_parts).
+template <typename Elem, bool FOUND = false>
 __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendParams p) {
   warm_args(p);
   // grid: (rows of the longest sequence * heads / 4, sequences)
@@ -791,7 +795,7 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendParams p) {
   sequence_of(p, b, start, n, ctx);
   const int r = (int)blockIdx.x * (kThreads / 64) + (int)(threadIdx.x >> 6);
   const int i = r / p.hq, h = r - i * p.hq;
-  const int splits = splits_of(p, n, ctx);
+  const int splits = FOUND ? (int)(((uint32_t)max(ctx + n, 1) - 1) / (uint32_t)*chunk_of_parts(p)) + 1 : splits_of(p, n, ctx);
   if (i >= n || splits == 1) return;  // one chunk: its workgroup wrote the output
   const int64_t row = start + i, of = part_row(p, b, start, i);
   const int lane = threadIdx.x & 63;

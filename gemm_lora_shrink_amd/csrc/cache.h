@@ -107,6 +107,7 @@ struct AttendQuantizedParams : AttendParams {
   const int8_t *k_exp, *v_exp;
   int64_t k_exp_page, k_exp_head, v_exp_page, v_exp_head;
   FastDiv block;  // by the rows of a block
+  int cuts;       // chunks to be had where they are cut by the sequences' lengths, else 0
 };
 
 struct PoolParams {

@@ -313,6 +313,40 @@ def test_attention(case, dt, fmt):
     s.check(what=f"{contexts} {counts}")
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_many_units(dt, fmt):
+    """More sequences than chunks are cut for by their lengths, and chains of several row tiles with units enough."""
+    rng = np.random.default_rng(0)
+    contexts = rng.integers(0, 300, 300)
+    contexts[17] = 1500
+    s = Step(contexts.tolist(), [1 + b % 2 for b in range(300)], 2, 1, 64, dt, fmt, tree=False, block=8)
+    s.poison_unused()
+    s.check(what="many sequences")
+    s = Step([0, 100, 33, 5, 0, 64, 1, 9], [70, 64, 5, 66, 80, 1, 0, 90], 64, 16, 64, dt, fmt, tree=False)
+    s.poison_unused()
+    s.check(what="long chains")
+
+
+@pytest.mark.parametrize("ctx", [None, 9000, 1000000])
+@pytest.mark.parametrize("counts", [[1] * 6, [9, 40, 2, 17, 33, 0], [70, 64, 1, 90, 3, 80]])
+def test_chunks_of_unlike_lengths(counts, ctx):
+    """Sequences of many chunks next to ones of one and of none, under bounds that they reach or stay far below."""
+    s = Step([5000, 3, 700, 64, 0, 2100], counts, 8, 2, 64, "bf16", "e4m3", block=4)
+    s.poison_unused()
+    s.check(**({} if ctx is None else dict(max_context=ctx)))
+
+
+@pytest.mark.parametrize("B", [63, 64, 65])
+def test_chunks_of_many_sequences(B):
+    rng = np.random.default_rng(B)
+    contexts, counts = rng.integers(0, 80, B), rng.integers(0, 3, B)
+    contexts[B - 1], counts[B - 1], counts[0] = 3000, 2, 0
+    s = Step(contexts.tolist(), counts.tolist(), 4, 1, 64, "f16", "int8", tree=False)
+    s.poison_unused()
+    s.check(max_context=5000)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 def test_scores_far_apart(dt):
     """Large queries: one key takes all, sums stay exact enough; and negative or no scale."""
