@@ -406,7 +406,7 @@ LORA_EXPORT lora_status lora_release_pages(int32_t* refs, int64_t n_pages, int32
   if (page_size < 1) return fail(LORA_ERR_INVALID_ARG, "page_size = %d must be >= 1", page_size);
   if (n < 0) return fail(LORA_ERR_INVALID_ARG, "n = %d is negative", n);
   if (n > 65535) return fail(LORA_ERR_UNSUPPORTED, "n = %d exceeds 65535", n);
-  if (!rows && n != B) return fail(LORA_ERR_INVALID_ARG, "n = %d must be B = %d where no rows are listed", n, B);
+  if (!rows && n != 0 && n != B) return fail(LORA_ERR_INVALID_ARG, "n = %d must be B = %d where no rows are listed", n, B);
   if (n == 0 || n_table == 0) return LORA_OK;
   const PoolParams p = pool_of(refs, n_pages, page_table, ld_table, n_table, B, page_size, nullptr);
   const hipError_t e = launch_release(p, rows, keep, n, stream);

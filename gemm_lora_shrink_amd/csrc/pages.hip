@@ -450,9 +450,9 @@ dim3 rows4(int64_t rows) { return dim3((unsigned)ceil_div(rows, kThreads / 64));
 int64_t pages_scratch_bytes(int64_t n_pages, int32_t n_seqs) { return 4 * (n_pages + (int64_t)n_seqs + 1); }
 
 hipError_t launch_reserve(const PoolParams& p, const int32_t* lengths, int32_t* missing, hipStream_t stream) {
-  hipLaunchKernelGGL(count_missing_kernel, rows4(p.B), dim3(kThreads), 0, stream, p, lengths);
+  if (p.B > 0) hipLaunchKernelGGL(count_missing_kernel, rows4(p.B), dim3(kThreads), 0, stream, p, lengths);
   hipLaunchKernelGGL(take_pages_kernel, dim3(1), dim3(kOne), 0, stream, p, missing);
-  hipLaunchKernelGGL(hand_out_kernel, rows4(p.B), dim3(kThreads), 0, stream, p, lengths);
+  if (p.B > 0) hipLaunchKernelGGL(hand_out_kernel, rows4(p.B), dim3(kThreads), 0, stream, p, lengths);
   return hipGetLastError();
 }
 

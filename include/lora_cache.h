@@ -131,6 +131,10 @@ lora_status lora_keep_path_quantized(const lora_quantized_cache *cache, void *co
  * or move pages need a workspace of lora_pages_workspace_bytes (4-byte aligned,
  * no clearing, nothing kept in it; calls that may overlap need distinct ones).
  * Calls on one pool have to follow one another.
+ *
+ * A page that several sequences hold is not to be written.  Forks see to that:
+ * what follows a sequence's tokens lies on a page of its own.  A sequence that
+ * goes back to a length inside a page that it shares is forked at that length.
  */
 #define LORA_MAX_POOL_PAGES (1 << 28)
 size_t lora_pages_workspace_bytes(int64_t n_pages, int32_t n_seqs);

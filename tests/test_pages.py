@@ -296,3 +296,54 @@ def test_forked_sequences_attend_as_copies_do():
     glsa.release_pages(refs, table, ints([0, 2]))
     glsa.release_pages(refs, table, ints([1, 3]), keep=ints([10, 0]), page_size=page)
     assert int(refs.sum()) == 1 and int((table >= 0).sum()) == 1
+
+
+def test_calls_of_nothing():
+    """No sequences, no forks, no rows, no columns and an empty pool: nothing but the counts is written."""
+    refs, table, none, missing = ints([0, 2, 0, 1]), ints([[1, 3], [1, -1]]), ints([]), ints([7])
+    was = refs.clone(), table.clone()
+    for t in (torch.empty(0, 5, dtype=torch.int32, device="cuda"), torch.empty(3, 0, dtype=torch.int32, device="cuda")):
+        missing.fill_(7)
+        glsa.reserve_pages(refs, t, torch.full((t.size(0),), 9, dtype=torch.int32, device="cuda"), page_size=4, missing=missing)
+        assert int(missing) == 0
+        glsa.release_pages(refs, t)
+    missing.fill_(7)
+    glsa.fork_sequences(refs, table, none, none, none, page_size=4, missing=missing)
+    glsa.release_pages(refs, table, none)
+    assert int(missing) == 0 and torch.equal(refs, was[0]) and torch.equal(table, was[1])
+    missing.fill_(7)
+    held = torch.full((2, 3), -1, dtype=torch.int32, device="cuda")
+    glsa.reserve_pages(none, held, ints([1, 9]), page_size=4, missing=missing)
+    assert int(missing) == 4 and bool((held == -1).all())
+    assert int(glsa.compact_pages(none, held)) == 0
+
+
+def test_calls_on_another_stream():
+    """The calls follow the work of the stream that they are given, workspaces made within them too."""
+    pool, s = Pool([70, 33, 0, 129], 16, 60), torch.cuda.Stream()
+    refs, table = pool.on_gpu()
+    tensors = pool.tensors()
+    want_refs, want_table = refs.clone(), table.clone()
+    want = [t.clone() for t in tensors]
+    lengths, forks = ints([80, 40, 20, 130]), [ints(x) for x in ([0, 3], [2, 1], [37, 100])]
+
+    def calls(refs, table, tensors, **kw):
+        glsa.release_pages(refs, table, forks[1], **kw)
+        glsa.fork_sequences(refs, table, *forks, page_size=16, tensors=tensors, **kw)
+        glsa.reserve_pages(refs, table, lengths, page_size=16, **kw)
+        return glsa.compact_pages(refs, table, tensors=tensors, **kw)
+
+    live = int(calls(want_refs, want_table, want))
+    torch.cuda.synchronize()
+    late = refs.clone().zero_(), table.clone().fill_(-1)
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        late[0].copy_(refs)
+        late[1].copy_(table)
+    got = calls(*late, tensors, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert int(got) == live and torch.equal(late[0], want_refs) and torch.equal(late[1], want_table)
+    held = sorted(set(want_table[want_table >= 0].tolist()))
+    for a, b in zip(tensors, want):
+        assert np.array_equal(raw(a)[held], raw(b)[held])

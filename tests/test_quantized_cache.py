@@ -529,6 +529,30 @@ def test_keep(case, fmt):
         equal(c, w, ~dead)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("n_path,block", [(64, 16), (65, 4), (100, 16), (200, 1)])
+def test_keep_long_paths(n_path, block, fmt):
+    g, rng = torch.Generator("cuda").manual_seed(n_path), np.random.default_rng(n_path)
+    contexts, nodes, page, B = [5, 64, 0], 260, 16, 3
+    path = np.stack([np.sort(rng.choice(nodes, n_path, replace=False)) for _ in range(B)]).astype(np.int32)
+    path[1, :30] = np.arange(30)      # the first nodes stay where they are
+    path[1, 30:] = np.sort(rng.choice(np.arange(30, nodes), n_path - 30, replace=False))
+    path[2, 50] = path[2, 49]         # ends there
+    kept = [n_path, n_path - 1, n_path]
+    per = -(-(max(contexts) + nodes) // page)
+    table = rng.permutation(B * per + 1)[:B * per].reshape(B, per).astype(np.int32)
+    table[0, 3] = -1
+    cache = made(B * per + 1, 3, page, 48, fmt, block, g, False, spread=4)
+    want = co.keep(on_host(cache), table, contexts, path, kept)
+    live = np.zeros((B * per + 1, page), bool)
+    for b in range(B):
+        for pos in range(contexts[b] + (50 if b == 2 else kept[b])):
+            if table[b][pos // page] >= 0:
+                live[table[b][pos // page], pos % page] = True
+    glsa.keep_path_quantized([cache], ints(table), ints(contexts), ints(path), ints(kept))
+    equal(cache, want, live)
+
+
 def test_keep_with_missing_pages_and_many_layers():
     g = torch.Generator("cuda").manual_seed(0)
     caches = [made(8, 2, 8, 32, "int8", 8, g, spread=4) for _ in range(70)]  # more than a launch takes
@@ -599,3 +623,36 @@ def test_calls_on_another_stream():
     glsa.tree_attention_quantized(*args, out=out, lse=lse, stream=side, **more)
     side.synchronize()
     assert np.array_equal(f64(out).reshape(want.shape), want) and np.array_equal(f64(lse), want_lse)
+
+
+@pytest.mark.parametrize("nodes", [1, 40])
+def test_replays_follow_the_lengths(nodes):
+    """Two graphs, each with a workspace of its own, replayed with contexts and nodes that change between: every
+    replay cuts the keys anew, as the eager call does."""
+    s = Step([900, 3000, 31, 0], [nodes, nodes, min(nodes, 9), 1], 8, 2, 64, "f16", "int8", tree=False)
+    table, context, q_start = ints(s.table), ints(s.context), ints(s.q_start)
+    outs = [torch.zeros_like(s.q) for _ in range(3)]
+    spaces = [s.workspace(nodes, 3000) for _ in range(3)]
+
+    def call(i):
+        glsa.tree_attention_quantized(s.q, s.cache, table, context, q_start, max_nodes=nodes, max_context=3000, out=outs[i],
+                                      workspace=spaces[i])
+
+    call(2)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            call(i)
+    for contexts, counts in (([900, 3000, 31, 0], [nodes, nodes, min(nodes, 9), 1]), ([3, 1, 0, 7], [1, 0, 1, 0]),
+                             ([0, 0, 3000, 2999], [0, nodes, 1, nodes]), ([0] * 4, [0] * 4), ([64, 700, 1, 1], [1, 1, nodes, 0])):
+        context.copy_(ints(contexts))
+        q_start.copy_(ints(np.concatenate([[0], np.cumsum(counts)])))
+        for o in outs:
+            o.fill_(5)
+        call(2)
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
+        assert bool((outs[2][sum(counts):] == 5).all()) and not bool((outs[2][:sum(counts)] == 5).all(1).any())
