@@ -3,6 +3,7 @@ the header declares, sizes of workspaces, and bad arguments are rejected on the
 host before anything reaches the GPU."""
 
 import os
+import random
 import re
 
 import pytest
@@ -315,3 +316,20 @@ def test_runs_of_a_page():
     for bad in (torch.zeros(2, 2, 4, 4, 8)[:, :, :3, :3, :4], torch.zeros(2, 1, 4).expand(2, 3, 4)):
         with pytest.raises(glsa.LoraError):
             C._runs(bad)
+
+
+@pytest.mark.skipif(os.path.exists("/dev/kfd"), reason="the calls pass the checks and would reach the GPU")
+def test_a_workspace_suffices_for_every_smaller_call():
+    """No call within the sizes asked for is refused for its workspace, whatever its type and number of chunks."""
+    rng = random.Random(0)
+    for hq, hk, d, B, T, nodes, ctx in ((32, 8, 128, 70, 400, 48, 20000), (8, 8, 64, 5, 9, 9, 100000), (16, 1, 256, 24, 24, 70, 3000),
+                                        (4, 2, 80, 300, 900, 33, 9000), (2, 1, 16, 600, 600, 1, 700000)):
+        most = glsa.quantized_workspace_bytes(B, T, nodes, ctx, hq, hk, d)
+        cache = _cache(k_head=16 * d, k_row=d, v_head=16 * d, v_row=d, k_page=16 * hk * d, v_page=16 * hk * d, page_size=16,
+                       block=16, k_exp_page=hk, k_exp_head=1, v_exp_page=hk, v_exp_head=1)
+        n_table = -(-(ctx + nodes) // 16)
+        for _ in range(200):
+            b, n, c, t = rng.randint(1, B), rng.randint(1, nodes), rng.choice([ctx, rng.randint(0, ctx)]), rng.randint(1, T)
+            status = _attend(cache, dt=rng.randint(0, 2), T=t, B=b, hq=hq, hk=hk, d=d, ldq=hq * d, ldo=hq * d, ld=n_table,
+                             n_table=n_table, nodes=n, ctx=c, ws_bytes=most)
+            assert status not in (BAD, NOT), (b, n, c, t, C._lib().lora_last_error())

@@ -28,3 +28,13 @@ def test_tree_step_matches_single_tokens(norm):
     off = float((tree - single).abs().max())
     assert off <= 2 * 2 * 4 * 512 * 2.0 ** -24 * float(single.abs().max()), off
     assert float((tree[0] - tree[1]).abs().max()) > 0.1  # different tokens do come out different
+
+
+@pytest.mark.parametrize("held", [torch.float8_e4m3fn, torch.int8])
+def test_tree_step_runs_over_a_quantized_cache(held):
+    """The two runs store the tokens in other steps, so their bytes may differ by a rounding: only that both run."""
+    import tree_step
+
+    tree, single = tree_step.run(torch.bfloat16, False, held)
+    assert tree.shape == single.shape == (8, tree_step.HIDDEN)
+    assert bool(torch.isfinite(tree).all()) and bool(torch.isfinite(single).all())
