@@ -22,7 +22,7 @@ of float8_e4m3fn or int8 with unit inner stride, exponents int8 [n_pages,
 kv_heads, blocks of a page].  The page calls go by refs (int32 [n_pages], how
 many table entries name a page; 0: free) and a page table (int32 [B, pages], -1
 where a sequence holds none), both on the GPU, so that a step can be captured
-with them.
+with them.  The GPU of the tensors has to be the current one.
 """
 
 import ctypes
@@ -32,11 +32,19 @@ from typing import NamedTuple
 import torch
 
 from . import _DTYPES, _check, _load
-from .attention import _I32, _I64, _F32, _U8, MAX_HEAD_DIM, _bad, _gpu, _i32, _int_rows, _made, _matrix, _stream_of, _vector
+from .attention import _I32, _I64, _F32, _U8, MAX_HEAD_DIM, _bad, _gpu, _i32, _int_rows, _made, _matrix, _vector
 
 CACHE_FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}
 MAX_KEEP_LAYERS = 128
 _I8 = torch.int8
+
+
+def _stream_of(stream, dev):
+    """The stream's handle: `stream`, or the current one.  The default stream has the same handle on every GPU, so a
+    call for another GPU than the current one would run on the wrong card."""
+    if torch._C._cuda_getDevice() != dev:
+        raise _bad(f"the tensors are on GPU {dev}, which is not the current one")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 class QuantizedCache(NamedTuple):
@@ -224,7 +232,7 @@ def tree_attention_quantized(q, cache, page_table, context, q_start, *, max_node
 
 def keep_path_quantized(caches, page_table, context, path, n_kept, *, stream=None):
     """keep_path over the layers' quantized caches, alike in shapes, strides and
-    type (a list of them, any number).  A row that moves into a block of a
+    type (a list of them, any number, none of them twice).  A row that moves into a block of a
     larger exponent is rounded again."""
     n = len(caches)
     if n < 1:
@@ -243,6 +251,8 @@ def keep_path_quantized(caches, page_table, context, path, n_kept, *, stream=Non
                     not x.is_contiguous() if dense else x.stride() != stride):
                 raise _bad("the layers' caches must be alike in shape, strides, type and GPU")
         at.append([x.data_ptr() for x in t])
+    if len({*at[0], *at[1]}) != 2 * n:
+        raise _bad("a cache is listed twice")  # its rows would move twice at once
     B = _i32(context.numel(), "the number of sequences")
     table = _int_rows(page_table, "page_table", dev, B)
     steps = _int_rows(path, "path", dev, B)

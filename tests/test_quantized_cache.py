@@ -656,3 +656,37 @@ def test_replays_follow_the_lengths(nodes):
         torch.cuda.synchronize()
         assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
         assert bool((outs[2][sum(counts):] == 5).all()) and not bool((outs[2][:sum(counts)] == 5).all(1).any())
+
+
+def test_a_cache_listed_twice_is_refused():
+    g = torch.Generator("cuda").manual_seed(0)
+    a, b = (made(4, 2, 8, 32, "int8", 8, g) for _ in range(2))
+    was = [t.clone() for t in (*a, *b)]
+    args = ints([[0, 1], [2, 3]]), ints([7, 3]), ints([[2, 4], [1, 3]]), ints([2, 2])
+    for caches in ([a, b, a], [a, (b[0], a[1], b[2], b[3])]):
+        with pytest.raises(glsa.LoraError):
+            glsa.keep_path_quantized(caches, *args)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip((*a, *b), was))
+
+
+def test_another_gpu_than_the_current_one_is_refused(monkeypatch):
+    s = Step([9, 3], [1, 1], 4, 2, 64, "bf16", "e4m3", tree=False)
+    table, context, q_start = ints(s.table), ints(s.context), ints(s.q_start)
+    kv, rows, refs = torch.zeros(2, 128, device="cuda", dtype=torch.bfloat16), ints([0, 16]), ints([0] * s.n_pages)
+    out, ws = torch.full_like(s.q, 3), s.workspace()
+    was = [t.clone() for t in s.cache]
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: s.q.get_device() + 1)
+    calls = (lambda: glsa.store_quantized(kv, kv, s.cache, rows),
+             lambda: glsa.tree_attention_quantized(s.q, s.cache, table, context, q_start, max_nodes=1, max_context=9, out=out,
+                                                   workspace=ws),
+             lambda: glsa.keep_path_quantized([s.cache], table, context, rows.view(2, 1), rows),
+             lambda: glsa.copy_pages(list(s.cache), rows, rows), lambda: glsa.reserve_pages(refs, table, context, page_size=16),
+             lambda: glsa.fork_sequences(refs, table, rows, rows, rows, page_size=16),
+             lambda: glsa.release_pages(refs, table), lambda: glsa.compact_pages(refs, table))
+    for call in calls:
+        with pytest.raises(glsa.LoraError, match="not the current one"):
+            call()
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert bool((out == 3).all()) and all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(s.cache, was))
