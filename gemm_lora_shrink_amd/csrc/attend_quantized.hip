@@ -833,8 +833,8 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
 // The heads that leave the kernel above no registers: four waves of 32 rows share
 // stages of 32 keys, double buffered.  A stage's bytes are in registers during the
 // stage before it and converted into the other place at its end.  4 sequences of 8192
-// keys and 32 nodes, 16 + 4 bf16 heads of 256, e4m3: 124 us; its output and query fill
-// the registers, and up to 94 more (bf16), 115 (fp16) and 227 (fp32) are spilled.
+// keys and 32 nodes, 16 + 4 bf16 heads of 256, e4m3: 84 us;
+// the output and the query fill the registers, fp32 ones spill 84 (INT8) to 114.
 template <typename Out, typename F, int DP>
 __global__ __launch_bounds__(kThreads, 1) void attend_wide_quantized_kernel(AttendQuantizedParams p) {
   using Elem = typename Tiles<Out>::Elem;
@@ -887,11 +887,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_quantized_kernel(Atte
       const uint32_t valid =
           __builtin_amdgcn_readfirstlane(*reinterpret_cast<const uint32_t*>(s_stage.valid[t % Stage::kRing]));
       uint32_t seen[1] = {valid};
-      bool uneven = false;
-      if constexpr (kTail) {
-        seen[0] &= rb.sees(p, w, (int)first_key(t));
-        uneven = __any(seen[0] != valid);
-      }
+      if constexpr (kTail) seen[0] &= rb.sees(p, w, (int)first_key(t));
       if constexpr (Stage::kFactors) {
         const uint32_t at = (uint32_t)(uintptr_t)s_stage.factors[t % Stage::kRing];
         rb.weigh_scaled(s, seen, at, at + 4 * KT, at + 8 * KT);
@@ -900,9 +896,12 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_quantized_kernel(Atte
         rb.weigh(s, c);
       }
       const char* vb = place(t) + kTile;
-      if (kTail && F::kHasNan && uneven && rb.any_odd(vb, KT)) {
-        rb.template add_values<kTail, 0>(rb.pack(s[0]));
-        rb.add_odd(vb, seen[0]);
+      // One form of the products a loop: choosing between two by what a tile holds, as the
+      // kernel above does, left 94 registers in memory (124 us for 84 at 4 x 32 nodes over
+      // 8224 keys of 16 + 4 bf16 heads of 256).
+      if constexpr (kTail && F::kHasNan) {
+        rb.template add_values<true, 0>(rb.pack(s[0]));
+        if (rb.any_odd(vb, KT)) rb.add_odd(vb, seen[0]);
       } else {
         rb.template add_values<false, 0>(rb.pack(s[0]));
       }
