@@ -11,6 +11,7 @@
 
 #include "attend_unit.h"
 #include "cache.h"
+#include "stage_order.h"
 
 namespace lora {
 
@@ -544,14 +545,13 @@ template <typename Elem, typename F, int DP, int KT> struct Staging {
   static constexpr bool kFactors = Traits<Elem>::kDtype == LORA_F16;
   static constexpr int kWaves = KT / 8, kPieces = DP / 16;  // pieces: of a row of bytes
   static constexpr int NP = kPieces < 8 ? 1 : kPieces / 4;  // pieces of a lane: of K, then of V (DP = 64: of either)
-  static constexpr int kRing = 8;  // stages that valid[] and factors[] hold
   // in LDS
   struct Shared {
     const char* row[kWaves][64];
     int id[kWaves][64], exponent[kWaves][64];
     float scale[kWaves][2][kFactors ? 1 : 64];
-    float factors[kRing][kFactors ? 3 * KT : 1];
-    __attribute__((aligned(8))) uint8_t valid[kRing][kWaves];
+    float factors[kFactorRing][kFactors ? 3 * KT : 1];
+    __attribute__((aligned(8))) uint8_t valid[kValidRing][kWaves];
   };
   Shared* sh;
   int wave, lane;
@@ -586,13 +586,13 @@ template <typename Elem, typename F, int DP, int KT> struct Staging {
     byte_to_lds(ok ? reinterpret_cast<const char*>(e.at((uint32_t)id, p.block.div((uint32_t)a.place))) : none,
                 (uint32_t)(uintptr_t)sh->exponent[wave]);
     const uint64_t all = __ballot(ok);
-    if ((lane & 15) == 0) sh->valid[(four * 4 + (lane >> 4)) % kRing][wave] = (uint8_t)(all >> lane);
+    if ((lane & 15) == 0) sh->valid[(four * 4 + (lane >> 4)) % kValidRing][wave] = (uint8_t)(all >> lane);
   }
   template <int NEWER> __device__ __forceinline__ void settle(int four, float c) {
     wait_loads<NEWER>();
     const int e = exponent_of<F>((int8_t)sh->exponent[wave][lane]);
     if constexpr (kFactors) {
-      float* f = sh->factors[(four * 4 + (lane >> 4)) % kRing] + wave * 8 + (lane & 7);
+      float* f = sh->factors[(four * 4 + (lane >> 4)) % kFactorRing] + wave * 8 + (lane & 7);
       if ((lane >> 3) & 1) {
         // Smaller exponents than -60 are taken for it: what they stand for is far below
         // the smallest fp16 output either way, and the last factor stays finite in sums.
@@ -665,7 +665,7 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
   using R = Rows<Elem, DP>;
   using Block = RowBlock<Elem, DP, Out, Tiles<Out>::NT>;
   using Stage = Staging<Elem, F, DP, 64>;
-  constexpr int KT = 64, NS = 2 / KG, kRing = 4;
+  constexpr int KT = 64, NS = 2 / KG, kRing = kTurnsRing;
   constexpr int kTile = KT * R::kBytes, kStage = 2 * kTile;
   // (aligned to its size, so that an XOR changes stages)
   __shared__ __attribute__((aligned(kRing * kStage))) char s_kv[kRing][kStage];
@@ -721,7 +721,7 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
   };
   auto soften = [&](int t, auto tail) __attribute__((always_inline)) {
     if (idle) return;
-    const uint64_t at_all = *reinterpret_cast<const uint64_t*>(s_stage.valid[t % Stage::kRing]);
+    const uint64_t at_all = *reinterpret_cast<const uint64_t*>(s_stage.valid[t % kValidRing]);
     const uint64_t all = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at_all >> 32)) << 32) |
                          (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at_all);
     bool uneven = false;
@@ -736,7 +736,7 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
       if (!Stage::kFactors && __any(seen[b] != ~0u)) rb.mask_scores(s[b], seen[b]);
     }
     if constexpr (Stage::kFactors) {
-      const uint32_t at = (uint32_t)(uintptr_t)s_stage.factors[t % Stage::kRing] + 4 * part * kBlock;
+      const uint32_t at = (uint32_t)(uintptr_t)s_stage.factors[t % kFactorRing] + 4 * part * kBlock;
       rb.weigh_scaled(s, seen, at, at + 4 * KT, at + 8 * KT);
     } else {
       rb.weigh(s, c);
@@ -756,9 +756,9 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
       if (t + 3 < nt) {
         stage.load(p, t + 3);
         // the rows of stages 4 k + 4 .. 4 k + 7 in step 4 k, once those of the four before are on their way
-        if ((t & 3) == 0) stage.template find<Stage::NP>(p, w, (t >> 2) + 1);
-        if ((t & 3) == 1) stage.template settle<Stage::NP>((t >> 2) + 1, c);
-        if ((t & 3) == 2) stage.ask(p, w, (t >> 2) + 2);
+        if ((t & 3) == kTurnsFind) stage.template find<Stage::NP>(p, w, (t >> 2) + 1);
+        if ((t & 3) == kTurnsSettle) stage.template settle<Stage::NP>((t >> 2) + 1, c);
+        if ((t & 3) == kTurnsAsk) stage.ask(p, w, (t >> 2) + 2);
       }
     }
   };
@@ -845,7 +845,8 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_quantized_kernel(Atte
   constexpr int kLds = kTile < kStoreBytes<DP> ? 4 * kStoreBytes<DP> : 4 * kTile;
   // (aligned to its two stages, so that an XOR changes them)
   __shared__ __attribute__((aligned(4 * kTile))) char s_kv[kLds];
-  const auto place = [&](int t) { return s_kv + (t & 1) * 2 * kTile; };
+  const auto place = [&](int t) { return s_kv + t % kWideRing * 2 * kTile; };
+  static_assert(kWideRing == 2, "an XOR changes places");
   __shared__ __attribute__((aligned(16))) typename Stage::Shared s_stage;
   warm_args(p);
   const Work w = quantized_work<4 * kBlock, true, 64>(p);
@@ -877,19 +878,19 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_quantized_kernel(Atte
       if (t + 2 < nt) {
         stage.load(p, t + 2);
         // the rows of stages 4 k + 4 .. 4 k + 7 in step 4 k + 1, once those of the four before are on their way
-        if ((t & 3) == 1) stage.template find<Stage::NP>(p, w, (t >> 2) + 1);
-        if ((t & 3) == 2) stage.template settle<Stage::NP>((t >> 2) + 1, c);
-        if ((t & 3) == 3) stage.ask(p, w, (t >> 2) + 2);
+        if ((t & 3) == kWideFind) stage.template find<Stage::NP>(p, w, (t >> 2) + 1);
+        if ((t & 3) == kWideSettle) stage.template settle<Stage::NP>((t >> 2) + 1, c);
+        if ((t & 3) == kWideAsk) stage.ask(p, w, (t >> 2) + 2);
       }
     }
     if (!idle) {
       f32x16 s[1] = {rb.template scores<0>()};
       const uint32_t valid =
-          __builtin_amdgcn_readfirstlane(*reinterpret_cast<const uint32_t*>(s_stage.valid[t % Stage::kRing]));
+          __builtin_amdgcn_readfirstlane(*reinterpret_cast<const uint32_t*>(s_stage.valid[t % kValidRing]));
       uint32_t seen[1] = {valid};
       if constexpr (kTail) seen[0] &= rb.sees(p, w, (int)first_key(t));
       if constexpr (Stage::kFactors) {
-        const uint32_t at = (uint32_t)(uintptr_t)s_stage.factors[t % Stage::kRing];
+        const uint32_t at = (uint32_t)(uintptr_t)s_stage.factors[t % kFactorRing];
         rb.weigh_scaled(s, seen, at, at + 4 * KT, at + 8 * KT);
       } else {
         if (__any(seen[0] != ~0u)) rb.mask_scores(s[0], seen[0]);
