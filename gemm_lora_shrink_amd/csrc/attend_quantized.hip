@@ -68,6 +68,14 @@ template <> struct Tiles<half_t> {
   static constexpr int NT = 1;
 };
 
+// A product of a weight (up to 2^8), a byte's number (below 2^9) and a power of two
+// of up to 2^kRoom stays finite in sums of 2^31 of them.  Where a value has a larger
+// one (up to 2^121), m is kept kRaise above the scores of its tile, and the weights so
+// much lower.  Finding how far each tile needs cost a branch a tile: 66.2 us for
+// 65.0 on 64 nodes over 32768 keys.
+constexpr int kRoom = 72;
+constexpr float kRaise = 49.f;
+
 // A byte to a dword of LDS for each lane.
 __device__ inline void byte_to_lds(const char* g, uint32_t lds) {
   lds = __builtin_amdgcn_readfirstlane(lds);
@@ -354,12 +362,18 @@ __global__ __launch_bounds__(256, Tile8<DP>::kGroups) void attend_narrow_quantiz
       }
     }
     // the exponents (bf16 keys: the values') become factors
+    bool over = false;  // a value's exponent is over kRoom
 #pragma unroll
     for (int i = 0; i < (KT >= 64 ? 2 * KT / 64 : 1); ++i) {
       if (!kScores && KT >= 64 && i < KT / 64) continue;
-      int* e = &s_exp[wave][t & 1][64 * i + lane];
-      if (kScores || KT >= 64 || hi) *reinterpret_cast<float*>(e) = power_of_two(exponent_of<F>((int8_t)*e));
+      int* at = &s_exp[wave][t & 1][64 * i + lane];
+      if (kScores || KT >= 64 || hi) {
+        const int e = exponent_of<F>((int8_t)*at);
+        if (KT >= 64 ? i >= KT / 64 : hi != 0) over = e > kRoom;
+        *reinterpret_cast<float*>(at) = power_of_two(e);
+      }
     }
+    const float above = __any(over) ? kRaise : 0.f;
     const auto times = [&](f32x16& x, int first) __attribute__((always_inline)) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -390,7 +404,7 @@ __global__ __launch_bounds__(256, Tile8<DP>::kGroups) void attend_narrow_quantiz
       }
       if (__any(seen[b] != ~0u)) rb.mask_scores(s[b], seen[b]);
     }
-    rb.weigh(s, c);
+    rb.template weigh<true>(s, c, above);
     typename Block::Weights weights[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -551,8 +565,14 @@ template <typename Elem, typename F, int DP, int KT> struct Staging {
     int id[kWaves][64], exponent[kWaves][64];
     float scale[kWaves][2][kFactors ? 1 : 64];
     float factors[kFactorRing][kFactors ? 3 * KT : 1];
-    __attribute__((aligned(8))) uint8_t valid[kValidRing][kWaves];
+    // of a stage, of each wave's rows: which are keys, and whether an exponent of their
+    // values is over kRoom (read together, as 32-bit words)
+    struct About {
+      uint8_t valid[kWaves], over[kFactors ? 0 : kWaves];
+    };
+    __attribute__((aligned(16))) About about[kValidRing];
   };
+  static constexpr int kWords = kWaves / 4;
   Shared* sh;
   int wave, lane;
   int64_t k0;
@@ -586,7 +606,7 @@ template <typename Elem, typename F, int DP, int KT> struct Staging {
     byte_to_lds(ok ? reinterpret_cast<const char*>(e.at((uint32_t)id, p.block.div((uint32_t)a.place))) : none,
                 (uint32_t)(uintptr_t)sh->exponent[wave]);
     const uint64_t all = __ballot(ok);
-    if ((lane & 15) == 0) sh->valid[(four * 4 + (lane >> 4)) % kValidRing][wave] = (uint8_t)(all >> lane);
+    if ((lane & 15) == 0) sh->about[(four * 4 + (lane >> 4)) % kValidRing].valid[wave] = (uint8_t)(all >> lane);
   }
   template <int NEWER> __device__ __forceinline__ void settle(int four, float c) {
     wait_loads<NEWER>();
@@ -604,7 +624,22 @@ template <typename Elem, typename F, int DP, int KT> struct Staging {
       }
     } else {
       sh->scale[wave][four & 1][lane] = power_of_two(e);
+      const uint64_t over = __ballot(e > kRoom) >> (lane & 48);  // (from bit 8 on: the values')
+      if ((lane & 15) == 0) sh->about[(four * 4 + (lane >> 4)) % kValidRing].over[wave] = (uint8_t)(over >> 8);
     }
+  }
+  // Which rows of stage t are keys, and how far m is to stay above their scores.
+  __device__ __forceinline__ float read_about(int t, uint32_t (&valid)[kWords]) const {
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(&sh->about[t % kValidRing]);
+    uint32_t over = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      valid[i] = at[i];
+      if constexpr (!kFactors) over |= at[kWords + i];
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) valid[i] = __builtin_amdgcn_readfirstlane(valid[i]);
+    return over ? kRaise : 0.f;
   }
   // Row and piece of the lane's i-th 16 bytes among the wave's 8 rows of K and 8 of V.
   struct Mine {
@@ -721,13 +756,12 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
   };
   auto soften = [&](int t, auto tail) __attribute__((always_inline)) {
     if (idle) return;
-    const uint64_t at_all = *reinterpret_cast<const uint64_t*>(s_stage.valid[t % kValidRing]);
-    const uint64_t all = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at_all >> 32)) << 32) |
-                         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at_all);
+    uint32_t all[Stage::kWords];
+    const float above = stage.read_about(t, all);
     bool uneven = false;
 #pragma unroll
     for (int b = 0; b < NS; ++b) {
-      const uint32_t valid = (uint32_t)(all >> (32 * (part + b)));
+      const uint32_t valid = all[part + b];
       seen[b] = valid;
       if constexpr (decltype(tail)::value) {
         seen[b] &= rb.sees(p, w, (int)first_key(t) + (part + b) * kBlock);
@@ -739,7 +773,7 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
       const uint32_t at = (uint32_t)(uintptr_t)s_stage.factors[t % kFactorRing] + 4 * part * kBlock;
       rb.weigh_scaled(s, seen, at, at + 4 * KT, at + 8 * KT);
     } else {
-      rb.weigh(s, c);
+      rb.template weigh<true>(s, c, above);
     }
 #pragma unroll
     for (int b = 0; b < NS; ++b) weights[b] = rb.pack(s[b]);
@@ -885,16 +919,15 @@ __global__ __launch_bounds__(kThreads, 1) void attend_wide_quantized_kernel(Atte
     }
     if (!idle) {
       f32x16 s[1] = {rb.template scores<0>()};
-      const uint32_t valid =
-          __builtin_amdgcn_readfirstlane(*reinterpret_cast<const uint32_t*>(s_stage.valid[t % kValidRing]));
-      uint32_t seen[1] = {valid};
+      uint32_t seen[1];
+      const float above = stage.read_about(t, seen);
       if constexpr (kTail) seen[0] &= rb.sees(p, w, (int)first_key(t));
       if constexpr (Stage::kFactors) {
         const uint32_t at = (uint32_t)(uintptr_t)s_stage.factors[t % kFactorRing];
         rb.weigh_scaled(s, seen, at, at + 4 * KT, at + 8 * KT);
       } else {
         if (__any(seen[0] != ~0u)) rb.mask_scores(s[0], seen[0]);
-        rb.weigh(s, c);
+        rb.template weigh<true>(s, c, above);
       }
       const char* vb = place(t) + kTile;
       // One form of the products a loop: choosing between two by what a tile holds, as the

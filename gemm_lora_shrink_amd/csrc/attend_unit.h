@@ -387,8 +387,10 @@ template <typename Elem, int DP, typename Out = Elem, int NT = 1> struct RowBloc
   // Running softmax over NS blocks of scores (-inf where masked): scores become
   // weights.  c > 0 turns scores into powers of two.  m is moved only where a weight
   // would pass 2^kMost, and then below the score by kBelow: most tiles leave the
-  // output as it is, and sums and weights stay clear of overflow.
-  template <int NS> __device__ __forceinline__ void weigh(f32x16 (&s)[NS], float c) {
+  // output as it is, and sums and weights stay clear of overflow.  RAISED: m stays
+  // `above` these scores, so that the weights are at most 2^(kMost - above).
+  template <bool RAISED = false, int NS>
+  __device__ __forceinline__ void weigh(f32x16 (&s)[NS], float c, float above = 0.f) {
     constexpr float kBelow = Mma32<Elem>::kBelow, kMost = Mma32<Elem>::kMost;
     // four chains each for the maximum and the sum: an operation waits twice its
     // own time for the one before it
@@ -399,6 +401,7 @@ template <typename Elem, int DP, typename Out = Elem, int NT = 1> struct RowBloc
       for (int i = b ? 0 : 4; i < 16; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[b][i]);
     float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
     mx = __fmul_rn(half_max(mx), c);
+    if constexpr (RAISED) mx += above;
     if (__any(mx - m > kMost)) {
       float mn = mx - kBelow;
       if (kBelow > 0.f && mx - mn > kMost) mn = mx;  // a score that has no units left

@@ -16,7 +16,7 @@
 
 namespace lora {
 
-constexpr int kValidRing = 16;   // stages whose rows' existence is held
+constexpr int kValidRing = 16;   // stages of which it is held which rows are keys
 constexpr int kFactorRing = 8;   // stages whose factors are held
 constexpr int kTurnsRing = 4;    // stages in LDS, kernel with turns
 constexpr int kTurnsFind = 0, kTurnsSettle = 1, kTurnsAsk = 2;  // of four steps

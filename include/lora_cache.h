@@ -87,7 +87,11 @@ lora_status lora_store_quantized(lora_dtype dt, const void *k, int64_t ldk, cons
  *   dt   of q and out.  Keys and values enter the products as they are held,
  *        exactly.  q is exact too; the softmax weights, times the power of two
  *        of their value's block, are rounded to 8 bits for bf16, 11 at least
- *        for fp16 and 24 for fp32.
+ *        for fp16 and 24 for fp32.  fp16 calls of more than 32 rows a key head
+ *        (max_nodes times the q_heads / kv_heads heads that share it) round such
+ *        a product to 11 bits down to 2^-26 of the row's largest one, to steps of
+ *        2^-36 of that below.  Sums hold every value: an output is infinite only
+ *        where it is beyond its type.
  */
 size_t lora_quantized_workspace_bytes(int32_t B, int32_t T, int32_t max_nodes, int32_t max_context, int32_t q_heads,
                                       int32_t kv_heads, int32_t d);
