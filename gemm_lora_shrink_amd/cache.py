@@ -232,8 +232,8 @@ def tree_attention_quantized(q, cache, page_table, context, q_start, *, max_node
 
 def keep_path_quantized(caches, page_table, context, path, n_kept, *, stream=None):
     """keep_path over the layers' quantized caches, alike in shapes, strides and
-    type (a list of them, any number, none of them twice).  A row that moves into a block of a
-    larger exponent is rounded again."""
+    type (a list of them, any number; no tensor twice, exponents neither).  A row that
+    moves into a block of a larger exponent is rounded again."""
     n = len(caches)
     if n < 1:
         raise _bad("need one cache at least")
@@ -251,8 +251,8 @@ def keep_path_quantized(caches, page_table, context, path, n_kept, *, stream=Non
                     not x.is_contiguous() if dense else x.stride() != stride):
                 raise _bad("the layers' caches must be alike in shape, strides, type and GPU")
         at.append([x.data_ptr() for x in t])
-    if len({*at[0], *at[1]}) != 2 * n:
-        raise _bad("a cache is listed twice")  # its rows would move twice at once
+    if len(set().union(*at)) != 4 * n:
+        raise _bad("a cache, or exponents, are listed twice")  # rows would move, or be rounded, twice at once
     B = _i32(context.numel(), "the number of sequences")
     table = _int_rows(page_table, "page_table", dev, B)
     steps = _int_rows(path, "path", dev, B)

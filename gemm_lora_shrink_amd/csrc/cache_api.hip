@@ -57,6 +57,21 @@ lora_status check_pointers(const void* k, const void* v, const int8_t* k_exp, co
   return LORA_OK;
 }
 
+// Whether some address comes twice among n of each list (n <= LORA_MAX_KEEP_LAYERS).
+bool any_twice(const void* const* const (&lists)[4], int n) {
+  constexpr uint32_t kSlots = 8 * LORA_MAX_KEEP_LAYERS;  // half of them stay empty
+  static_assert((kSlots & (kSlots - 1)) == 0, "");
+  const void* seen[kSlots] = {};
+  for (const void* const* list : lists)
+    for (int i = 0; i < n; ++i) {
+      uint32_t at = (uint32_t)((reinterpret_cast<uintptr_t>(list[i]) * 0x9e3779b97f4a7c15ull) >> 40);
+      for (; seen[at % kSlots]; ++at)
+        if (seen[at % kSlots] == list[i]) return true;
+      seen[at % kSlots] = list[i];
+    }
+  return false;
+}
+
 QuantizedView view_of(const lora_quantized_cache& c) {
   return QuantizedView{c.k,      c.v,          c.k_exp,      c.v_exp,      c.k_page,
                        c.k_head, c.k_row,      c.v_page,     c.v_head,     c.v_row,
@@ -310,6 +325,8 @@ LORA_EXPORT lora_status lora_keep_path_quantized(const lora_quantized_cache* cac
     return fail(LORA_ERR_INVALID_ARG, "k, v, k_exp, v_exp, context, path or n_kept is null");
   for (int i = 0; i < n_layers; ++i)
     if ((st = check_pointers(k[i], v[i], k_exp[i], v_exp[i])) != LORA_OK) return st;
+  if (any_twice({k, v, reinterpret_cast<const void* const*>(k_exp), reinterpret_cast<const void* const*>(v_exp)}, n_layers))
+    return fail(LORA_ERR_INVALID_ARG, "an address is listed twice: its rows would move twice at once");
   KeepQuantizedParams p{};
   p.page_table = page_table;
   p.context = context;

@@ -113,7 +113,7 @@ lora_status lora_tree_attention_quantized(lora_dtype dt, const void *q, int64_t 
  * afterwards.
  *   cache                  [host] strides and sizes of every layer; its pointers
  *                          are not read
- *   k, v, k_exp, v_exp     [host] n_layers pointers each, none of them twice
+ *   k, v, k_exp, v_exp     [host] n_layers pointers each, no address twice in all (checked)
  */
 lora_status lora_keep_path_quantized(const lora_quantized_cache *cache, void *const *k, void *const *v,
                                      int8_t *const *k_exp, int8_t *const *v_exp, int32_t n_layers, int32_t kv_heads,

@@ -1,0 +1,54 @@
+"""Arguments of the quantized cache's and the pages' calls at their edges: what
+must be refused on the host, and what looks odd but is a call like any other."""
+
+import numpy as np
+import pytest
+import torch
+
+import gemm_lora_shrink_amd as glsa
+from gemm_lora_shrink_amd import cache as C
+from test_cache_abi import BAD, FAKE, _keep
+
+DEVICES = pytest.mark.gpu
+
+
+def ints(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device="cuda")
+
+
+def raw(tensors):
+    return [t.clone().view(torch.uint8) for t in tensors]
+
+
+@pytest.mark.parametrize("layers", [2, 128])
+def test_keep_refuses_an_address_that_comes_twice(layers):
+    """Keys, values or exponents of two layers, or of one, at one address: nothing is enqueued."""
+    names = ("k", "v", "ke", "ve")
+    pack = C.struct.Struct(f"@{layers}P").pack
+
+    def lists():
+        return {n: [FAKE + (i * layers + j) * 4096 for j in range(layers)] for i, n in enumerate(names)}
+
+    for a, i, b, j in (("k", 0, "k", layers - 1), ("v", 1, "v", 0), ("ke", 0, "ke", 1), ("ve", layers - 1, "ve", 0),
+                       ("ke", 0, "ve", 0), ("ke", 1, "ve", layers - 2), ("k", 0, "v", 0), ("k", 1, "ve", 0)):
+        at = lists()
+        at[a][i] = at[b][j]
+        assert _keep(layers=layers, **{n: pack(*x) for n, x in at.items()}) == BAD
+        assert b"twice" in glsa.lib().lora_last_error()
+
+
+@DEVICES
+def test_keep_refuses_exponents_that_come_twice():
+    a, b = ([t.clone() for t in glsa.alloc_quantized_cache(4, 2, 8, 32, "cuda", dtype=torch.int8)] for _ in range(2))
+    for t in a + b:
+        t.copy_(torch.randint(-9, 9, t.shape, device="cuda").to(torch.int8))
+    was = raw(a + b)
+    args = ints([[0, 1], [2, 3]]), ints([7, 3]), ints([[2, 4], [1, 3]]), ints([2, 2])
+    for caches in ([a, [*b[:2], a[2], b[3]]], [a, [*b[:3], a[3]]], [[*a[:3], a[2]]], [a, [*b[:2], a[3], b[3]]]):
+        with pytest.raises(glsa.LoraError, match="twice"):
+            glsa.keep_path_quantized(caches, *args)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(raw(a + b), was))
+    glsa.keep_path_quantized([a, b], *args)
+    torch.cuda.synchronize()
+    assert not all(torch.equal(x, y) for x, y in zip(raw(a + b), was))
