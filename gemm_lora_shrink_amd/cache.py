@@ -251,7 +251,7 @@ def keep_path_quantized(caches, page_table, context, path, n_kept, *, stream=Non
                     not x.is_contiguous() if dense else x.stride() != stride):
                 raise _bad("the layers' caches must be alike in shape, strides, type and GPU")
         at.append([x.data_ptr() for x in t])
-    if len(set().union(*at)) != 4 * n:
+    if shape[0] and len(set().union(*at)) != 4 * n:
         raise _bad("a cache, or exponents, are listed twice")  # rows would move, or be rounded, twice at once
     B = _i32(context.numel(), "the number of sequences")
     table = _int_rows(page_table, "page_table", dev, B)

@@ -191,11 +191,12 @@ LORA_EXPORT lora_status lora_store_quantized(lora_dtype dt, const void* k, int64
     return fail(LORA_ERR_UNSUPPORTED, "the cache has more rows than cache_rows can name");
   if (!store_quantized_fits(T)) return fail(LORA_ERR_UNSUPPORTED, "T = %d tokens are more than a launch holds", T);
   if (T == 0) return LORA_OK;
-  if ((st = check_pointers(cache->k, cache->v, cache->k_exp, cache->v_exp)) != LORA_OK) return st;
+  if (cache->n_pages > 0 && (st = check_pointers(cache->k, cache->v, cache->k_exp, cache->v_exp)) != LORA_OK) return st;
   const int64_t width = (int64_t)kv_heads * d;
   if ((st = check_rows(dt, "k", k, ldk, width)) != LORA_OK) return st;
   if ((st = check_rows(dt, "v", v, ldv, width)) != LORA_OK) return st;
   if (!cache_rows) return fail(LORA_ERR_INVALID_ARG, "cache_rows is null");
+  if (cache->n_pages == 0) return LORA_OK;
   StoreParams p{};
   p.k = k;
   p.v = v;
@@ -243,7 +244,7 @@ LORA_EXPORT lora_status lora_tree_attention_quantized(lora_dtype dt, const void*
   if ((st = check_format(*cache)) != LORA_OK) return st;
   if (T == 0 || B == 0) return LORA_OK;
   if (!context || !q_start) return fail(LORA_ERR_INVALID_ARG, "context or q_start is null");
-  if ((st = check_pointers(cache->k, cache->v, cache->k_exp, cache->v_exp)) != LORA_OK) return st;
+  if (cache->n_pages > 0 && (st = check_pointers(cache->k, cache->v, cache->k_exp, cache->v_exp)) != LORA_OK) return st;
   const int64_t most = ((int64_t)1 << 32) - 1;
   if (cache->k_page > most || cache->v_page > most || cache->k_row > most || cache->v_row > most ||
       cache->k_exp_page > most || cache->v_exp_page > most)
@@ -323,6 +324,7 @@ LORA_EXPORT lora_status lora_keep_path_quantized(const lora_quantized_cache* cac
   if (B == 0 || n_layers == 0 || n_path == 0) return LORA_OK;
   if (!k || !v || !k_exp || !v_exp || !context || !path || !n_kept)
     return fail(LORA_ERR_INVALID_ARG, "k, v, k_exp, v_exp, context, path or n_kept is null");
+  if (cache->n_pages == 0) return LORA_OK;
   for (int i = 0; i < n_layers; ++i)
     if ((st = check_pointers(k[i], v[i], k_exp[i], v_exp[i])) != LORA_OK) return st;
   if (any_twice({k, v, reinterpret_cast<const void* const*>(k_exp), reinterpret_cast<const void* const*>(v_exp)}, n_layers))

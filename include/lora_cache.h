@@ -47,7 +47,9 @@ typedef LORA_ENUM { LORA_CACHE_E4M3 = 0, LORA_CACHE_INT8 = 1 } lora_cache_format
  * grid, and so is the conversion to the 16-bit operands of the products.
  *   k, v           as in lora_kv_cache, one byte an element; strides in bytes,
  *                  multiples of 16 (as head_dim then is)
- *   k_exp, v_exp   [page][head][block] int8, unit stride over the blocks of a page */
+ *   k_exp, v_exp   [page][head][block] int8, unit stride over the blocks of a page
+ * With n_pages = 0 none of the pointers is read: nothing is placed or moved, and no
+ * sequence has keys. */
 typedef struct {
   void *k, *v;
   int8_t *k_exp, *v_exp;

@@ -52,3 +52,21 @@ def test_keep_refuses_exponents_that_come_twice():
     glsa.keep_path_quantized([a, b], *args)
     torch.cuda.synchronize()
     assert not all(torch.equal(x, y) for x, y in zip(raw(a + b), was))
+
+
+@DEVICES
+@pytest.mark.parametrize("fmt", [torch.float8_e4m3fn, torch.int8])
+def test_caches_of_no_pages(fmt):
+    """Nothing is placed, nothing moves, and rows see no key: outputs of 0."""
+    caches = [glsa.alloc_quantized_cache(0, 2, 16, 64, "cuda", dtype=fmt, block=8) for _ in range(3)]
+    table, context = ints([[-1, -1, -1], [0, 5, -1]]), ints([7, 20])
+    x = torch.randn(4, 8 * 64, device="cuda").bfloat16()
+    glsa.store_quantized(x[:, :128], x[:, 128:256], caches[0], ints([0, 5, -1, 40]))
+    glsa.keep_path_quantized(caches, table, context, ints([[0, 2], [1, 2]]), ints([2, 1]))
+    lse = torch.zeros(4, 8, device="cuda")
+    for nodes, counts in ((3, [3, 1]), (20, [1, 3])):  # one block of rows, and more
+        out = torch.full_like(x, 5)
+        ws = glsa.alloc_quantized_workspace(2, 4, nodes, 48, 8, 2, 64, "cuda")
+        glsa.tree_attention_quantized(x, caches[0], table, context, ints(np.cumsum([0] + counts)), max_nodes=nodes,
+                                      max_context=48, out=out, lse=lse, workspace=ws)
+        assert not out.any() and bool((lse == -float("inf")).all())
