@@ -79,9 +79,9 @@ QuantizedView view_of(const lora_quantized_cache& c) {
                        fast_div((uint32_t)c.page_size), fast_div((uint32_t)c.block)};
 }
 
-lora_status check_table(const int32_t* page_table, int64_t ld_table, int32_t n_table) {
+lora_status check_table(const int32_t* page_table, int64_t ld_table, int32_t n_table, int32_t B) {
   if (n_table < 0) return fail(LORA_ERR_INVALID_ARG, "n_table = %d is negative", n_table);
-  if (n_table > 0 && !page_table) return fail(LORA_ERR_INVALID_ARG, "page_table is null");
+  if (B > 0 && n_table > 0 && !page_table) return fail(LORA_ERR_INVALID_ARG, "page_table is null");
   if (ld_table < n_table) return fail(LORA_ERR_INVALID_ARG, "ld_table is smaller than n_table");
   return LORA_OK;
 }
@@ -117,7 +117,7 @@ lora_status check_pool(const int32_t* refs, int64_t n_pages, const int32_t* tabl
   if (n_pages > 0 && !refs) return fail(LORA_ERR_INVALID_ARG, "refs is null");
   lora_status st = check_sequences(B);
   if (st != LORA_OK) return st;
-  return B > 0 ? check_table(table, ld_table, n_table) : LORA_OK;
+  return B > 0 ? check_table(table, ld_table, n_table, B) : LORA_OK;
 }
 
 lora_status check_workspace(const void* workspace, size_t bytes, int64_t n_pages, int32_t n_seqs) {
@@ -239,7 +239,7 @@ LORA_EXPORT lora_status lora_tree_attention_quantized(lora_dtype dt, const void*
       return fail(LORA_ERR_INVALID_ARG, "mask_words = %d is too small for %d nodes", mask_words, max_nodes);
     if (reinterpret_cast<uintptr_t>(mask) & 7u) return fail(LORA_ERR_UNSUPPORTED, "mask must be 8-byte aligned");
   }
-  if ((st = check_table(page_table, ld_table, n_table)) != LORA_OK) return st;
+  if ((st = check_table(page_table, ld_table, n_table, B)) != LORA_OK) return st;
   if (!cache) return fail(LORA_ERR_INVALID_ARG, "cache is null");
   if ((st = check_format(*cache)) != LORA_OK) return st;
   if (T == 0 || B == 0) return LORA_OK;
@@ -318,7 +318,7 @@ LORA_EXPORT lora_status lora_keep_path_quantized(const lora_quantized_cache* cac
   if (n_path > LORA_MAX_KEEP_PATH)
     return fail(LORA_ERR_UNSUPPORTED, "n_path = %d exceeds %d", n_path, LORA_MAX_KEEP_PATH);
   if (ld_path < n_path) return fail(LORA_ERR_INVALID_ARG, "ld_path is smaller than n_path");
-  if ((st = check_table(page_table, ld_table, n_table)) != LORA_OK) return st;
+  if ((st = check_table(page_table, ld_table, n_table, B)) != LORA_OK) return st;
   if (!cache) return fail(LORA_ERR_INVALID_ARG, "cache is null");
   if ((st = check_format(*cache)) != LORA_OK) return st;
   if (B == 0 || n_layers == 0 || n_path == 0) return LORA_OK;
@@ -389,7 +389,7 @@ LORA_EXPORT lora_status lora_fork_sequences(int32_t* refs, int64_t n_pages, cons
   lora_status st = check_pool(refs, n_pages, to_table, ld_to, n_table, B_to);
   if (st != LORA_OK) return st;
   if ((st = check_sequences(B_from)) != LORA_OK) return st;
-  if (B_from > 0 && (st = check_table(from_table, ld_from, n_table)) != LORA_OK) return st;
+  if (B_from > 0 && (st = check_table(from_table, ld_from, n_table, B_from)) != LORA_OK) return st;
   if (n_forks < 0) return fail(LORA_ERR_INVALID_ARG, "n_forks = %d is negative", n_forks);
   if (n_forks > 65535) return fail(LORA_ERR_UNSUPPORTED, "n_forks = %d exceeds 65535", n_forks);
   if (page_size < 1) return fail(LORA_ERR_INVALID_ARG, "page_size = %d must be >= 1", page_size);

@@ -7,7 +7,7 @@ import torch
 
 import gemm_lora_shrink_amd as glsa
 from gemm_lora_shrink_amd import cache as C
-from test_cache_abi import BAD, FAKE, _keep
+from test_cache_abi import BAD, FAKE, OK, _attend, _keep
 
 DEVICES = pytest.mark.gpu
 
@@ -70,3 +70,22 @@ def test_caches_of_no_pages(fmt):
         glsa.tree_attention_quantized(x, caches[0], table, context, ints(np.cumsum([0] + counts)), max_nodes=nodes,
                                       max_context=48, out=out, lse=lse, workspace=ws)
         assert not out.any() and bool((lse == -float("inf")).all())
+
+
+def test_no_sequences_need_no_table():
+    """An empty page table has no address, however many columns."""
+    assert _attend(B=0, table=None, context=None, q_start=None) == OK
+    assert _keep(B=0, table=None, context=None, path=None, kept=None) == OK
+    assert _attend(B=0, table=None, n_table=-1) == BAD and _keep(B=0, table=None, n_table=-1, ld=4) == BAD
+    assert _attend(B=1, table=None) == BAD and _keep(B=1, table=None) == BAD
+
+
+@DEVICES
+def test_calls_of_no_sequences():
+    cache = glsa.alloc_quantized_cache(4, 2, 16, 64, "cuda")
+    table, none = torch.empty(0, 9, dtype=torch.int32, device="cuda"), ints([])
+    x = torch.randn(3, 8 * 64, device="cuda").half()
+    out = torch.full_like(x, 5)
+    glsa.tree_attention_quantized(x, cache, table, none, ints([0]), max_nodes=3, out=out)
+    glsa.keep_path_quantized([cache], table, none, table, none)
+    assert bool((out == 5).all())
