@@ -79,15 +79,14 @@ __device__ __forceinline__ int free_pages(Scan& scan, const int32_t* refs, int64
   return min(found, want);
 }
 
-__device__ inline int clamped(int64_t x, int64_t hi) { return (int)(x < 0 ? 0 : (x > hi ? hi : x)); }
 __device__ inline bool names_page(int entry, int64_t n_pages) { return entry >= 0 && entry < n_pages; }
 
 // ---- reserve ----------------------------------------------------------------
 
 // The workspace of a reservation: [0, B) what each sequence lacks, then where its
 // share of the free pages starts; [B] how many there are; from B + 1 on the pages.
-__device__ inline int wanted_columns(const PoolParams& p, int64_t tokens) {
-  return clamped((int64_t)p.page.div((uint32_t)clamped(tokens + p.page.d - 1, 0x7fffffff)), p.n_table);
+__device__ inline int wanted_columns(const PoolParams& p, int tokens) {
+  return tokens <= 0 ? 0 : min((int)p.page.div((uint32_t)(tokens - 1)) + 1, p.n_table);
 }
 
 __global__ __launch_bounds__(kThreads) void count_missing_kernel(PoolParams p, const int32_t* lengths) {

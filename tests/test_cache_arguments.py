@@ -7,6 +7,7 @@ import torch
 
 import gemm_lora_shrink_amd as glsa
 from gemm_lora_shrink_amd import cache as C
+from oracle import cache_oracle as co
 from test_cache_abi import BAD, FAKE, OK, _attend, _keep
 
 DEVICES = pytest.mark.gpu
@@ -89,3 +90,21 @@ def test_calls_of_no_sequences():
     glsa.tree_attention_quantized(x, cache, table, none, ints([0]), max_nodes=3, out=out)
     glsa.keep_path_quantized([cache], table, none, table, none)
     assert bool((out == 5).all())
+
+
+@DEVICES
+@pytest.mark.parametrize("page", [1, 3, 1 << 29, (1 << 30) + 1, 2 ** 31 - 1])
+def test_lengths_near_2_to_31(page):
+    """Columns are ceil(tokens / page_size) up to the largest lengths and pages."""
+    top = 2 ** 31 - 1
+    lengths = np.array([top, top - 1, 1 << 30, (1 << 30) + 1, page, min(page, top - 1) + 1, page - 1, 0, -5, -top - 1], np.int64)
+    B, n = len(lengths), 60
+    refs, table, missing = np.zeros(n, np.int64), np.full((B, 5), -1), ints([0])
+    got_refs, got = ints(refs), ints(table)
+    lacking = co.reserve(refs, table, lengths, page)
+    glsa.reserve_pages(got_refs, got, ints(lengths), page_size=page, missing=missing)
+    assert np.array_equal(got.cpu().numpy(), table) and np.array_equal(got_refs.cpu().numpy(), refs) and int(missing) == lacking == 0
+    keep = lengths[[3, 5, 0, 2, 6, 1, 4, 8, 9, 7]]
+    co.release(refs, table, range(B), keep, page)
+    glsa.release_pages(got_refs, got, keep=ints(keep), page_size=page)
+    assert np.array_equal(got.cpu().numpy(), table) and np.array_equal(got_refs.cpu().numpy(), refs)
