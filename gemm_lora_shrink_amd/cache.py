@@ -288,12 +288,17 @@ def _runs(t):
     return joined[0], joined[1], run
 
 
+def _listed(tensors):
+    """A tuple of tensors, or of the one that is given."""
+    return (tensors,) if isinstance(tensors, torch.Tensor) else tuple(tensors)
+
+
 class PagedTensors:
     """Tensors whose first dimension is the pages of one pool (the layers' k, v and
     exponents), laid out once for copy_pages, fork_sequences and compact_pages."""
 
     def __init__(self, tensors):
-        self.tensors = tuple(tensors)
+        self.tensors = _listed(tensors)
         if not self.tensors:
             raise _bad("need one tensor at least")
         self.dev = _gpu(self.tensors[0], "a paged tensor")
@@ -323,7 +328,7 @@ def _paged(tensors):
 def _of_pool(tensors, n_pages, dev):
     """(the C view, the number) of a pool's tensors, of which there may be none."""
     if not isinstance(tensors, PagedTensors):
-        tensors = tuple(tensors)
+        tensors = _listed(tensors)
         if not tensors:
             return None, 0
         tensors = PagedTensors(tensors)

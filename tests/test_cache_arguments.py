@@ -108,3 +108,28 @@ def test_lengths_near_2_to_31(page):
     co.release(refs, table, range(B), keep, page)
     glsa.release_pages(got_refs, got, keep=ints(keep), page_size=page)
     assert np.array_equal(got.cpu().numpy(), table) and np.array_equal(got_refs.cpu().numpy(), refs)
+
+
+def test_one_tensor_is_a_list_of_it():
+    """Not a list of its pages, which would be copied as if their heads were pages."""
+    x = torch.zeros(4, 4, 8)
+    for listed in (C._listed(x), C._listed([x]), C._listed((x,))):
+        assert len(listed) == 1 and listed[0] is x
+    assert C._listed(()) == () and len(C._listed(glsa.alloc_quantized_cache(2, 1, 4, 16, "cpu"))) == 4
+
+
+@DEVICES
+def test_pages_of_one_tensor():
+    x = torch.arange(4 * 4 * 8, device="cuda").view(4, 4, 8).float()
+    want = x.clone()
+    want[3] = want[1]
+    glsa.copy_pages(x, ints([1]), ints([3]))
+    assert torch.equal(x, want)
+    refs, table = ints([0, 0, 0, 1]), ints([[3]])
+    assert int(glsa.compact_pages(refs, table, tensors=x)) == 1
+    want[0] = want[3]
+    assert torch.equal(x, want) and table.tolist() == [[0]]
+    to = ints([[7]])
+    glsa.fork_sequences(refs, table, ints([0]), ints([0]), ints([3]), page_size=4, tensors=x, out_table=to)
+    want[1] = want[0]
+    assert torch.equal(x, want) and to.tolist() == [[1]]
