@@ -222,6 +222,9 @@ template <int ROWS, bool SPREAD, int KEYS> __device__ __forceinline__ Work quant
 // (1.1 GB): 197 us, 5.5 TB/s; 64 sequences of 4096 (0.54 GB): 92 us, 5.9 TB/s.  Two
 // workgroups a compute unit, one of which is at its first loads while the other
 // reads (260 us on the first with one of twice the tiles, 300 with one of these).
+// e4m3 has two forms of the products with the values, of which a tile takes one.  With
+// heads of 128 and an fp16 or fp32 query, and with heads of 256, 30 to 190 registers
+// then lie in memory; INT8 has one form, and none but with fp32 (4 and 62).
 template <typename Out, typename F, int DP>
 __global__ __launch_bounds__(256, Tile8<DP>::kGroups) void attend_narrow_quantized_kernel(AttendQuantizedParams p) {
   using L8 = Tile8<DP>;
@@ -694,6 +697,7 @@ template <typename Elem, typename F, int DP, int KT> struct Staging {
 // other at the barriers; a workgroup's start, first stages and output are some 18 us.
 // 64 nodes over 32768 keys, 32 + 8 bf16 heads of 128, e4m3: 61 us and the join 8, 34
 // GFLOP; 16 sequences of 256 to 8192 keys and 23 to 45 nodes, fp16, INT8: 139 and 11.
+// With e4m3, heads of 128 and more than 128 rows 4 registers (fp16: 12) lie in memory.
 template <typename Out, typename F, int DP, int KG>
 __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQuantizedParams p) {
   using Elem = typename Tiles<Out>::Elem;
@@ -867,8 +871,8 @@ __global__ __launch_bounds__(512, 2) void attend_turns_quantized_kernel(AttendQu
 // The heads that leave the kernel above no registers: four waves of 32 rows share
 // stages of 32 keys, double buffered.  A stage's bytes are in registers during the
 // stage before it and converted into the other place at its end.  4 sequences of 8192
-// keys and 32 nodes, 16 + 4 bf16 heads of 256, e4m3: 84 us;
-// the output and the query fill the registers, fp32 ones spill 84 (INT8) to 114.
+// keys and 32 nodes, 16 + 4 bf16 heads of 256, e4m3: 82 us; the output and the query
+// fill the registers, with fp32 ones 90 (INT8) to 114 lie in memory.
 template <typename Out, typename F, int DP>
 __global__ __launch_bounds__(kThreads, 1) void attend_wide_quantized_kernel(AttendQuantizedParams p) {
   using Elem = typename Tiles<Out>::Elem;
@@ -991,9 +995,12 @@ Plan plan_kind(bool fp32, int32_t nodes, int32_t group, int32_t d) {
 // How the keys are cut: by their lengths where a lane can count for each sequence,
 // else into even chunks, so long that about `groups` workgroups run in all where
 // every sequence is as long as its bound; no shorter than kMinChunk.  groups: as many
-// as the chip holds at once (the wide kernel: two a compute unit).  More cost their
-// first loads and parts: 64 sequences of 4096 keys, 32 + 8 bf16 heads of 128, 92 us
-// with 512 workgroups, 99 with 1024, 104 with 2048; one of 32768: 27, 31 and 37.
+// as the chip holds at once.  More cost their first loads and parts: 64 sequences of
+// 4096 keys, 32 + 8 bf16 heads of 128, 92 us with 512 workgroups, 99 with 1024, 104
+// with 2048; one of 32768: 27, 31 and 37.  The wide kernel is given twice as many as
+// its registers leave room for (one a compute unit), and that costs it too: 4
+// sequences of 8192 keys and 32 nodes, 16 + 4 bf16 heads of 256, take 82 us with 512
+// and 66 with 256; 16 unlike ones of up to 8192 keys and 45 nodes 182 and 165.
 constexpr int64_t kMaxChunk = (int64_t)1 << 30;
 
 // The most chunks of a sequence; even: if all are as long.  Where others may be short

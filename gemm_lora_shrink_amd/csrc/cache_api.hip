@@ -3,6 +3,8 @@
 // runs before anything is enqueued.
 #include <math.h>
 
+#include <algorithm>
+
 #include "cache.h"
 
 #define LORA_EXPORT extern "C" __attribute__((visibility("default")))
@@ -59,15 +61,17 @@ lora_status check_pointers(const void* k, const void* v, const int8_t* k_exp, co
 
 // Whether some address comes twice among n of each list (n <= LORA_MAX_KEEP_LAYERS).
 bool any_twice(const void* const* const (&lists)[4], int n) {
-  constexpr uint32_t kSlots = 8 * LORA_MAX_KEEP_LAYERS;  // half of them stay empty
-  static_assert((kSlots & (kSlots - 1)) == 0, "");
-  const void* seen[kSlots] = {};
+  const void* seen[8 * LORA_MAX_KEEP_LAYERS];
+  uint32_t slots = 8;  // a power of two of which half stay empty
+  while (slots < 8 * (uint32_t)n) slots *= 2;
+  static_assert((LORA_MAX_KEEP_LAYERS & (LORA_MAX_KEEP_LAYERS - 1)) == 0, "");
+  std::fill_n(seen, slots, nullptr);
   for (const void* const* list : lists)
     for (int i = 0; i < n; ++i) {
       uint32_t at = (uint32_t)((reinterpret_cast<uintptr_t>(list[i]) * 0x9e3779b97f4a7c15ull) >> 40);
-      for (; seen[at % kSlots]; ++at)
-        if (seen[at % kSlots] == list[i]) return true;
-      seen[at % kSlots] = list[i];
+      for (; seen[at % slots]; ++at)
+        if (seen[at % slots] == list[i]) return true;
+      seen[at % slots] = list[i];
     }
   return false;
 }

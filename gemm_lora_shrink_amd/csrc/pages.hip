@@ -484,7 +484,8 @@ hipError_t launch_move(const MoveParams& p, hipStream_t stream) {
   // some 16 workgroups a compute unit in all
   const dim3 grid((unsigned)std::min<int64_t>(most, std::max(4096 / rows, 64)), (unsigned)rows);
   // More than the last-level cache (256 MB) holds goes past the caches: 187 us for 196 to
-  // 205 for 0.83 GB, where 0.13 GB took 41 us for 38.
+  // 205 for 0.83 GB, where 0.13 GB took 41 us for 38.  The host knows the most that may
+  // move, half of a pool, not what does.
   if (bytes > (int64_t)1 << 29) hipLaunchKernelGGL(move_kernel<true>, grid, dim3(kThreads), 0, stream, p);
   else hipLaunchKernelGGL(move_kernel<false>, grid, dim3(kThreads), 0, stream, p);
   return hipGetLastError();
