@@ -112,7 +112,8 @@ lora_status lora_tree_attention_quantized(lora_dtype dt, const void *q, int64_t 
  * largest exponent of the blocks that they come from, and of its own where it
  * has rows of the context; rows are rounded again (to the nearest, ties to
  * even) where their exponent grows.  Rows behind the kept ones hold nothing
- * afterwards.
+ * afterwards.  An exponent that a token raised which is not kept stays where its
+ * block has rows of the context: they have been rounded for it.
  *   cache                  [host] strides and sizes of every layer; its pointers
  *                          are not read
  *   k, v, k_exp, v_exp     [host] n_layers pointers each, no address twice in all (checked)
